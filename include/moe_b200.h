@@ -283,6 +283,55 @@ int moe_forward_fp8(const void* h, const float* Wr, const float* bias, const moe
 int moe_fp8_dequantize(const void* codes, const int8_t* exps, int G, int R, int K, void* out,
                        void* ws, moe_stream_t stream);
 
+/* ---- 8-bit products ----------------------------------------------------
+ * The expert products with both operands in 8 bits: activations in the same
+ * E4M3 + power-of-two-exponent format as the weights, one int8 exponent per
+ * row and 128 columns.  The exponents are the tensor core's own block scales,
+ * so a product is one chain of fp32 accumulation over all of K.
+ * An expert FFN on grouped rows is moe_quantize_fp8 (with perm as the index),
+ * moe_gated_gemm_fp8, moe_quantize_fp8 on its output, moe_grouped_gemm_fp8,
+ * moe_combine.
+ *
+ * Quantisation of rows: codes [R, K] E4M3 and exps [R, ceil(K/128)] int8 of the
+ * bf16 rows x[idx[r]] (x[r] when idx is NULL, which needs R <= src_rows):
+ *   exps[r, b]  = the smallest e in [-117, 120] with
+ *                 max |x[idx[r], 128 b ..]| <= 448 * 2^e; 0 for a block of zeros
+ *   codes[r, c] = E4M3(x[idx[r], c] * 2^-e), rounded to nearest even
+ * x [src_rows, K] bf16, idx [R] int32 (rows may repeat); K a positive multiple
+ * of 16; x, idx and codes 16-byte aligned, exps without an alignment rule.
+ * A NaN or an infinity gets the NaN code 0x7F, counts for no exponent and
+ * raises MOE_ERR_NONFINITE; an index outside [0, src_rows) gives a row of
+ * zeros and raises MOE_ERR_BOUNDS (in the status word of ws; ws may be NULL:
+ * then neither is reported). */
+int moe_quantize_fp8(const void* x, int src_rows, const int32_t* idx, int R, int K, void* codes,
+                     int8_t* exps, void* ws, moe_stream_t stream);
+
+/* Grouped product of quantised rows with FP8 weights:
+ *   y[r, n] = sum_k e4m3(x[r, k]) 2^xe[r, k/128] * e4m3(W[g, n, k]) 2^We[g, n/128, k/128]
+ * for offsets[g] <= r < offsets[g + 1]; rows outside every group keep what y
+ * held.  x [R, K] codes, xe [R, ceil(K/128)], offsets [G + 1] int32
+ * (non-decreasing, within [0, R]; groups may be empty), W [G, N, K] codes, We
+ * [G, ceil(N/128), ceil(K/128)]; y [R, N], fp32 or (y_bf16 != 0) bf16, rounded
+ * once from the fp32 sum.  offsets may be NULL when G = 1: all R rows.
+ * 1 <= G <= 1024, N a positive multiple of 8, K a positive multiple of 16;
+ * R = 0 launches nothing.  Code, offset and output pointers are 16-byte
+ * aligned, exponents have no alignment rule and may be any int8 but -128,
+ * which raises MOE_ERR_BOUNDS like offsets out of order (no row is written
+ * then); ws holds the status word and may be NULL: then nothing is reported.
+ * The summation order depends on the sizes alone, so repeated calls give
+ * identical bits. */
+int moe_grouped_gemm_fp8(const void* x, const int8_t* xe, const int32_t* offsets, const void* W,
+                         const int8_t* We, int G, int R, int N, int K, void* y, int y_bf16,
+                         void* ws, moe_stream_t stream);
+
+/* The gate and up products of quantised rows, fused with the SiLU gate:
+ *   act[r, n] = silu(x[r] . W1[g, n]) * (x[r] . W3[g, n])
+ * rounded once to bf16: act [R, N] bf16, W1 and W3 [G, N, K] codes.  Operands,
+ * limits, groups and errors as moe_grouped_gemm_fp8. */
+int moe_gated_gemm_fp8(const void* x, const int8_t* xe, const int32_t* offsets, const void* W1,
+                       const int8_t* W1e, const void* W3, const int8_t* W3e, int G, int R, int N,
+                       int K, void* act, void* ws, moe_stream_t stream);
+
 /* Row gather, the data movement around the expert-parallel exchange (each
  * rank owns a block of experts; the pages' default multi-GPU layout is expert
  * parallelism, "GLM-5.2" PocketLLM, Implemented execution path):

@@ -91,6 +91,9 @@ def _load() -> ctypes.CDLL:
         "moe_expert_ffn_fp8": (I, [P, P, P, W8, D, P, P, Z, P]),
         "moe_forward_fp8": (I, [P, P, P, W8, D, P, P, P, P, Z, P]),
         "moe_fp8_dequantize": (I, [P, P, I, I, I, P, P, P]),
+        "moe_quantize_fp8": (I, [P, I, P, I, I, P, P, P, P]),
+        "moe_grouped_gemm_fp8": (I, [P, P, P, P, P, I, I, I, I, P, I, P, P]),
+        "moe_gated_gemm_fp8": (I, [P, P, P, P, P, P, P, I, I, I, I, P, P, P]),
         "moe_gather_rows": (I, [P, I, P, I, I, P, P, P]),
         "moe_forward_shared_overlap": (I, [D, I]),
         "moe_pipeline_device_bytes": (Z, [D]),
@@ -252,6 +255,85 @@ def moe_fp8_dequantize(codes, exps, out, ws=None, stream=None) -> None:
     _check(_lib.moe_fp8_dequantize(_code_ptr(codes, "codes"), _ptr(exps, torch.int8, "exps"),
                                    G, R, K, _ptr(out, torch.bfloat16, "out"), wp,
                                    _stream(stream)))
+
+
+def _same_device(first: torch.Tensor, *rest: Optional[torch.Tensor]) -> None:
+    """The kernels run on the current device: every tensor has to live there."""
+    dev = first.get_device()
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"tensors on cuda:{dev}, but the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    for t in rest:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensors on cuda:{dev} and {t.device}: expected one device")
+
+
+def _shape(t: torch.Tensor, want, name: str) -> None:
+    if tuple(t.shape) != tuple(want):
+        raise ValueError(f"{name}: expected shape {tuple(want)}, got {tuple(t.shape)}")
+
+
+def _blocks(n: int) -> int:
+    return (n + 127) // 128
+
+
+def moe_quantize_fp8(x, codes, exps, idx=None, ws=None, stream=None) -> None:
+    """x [src, K] bf16 -> codes [R, K] E4M3 (uint8 or float8_e4m3fn) and exps
+    [R, ceil(K/128)] int8 of the rows x[idx] (idx [R] int32; None: of x itself)."""
+    if x.dim() != 2 or codes.dim() != 2:
+        raise ValueError("x [src, K] and codes [R, K] expected")
+    R, K = codes.shape
+    _shape(codes, (x.shape[0] if idx is None else idx.numel(), x.shape[1]), "codes")
+    _shape(exps, (R, _blocks(K)), "exps")
+    args = (_ptr(x, torch.bfloat16, "x"), x.shape[0], _ptr(idx, torch.int32, "idx"), R, K,
+            _code_ptr(codes, "codes"), _ptr(exps, torch.int8, "exps"), _ws(ws)[0])
+    _same_device(x, codes, exps, idx, ws)
+    _check(_lib.moe_quantize_fp8(*args, _stream(stream)))
+
+
+def _gemm_fp8_args(x, xe, W, We, out, offsets):
+    if x.dim() != 2 or W.dim() not in (2, 3):
+        raise ValueError("x [R, K] and W [G, N, K] (or [N, K]) expected")
+    R, K = x.shape
+    G, N = (1, W.shape[0]) if W.dim() == 2 else W.shape[:2]
+    _shape(xe, (R, _blocks(K)), "xe")
+    _shape(out, (R, N), "output")
+    if offsets is not None:
+        _shape(offsets, (G + 1,), "offsets")
+    return G, R, N, K
+
+
+def _weight_fp8(W, We, G: int, N: int, K: int, name: str):
+    _shape(W, (N, K) if W.dim() == 2 and G == 1 else (G, N, K), name)
+    _shape(We, (_blocks(N), _blocks(K)) if We.dim() == 2 and G == 1 else
+           (G, _blocks(N), _blocks(K)), name + "e")
+    return _code_ptr(W, name), _ptr(We, torch.int8, name + "e")
+
+
+def moe_grouped_gemm_fp8(x, xe, W, We, y, offsets=None, ws=None, stream=None) -> None:
+    """x [R, K] codes with exponents xe [R, ceil(K/128)], W [G, N, K] codes with
+    We [G, ceil(N/128), ceil(K/128)] -> y [R, N] fp32 or bf16 (its dtype chooses);
+    offsets [G + 1] int32 (None: one group of all rows)."""
+    G, R, N, K = _gemm_fp8_args(x, xe, W, We, y, offsets)
+    if y.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"y: expected float32 or bfloat16, got {y.dtype}")
+    w, we = _weight_fp8(W, We, G, N, K, "W")
+    args = (_code_ptr(x, "x"), _ptr(xe, torch.int8, "xe"), _ptr(offsets, torch.int32, "offsets"), w,
+            we, G, R, N, K, _ptr(y, None, "y"), int(y.dtype == torch.bfloat16), _ws(ws)[0])
+    _same_device(x, xe, W, We, y, offsets, ws)
+    _check(_lib.moe_grouped_gemm_fp8(*args, _stream(stream)))
+
+
+def moe_gated_gemm_fp8(x, xe, W1, W1e, W3, W3e, act, offsets=None, ws=None, stream=None) -> None:
+    """silu(x W1^T) * (x W3^T) per group -> act [R, N] bf16; operands as
+    moe_grouped_gemm_fp8, W3 and W3e shaped like W1 and W1e."""
+    G, R, N, K = _gemm_fp8_args(x, xe, W1, W1e, act, offsets)
+    w1, w1e = _weight_fp8(W1, W1e, G, N, K, "W1")
+    w3, w3e = _weight_fp8(W3, W3e, G, N, K, "W3")
+    args = (_code_ptr(x, "x"), _ptr(xe, torch.int8, "xe"), _ptr(offsets, torch.int32, "offsets"), w1,
+            w1e, w3, w3e, G, R, N, K, _ptr(act, torch.bfloat16, "act"), _ws(ws)[0])
+    _same_device(x, xe, W1, W1e, W3, W3e, act, offsets, ws)
+    _check(_lib.moe_gated_gemm_fp8(*args, _stream(stream)))
 
 
 def moe_gather_rows(src, idx, dst, ws=None, stream=None) -> None:

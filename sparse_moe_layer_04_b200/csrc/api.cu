@@ -504,6 +504,53 @@ int forward_impl(const void* h, const float* Wr, const float* bias, const Expert
   return MOE_OK;
 }
 
+// The arguments both 8-bit products share; fills `a` (but for the output type
+// and W3).
+int check_gemm_fp8(const void* x, const int8_t* xe, const int32_t* offsets, const void* W,
+                   const int8_t* We, const char* wname, int G, int R, int N, int K, void* y,
+                   void* ws, Gemm8Args* a) {
+  if (G < 1 || G > 1024) return fail(MOE_ERR_INVALID_ARG, "G = %d outside [1, 1024]", G);
+  if (R < 0) return fail(MOE_ERR_INVALID_ARG, "R = %d < 0", R);
+  if (N < 8 || N % 8) return fail(MOE_ERR_INVALID_ARG, "N = %d not a positive multiple of 8", N);
+  if (K < 16 || K % 16) return fail(MOE_ERR_INVALID_ARG, "K = %d not a positive multiple of 16", K);
+  if ((long long)G * N >= (1ll << 31)) return fail(MOE_ERR_UNSUPPORTED, "G*N >= 2^31");
+  // tiles are numbered with 32 bits: R / 32 + G row blocks times N / 64 columns
+  if (((long long)R / 32 + G + 1) * (N / 64 + 1) >= (1ll << 31))
+    return fail(MOE_ERR_UNSUPPORTED, "R x N is too large for one call");
+  if (G > 1 && !offsets) return fail(MOE_ERR_INVALID_ARG, "offsets is NULL with G > 1");
+  if (R == 0) return MOE_OK;
+  MOE_CHECK_PTR(x);
+  if (!xe) return fail(MOE_ERR_INVALID_ARG, "xe is NULL");
+  if (!W || !aligned16(W))
+    return fail(MOE_ERR_INVALID_ARG, "%s is %s", wname, W ? "not 16-byte aligned" : "NULL");
+  if (!We) return fail(MOE_ERR_INVALID_ARG, "%se is NULL", wname);
+  if (offsets && !aligned16(offsets))
+    return fail(MOE_ERR_INVALID_ARG, "offsets is not 16-byte aligned");
+  MOE_CHECK_PTR(y);
+  if (ws && (reinterpret_cast<uintptr_t>(ws) & 255u))
+    return fail(MOE_ERR_WORKSPACE, "workspace is not 256-byte aligned");
+  a->x = static_cast<const uint8_t*>(x);
+  a->xe = xe;
+  a->offsets = offsets;
+  a->W1 = static_cast<const uint8_t*>(W);
+  a->W1e = We;
+  a->G = G; a->R = R; a->N = N; a->K = K;
+  a->y = y;
+  a->status = static_cast<int*>(ws);
+  return MOE_OK;
+}
+
+int run_gemm_fp8(const Gemm8Args& a, moe_stream_t stream) {
+  if (a.R == 0) return MOE_OK;
+  const int rc = check_device();
+  if (rc) return rc;
+  const char* why = "launch failed";
+  const cudaError_t e = launch_gemm_fp8(a, reinterpret_cast<cudaStream_t>(stream), &why);
+  if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "fp8 product: %s (%s)", why, cudaGetErrorString(e));
+  g_launches = 1;
+  return MOE_OK;
+}
+
 // Device memory of a host-buffer pipeline: two input slots, two output slots
 // and the layer's workspace, each 256-byte aligned.
 struct PipeLayout {
@@ -821,6 +868,61 @@ int moe_fp8_dequantize(const void* codes, const int8_t* exps, int G, int R, int 
   if (e != cudaSuccess) return cuda_fail(e, "dequantize launch");
   g_launches = 1;
   return MOE_OK;
+}
+
+int moe_quantize_fp8(const void* x, int src_rows, const int32_t* idx, int R, int K, void* codes,
+                     int8_t* exps, void* ws, moe_stream_t stream) {
+  g_err.clear();
+  g_launches = 0;
+  if (src_rows < 0 || R < 0) return fail(MOE_ERR_INVALID_ARG, "src_rows and R must be >= 0");
+  if (K < 16 || K % 16) return fail(MOE_ERR_INVALID_ARG, "K = %d is not a positive multiple of 16", K);
+  if (!idx && R > src_rows)
+    return fail(MOE_ERR_INVALID_ARG, "R = %d rows from %d without an index", R, src_rows);
+  if (R == 0) return MOE_OK;
+  MOE_CHECK_PTR(x);
+  MOE_CHECK_PTR(codes);
+  if (!exps) return fail(MOE_ERR_INVALID_ARG, "exps is NULL");
+  if (idx && !aligned16(idx)) return fail(MOE_ERR_INVALID_ARG, "idx is not 16-byte aligned");
+  if (ws && (reinterpret_cast<uintptr_t>(ws) & 255u))
+    return fail(MOE_ERR_WORKSPACE, "workspace is not 256-byte aligned");
+  int rc = check_device();
+  if (rc) return rc;
+  cudaError_t e = launch_quantize_fp8(static_cast<const uint16_t*>(x), src_rows, idx, R, K,
+                                      static_cast<uint8_t*>(codes), exps, static_cast<int*>(ws),
+                                      reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "quantize launch");
+  g_launches = 1;
+  return MOE_OK;
+}
+
+int moe_grouped_gemm_fp8(const void* x, const int8_t* xe, const int32_t* offsets, const void* W,
+                         const int8_t* We, int G, int R, int N, int K, void* y, int y_bf16,
+                         void* ws, moe_stream_t stream) {
+  g_err.clear();
+  g_launches = 0;
+  Gemm8Args a{};
+  const int rc = check_gemm_fp8(x, xe, offsets, W, We, "W", G, R, N, K, y, ws, &a);
+  if (rc) return rc;
+  a.y_bf16 = y_bf16 ? 1 : 0;
+  return run_gemm_fp8(a, stream);
+}
+
+int moe_gated_gemm_fp8(const void* x, const int8_t* xe, const int32_t* offsets, const void* W1,
+                       const int8_t* W1e, const void* W3, const int8_t* W3e, int G, int R, int N,
+                       int K, void* act, void* ws, moe_stream_t stream) {
+  g_err.clear();
+  g_launches = 0;
+  Gemm8Args a{};
+  const int rc = check_gemm_fp8(x, xe, offsets, W1, W1e, "W1", G, R, N, K, act, ws, &a);
+  if (rc) return rc;
+  if (R > 0) {
+    MOE_CHECK_PTR(W3);
+    if (!W3e) return fail(MOE_ERR_INVALID_ARG, "W3e is NULL");
+  }
+  a.W3 = static_cast<const uint8_t*>(W3);
+  a.W3e = W3e;
+  a.y_bf16 = 1;
+  return run_gemm_fp8(a, stream);
 }
 
 int moe_gather_rows(const void* src, int src_rows, const int32_t* idx, int n, int row_bytes,

@@ -1,0 +1,526 @@
+// Grouped products of E4M3 rows with E4M3 weights, one power-of-two exponent
+// per 128 columns of a row and per 128 x 128 block of a weight matrix:
+//
+//   y[r, n]   = sum_k xq[r, k] 2^xe[r, k/128] * wq[g, n, k] 2^we[g, n/128, k/128]
+//   act[r, n] = silu(y1[r, n]) * y3[r, n]        (gated: weights W1 and W3)
+//
+// for the rows offsets[g] <= r < offsets[g + 1] of each group g.
+//
+// The exponents are E8M0 scales as they stand (byte = e + 127), so the tensor
+// core applies them itself: tcgen05.mma kind::mxf8f6f4 with block scales takes
+// one scale per row and 32 K elements, and the 128 columns of an exponent are
+// four such steps that name the same byte.  The sum over all of K then stays in
+// one fp32 accumulator in tensor memory; no partial product is scaled or
+// added outside the tensor core.
+//
+// The weights are the M = 128 operand and the rows the N operand, in steps
+// of 16 up to NT: a group's ragged row count pads to 16 only, one thread of
+// the epilogue holds one output column, and a warp stores 32 neighbouring
+// columns of a row at a time.
+//
+// CTA structure (320 threads, tiles taken round-robin):
+//   warp 0      TMA producer: weight tile (128 x 128 codes) and row tile
+//               (NT x 128 codes), 128-byte swizzled, into a ring of stages
+//   warp 1      TMEM allocator and MMA issuer (one elected thread)
+//   warps 2-5   epilogue: TMEM -> registers -> global; two accumulators, so
+//               a tile's epilogue overlaps the next tile's products
+//   warps 6-9   scale writers: the exponents of four K-blocks at a time, as
+//               32-bit words of four E8M0 bytes, into one of two TMEM slots;
+//               each of the four warps fills its lane quarter with the same
+//               words, as the tensor core expects them
+// Gated tiles hold 64 output columns: the 128 weight rows alternate 16 of W1
+// and 16 of W3, so every warp's lanes 0-15 hold gates and lanes 16-31 the ups
+// of the same columns, which one shuffle per pair of rows brings together.
+//
+// Few tiles (one row through one matrix): a cluster of CTAs shares a tile,
+// each with its own range of K-blocks, and adds the partial tiles through
+// distributed shared memory in rank order, so results do not depend on timing.
+#include <algorithm>
+
+#include <cuda_bf16.h>
+
+#include "ffn_common.cuh"
+#include "sm100_scaled.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kBK = 128;                 // K elements of a stage = one exponent
+constexpr int kWTile = 128 * kBK;        // weight tile bytes
+constexpr int kThreads = 320;
+constexpr int kMaxStages = 11;
+constexpr int kMaxG = 1024;
+constexpr int kSfSlotCols = 12;          // 4 columns for the weights, 8 for the rows
+constexpr unsigned kAll = 0xffffffffu;
+
+struct alignas(64) GemmParams8 {
+  CUtensorMap x;        // [R, K] codes, box NT x 128
+  CUtensorMap w1, w3;   // [G * N, K] codes, box 128 (plain) or 16 (gated) x 128
+  const int8_t* xe;     // [R, KB]
+  const int8_t* w1e;    // [G, NB, KB]
+  const int8_t* w3e;
+  const int32_t* offsets;   // [G + 1]; nullptr: one group of all rows
+  void* y;
+  int y_bf16;
+  int G, R, N, K, KB, NB;
+  int nt;               // output column tiles of a group
+  int split;            // CTAs per tile (cluster size)
+  int* status;
+};
+
+// Row blocks of the groups: group g's rows are cut into equal blocks of at
+// most NT rows (a multiple of 16).
+struct GroupMap {
+  int total;                 // row blocks of all groups
+  int off[kMaxG + 1];
+  int prefix[kMaxG + 1];
+};
+
+struct Tile8 {
+  int g, n0, row0, rows;     // group, first output column, first row, rows
+};
+
+template <int NT>
+struct Cfg {
+  static constexpr int X_BYTES = NT * kBK;
+  static constexpr int STAGE = kWTile + X_BYTES;
+  static constexpr int STAGES = (200 * 1024) / STAGE < kMaxStages ? (200 * 1024) / STAGE : kMaxStages;
+  static constexpr int SF_COLS = 2 * kSfSlotCols;
+  static constexpr uint32_t TMEM_COLS = 2 * NT + SF_COLS <= 128   ? 128
+                                        : 2 * NT + SF_COLS <= 256 ? 256
+                                                                  : 512;
+  static_assert(2 * NT + SF_COLS <= 512 && NT % 16 == 0 && NT <= 240, "tensor memory columns");
+};
+
+struct Shared8 {
+  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t sf_full[2], sf_empty[2];
+  uint64_t acc_full[2], acc_empty[2];
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort;
+  int bad;
+  GroupMap gm;
+};
+
+template <int NT>
+constexpr int smem_bytes8() {
+  return 1024 + Cfg<NT>::STAGES * Cfg<NT>::STAGE + (int)sizeof(Shared8);
+}
+
+__device__ __forceinline__ int blocks_of(int rows, int nt) { return (rows + nt - 1) / nt; }
+
+// One warp: checks the offsets and counts each group's row blocks.  Offsets
+// that are not increasing within [0, R] give no tiles and raise kStBounds.
+template <int NT>
+__device__ void build_groups(GroupMap& gm, const GemmParams8& p, int lane) {
+  int carry = 0;
+  bool bad = false;
+  for (int base = 0; base < p.G; base += 32) {
+    const int g = base + lane;
+    int cnt = 0;
+    if (g < p.G) {
+      const int a = p.offsets ? p.offsets[g] : 0;
+      const int b = p.offsets ? p.offsets[g + 1] : p.R;
+      gm.off[g] = a;
+      if (g == p.G - 1) gm.off[p.G] = b;
+      if (a < 0 || b < a || b > p.R) bad = true;
+      else cnt = blocks_of(b - a, NT);
+    }
+    int incl = cnt;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(kAll, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (g < p.G) gm.prefix[g] = carry + incl - cnt;
+    carry += __shfl_sync(kAll, incl, 31);
+  }
+  bad = __any_sync(kAll, bad);
+  if (lane == 0) {
+    gm.prefix[p.G] = carry;
+    gm.total = bad ? 0 : carry;
+    if (bad && p.status) atomicOr(p.status, kStBounds);
+  }
+}
+
+// Tile t: groups in order, then output column tiles, row blocks fastest (the
+// CTAs that run together share weight tiles through L2).
+template <int NT, bool GATED>
+__device__ __forceinline__ Tile8 tile_at(int t, const GroupMap& gm, const GemmParams8& p) {
+  const int q = t / p.nt;
+  int lo = 0, hi = p.G - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (gm.prefix[mid] <= q) lo = mid; else hi = mid - 1;
+  }
+  const int rows = gm.off[lo + 1] - gm.off[lo];
+  const int nb = blocks_of(rows, NT);
+  const int local = t - gm.prefix[lo] * p.nt;
+  const int per = (blocks_of(rows, nb) + 15) / 16 * 16;   // rows per block
+  const int b = local % nb;
+  Tile8 ti;
+  ti.g = lo;
+  ti.n0 = (local / nb) * (GATED ? 64 : 128);
+  ti.row0 = gm.off[lo] + b * per;
+  ti.rows = max(0, min(per, rows - b * per));
+  return ti;
+}
+
+// Four E8M0 bytes of one row: exponents 4s .. 4s + 3 of its KB.  -128 has no
+// E8M0 counterpart (its byte would be the NaN scale).
+__device__ __forceinline__ uint32_t sf_word(const int8_t* e, int s, int KB, bool* bad) {
+  uint32_t w = 0;
+  const int8_t* q = e + 4 * s;
+  if (((reinterpret_cast<uintptr_t>(q) & 3u) == 0) && 4 * s + 4 <= KB) {
+    w = *reinterpret_cast<const uint32_t*>(q);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (4 * s + i < KB) w |= (uint32_t)(uint8_t)q[i] << (8 * i);
+  }
+  *bad |= __vcmpeq4(w, 0x80808080u) != 0;
+  return __vadd4(w, 0x7f7f7f7fu);
+}
+
+// Sixteen accumulator columns (rows of the group) of one weight row per
+// lane -> outputs.
+template <bool GATED>
+__device__ __forceinline__ void store16(const GemmParams8& p, const Tile8& ti, int q, int lane,
+                                        int c0, const float (&v)[16]) {
+  if (GATED) {
+    // lanes 0-15 finish the even rows of each pair, lanes 16-31 the odd ones
+    const bool up = lane >= 16;
+    const int n = ti.n0 + q * 16 + (lane & 15);
+    __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y);
+#pragma unroll
+    for (int j = 0; j < 16; j += 2) {
+      const float got = __shfl_xor_sync(kAll, up ? v[j] : v[j + 1], 16);
+      const float gate = up ? got : v[j];
+      const float mul = up ? v[j + 1] : got;
+      const int c = c0 + j + (up ? 1 : 0);
+      if (c < ti.rows && n < p.N)
+        y[(size_t)(ti.row0 + c) * p.N + n] = __float2bfloat16_rn(ffn::silu_times(gate, mul));
+    }
+  } else {
+    const int n = ti.n0 + q * 32 + lane;
+    if (n >= p.N) return;
+    if (p.y_bf16) {
+      __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y) + (size_t)(ti.row0 + c0) * p.N + n;
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        if (c0 + j < ti.rows) y[(size_t)j * p.N] = __float2bfloat16_rn(v[j]);
+    } else {
+      float* y = static_cast<float*>(p.y) + (size_t)(ti.row0 + c0) * p.N + n;
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        if (c0 + j < ti.rows) y[(size_t)j * p.N] = v[j];
+    }
+  }
+}
+
+template <int NT, bool GATED>
+__global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_constant__ GemmParams8 p) {
+  using C = Cfg<NT>;
+  constexpr int STAGES = C::STAGES;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = ptx::smem_addr(smem_raw);
+  uint8_t* ring = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+  Shared8& ss = *reinterpret_cast<Shared8*>(ring + STAGES * C::STAGE);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  ptx::pdl_launch_dependents();
+  if (warp == 1) {
+    ptx::tmem_alloc(&ss.tmem_base, C::TMEM_COLS);
+    ptx::tmem_relinquish();
+  }
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < STAGES; ++i) {
+      ptx::mbar_init(&ss.full[i], 1);
+      ptx::mbar_init(&ss.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(&ss.sf_full[i], 4);
+      ptx::mbar_init(&ss.sf_empty[i], 1);
+      ptx::mbar_init(&ss.acc_full[i], 1);
+      ptx::mbar_init(&ss.acc_empty[i], 4);
+    }
+    ptx::mbar_init(&ss.drain, 1);
+    ss.abort = 0;
+    ss.bad = 0;
+    ptx::fence_barrier_init();
+    ptx::tma_prefetch_desc(&p.x);
+    ptx::tma_prefetch_desc(&p.w1);
+    if (GATED) ptx::tma_prefetch_desc(&p.w3);
+  }
+  ptx::pdl_wait();
+  if (warp == 2) build_groups<NT>(ss.gm, p, lane);
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+
+  const uint32_t tmem = ss.tmem_base;
+  const uint32_t sf_base = tmem + 2 * NT;
+  volatile int* abort = &ss.abort;
+  // a cluster of `split` CTAs works on the same tiles, each on its K-blocks
+  const int rank = p.split > 1 ? (int)ptx::cluster_rank() : 0;
+  const int first = blockIdx.x / p.split, step = gridDim.x / p.split;
+  const int total = ss.gm.total * p.nt;
+  const int kb0 = (int)((long long)p.KB * rank / p.split);
+  const int kb1 = (int)((long long)p.KB * (rank + 1) / p.split);
+  // scale words cover K-blocks 4s .. 4s + 3
+  const int s0 = kb0 / 4, s1 = kb1 > kb0 ? (kb1 + 3) / 4 : s0;
+
+  if (warp == 0) {
+    if (ptx::elect_one()) {
+      int stage = 0;
+      uint32_t phase = 0, issued = 0, parity = 0;
+      bool ok = true;
+      for (int t = first; ok && t < total; t += step) {
+        const Tile8 ti = tile_at<NT, GATED>(t, ss.gm, p);
+        const int wrow = ti.g * p.N + ti.n0;
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (!ptx::mbar_wait(&ss.empty[stage], phase ^ 1u, abort)) { ok = false; break; }
+          uint8_t* sw = ring + stage * C::STAGE;
+          uint64_t* bar = &ss.full[stage];
+          ptx::mbar_arrive_expect_tx(bar, C::STAGE);
+          if (GATED) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              ptx::tma_load_2d(sw + j * 4096, &p.w1, bar, kb * kBK, wrow + j * 16);
+              ptx::tma_load_2d(sw + j * 4096 + 2048, &p.w3, bar, kb * kBK, wrow + j * 16);
+            }
+          } else {
+            ptx::tma_load_2d(sw, &p.w1, bar, kb * kBK, wrow);
+          }
+          ptx::tma_load_2d(sw + kWTile, &p.x, bar, kb * kBK, ti.row0);
+          issued |= 1u << stage;
+          parity = (parity & ~(1u << stage)) | (phase << stage);
+          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+        }
+      }
+      for (int s = 0; s < STAGES; ++s)
+        if (issued & (1u << s)) ffn::wait_drain(&ss.full[s], (parity >> s) & 1u, abort);
+    }
+  } else if (warp == 1) {
+    if (ptx::elect_one()) {
+      int stage = 0, buf = 0, slot = 0;
+      uint32_t phase = 0, aphase = 0, sphase = 0;
+      bool ok = true;
+      for (int t = first; ok && t < total; t += step) {
+        const Tile8 ti = tile_at<NT, GATED>(t, ss.gm, p);
+        const uint32_t idesc = ptx::idesc_mxf8(128, max(16, (ti.rows + 15) / 16 * 16));
+        if (!ptx::mbar_wait(&ss.acc_empty[buf], aphase ^ 1u, abort)) break;
+        const uint32_t acc = tmem + buf * NT;
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (kb == kb0 || (kb & 3) == 0) {
+            if (!ptx::mbar_wait(&ss.sf_full[slot], sphase, abort)) { ok = false; break; }
+          }
+          if (!ptx::mbar_wait(&ss.full[stage], phase, abort)) { ok = false; break; }
+          ptx::tc_fence_after();
+          const uint32_t sw = ptx::smem_addr(ring + stage * C::STAGE);
+          const uint64_t da = ptx::smem_desc_sw128(sw);
+          const uint64_t db = ptx::smem_desc_sw128(sw + kWTile);
+          const uint32_t id = idesc | ptx::idesc_sf_byte(kb & 3, kb & 3);
+          const uint32_t sfa = sf_base + slot * kSfSlotCols, sfb = sfa + 4;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            ptx::mma_mxf8_ss(acc, da + 2 * k, db + 2 * k, id, sfa, sfb, kb > kb0 || k > 0);
+          ptx::mma_commit(&ss.empty[stage]);
+          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+          if ((kb & 3) == 3 || kb == kb1 - 1) {
+            ptx::mma_commit(&ss.sf_empty[slot]);
+            if (++slot == 2) { slot = 0; sphase ^= 1u; }
+          }
+        }
+        if (!ok) break;
+        ptx::mma_commit(&ss.acc_full[buf]);
+        if (++buf == 2) { buf = 0; aphase ^= 1u; }
+      }
+      // nothing of this CTA is in flight when its tensor memory is freed
+      ptx::mma_commit(&ss.drain);
+      ffn::wait_drain(&ss.drain, 0, abort);
+    }
+  } else if (warp < 6) {
+    const int q = warp & 3;              // TMEM lane quarter of this warp
+    int buf = 0;
+    uint32_t aphase = 0;
+    for (int t = first; t < total; t += step) {
+      const Tile8 ti = tile_at<NT, GATED>(t, ss.gm, p);
+      if (__any_sync(kAll, !ptx::mbar_wait(&ss.acc_full[buf], aphase, abort))) break;
+      ptx::tc_fence_after();
+      const uint32_t acc = tmem + buf * NT + ((uint32_t)(q * 32) << 16);
+      for (int c = 0; c < ti.rows; c += 16) {
+        uint32_t r[16];
+        ptx::tmem_ld_x16(acc + c, r);
+        ptx::tmem_wait_ld();
+        float v[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] = kb1 > kb0 ? __uint_as_float(r[j]) : 0.f;
+        if (p.split > 1) {
+          // this CTA's part of the tile, [row][weight row], in the ring (all
+          // its loads and products are done, and a cluster has one tile)
+          float* part = reinterpret_cast<float*>(ring);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) part[(c + j) * 128 + q * 32 + lane] = v[j];
+        } else {
+          store16<GATED>(p, ti, q, lane, c, v);
+        }
+      }
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&ss.acc_empty[buf]);
+      if (++buf == 2) { buf = 0; aphase ^= 1u; }
+    }
+  } else {
+    const int q = warp & 3;
+    int slot = 0;
+    uint32_t sphase = 0;
+    bool bad = false, ok = true;
+    for (int t = first; ok && t < total; t += step) {
+      const Tile8 ti = tile_at<NT, GATED>(t, ss.gm, p);
+      const int8_t* we = (GATED && (lane & 16) ? p.w3e : p.w1e) +
+                         ((size_t)ti.g * p.NB + ti.n0 / 128) * p.KB;
+      constexpr int XC = (NT + 31) / 32;
+      for (int s = s0; s < s1; ++s) {
+        uint32_t wa[4], wx[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        wa[0] = wa[1] = wa[2] = wa[3] = sf_word(we, s, p.KB, &bad);
+#pragma unroll
+        for (int c = 0; c < XC; ++c)
+          if (c * 32 + lane < ti.rows)
+            wx[c] = sf_word(p.xe + (size_t)(ti.row0 + c * 32 + lane) * p.KB, s, p.KB, &bad);
+        if (__any_sync(kAll, !ptx::mbar_wait(&ss.sf_empty[slot], sphase ^ 1u, abort))) {
+          ok = false;
+          break;
+        }
+        ptx::tc_fence_after();
+        const uint32_t dst = sf_base + slot * kSfSlotCols + ((uint32_t)(q * 32) << 16);
+        ptx::tmem_st_x4(dst, wa);
+        if (XC > 4) ptx::tmem_st_x8(dst + 4, wx);
+        else if (XC > 1) ptx::tmem_st_x4(dst + 4, wx);
+        else ptx::tmem_st_x1(dst + 4, wx[0]);
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&ss.sf_full[slot]);
+        if (++slot == 2) { slot = 0; sphase ^= 1u; }
+      }
+    }
+    if (bad) ss.bad = 1;
+  }
+
+  __syncthreads();
+  if (p.split > 1) {
+    // partial tiles -> outputs: rank r finishes the rows r, r + split, ...
+    ptx::cluster_sync();
+    if (first < total && !*abort) {
+      const Tile8 ti = tile_at<NT, GATED>(first, ss.gm, p);
+      const uint32_t part = ptx::smem_addr(ring);
+      if (GATED) {
+        for (int i = threadIdx.x; i < ti.rows * 64; i += kThreads) {
+          const int c = i >> 6, f = i & 63;
+          if (c % p.split != rank) continue;
+          const uint32_t at = part + (c * 128 + (f >> 4) * 32 + (f & 15)) * 4;
+          float g = 0.f, u = 0.f;
+          for (int r = 0; r < p.split; ++r) {
+            g += ptx::ld_cluster_f32(at, r);
+            u += ptx::ld_cluster_f32(at + 64, r);
+          }
+          if (ti.n0 + f < p.N)
+            static_cast<__nv_bfloat16*>(p.y)[(size_t)(ti.row0 + c) * p.N + ti.n0 + f] =
+                __float2bfloat16_rn(ffn::silu_times(g, u));
+        }
+      } else {
+        for (int i = threadIdx.x; i < ti.rows * 128; i += kThreads) {
+          const int c = i >> 7, f = i & 127;
+          if (c % p.split != rank) continue;
+          float v = 0.f;
+          for (int r = 0; r < p.split; ++r) v += ptx::ld_cluster_f32(part + i * 4, r);
+          const size_t at = (size_t)(ti.row0 + c) * p.N + ti.n0 + f;
+          if (ti.n0 + f < p.N) {
+            if (p.y_bf16) static_cast<__nv_bfloat16*>(p.y)[at] = __float2bfloat16_rn(v);
+            else static_cast<float*>(p.y)[at] = v;
+          }
+        }
+      }
+    }
+    ptx::cluster_sync();   // no CTA leaves while another reads its part
+  }
+  if (warp == 1) ptx::tmem_dealloc(tmem, C::TMEM_COLS);
+  if (threadIdx.x == 0 && p.status) {
+    if (ss.abort) atomicOr(p.status, kStTimeout);
+    if (ss.bad) atomicOr(p.status, kStBounds);
+  }
+}
+
+template <int NT, bool GATED>
+cudaError_t launch_nt(const GemmParams8& p, long long tiles, cudaStream_t st) {
+  static std::atomic<uint64_t> smem_set{0};
+  cudaError_t e = set_smem_once(gemm_fp8_kernel<NT, GATED>, smem_bytes8<NT>(), smem_set);
+  if (e != cudaSuccess) return e;
+  const int sms = num_sms();
+  const long long want = tiles * p.split;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(p.split > 1 ? want : want < sms ? want : sms));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem_bytes8<NT>();
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = p.split;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, gemm_fp8_kernel<NT, GATED>, p);
+}
+
+template <int NT>
+cudaError_t launch_any(GemmParams8& p, bool gated, cudaStream_t st, const char** why,
+                       const Gemm8Args& a) {
+  const uint32_t box = gated ? 16 : 128;
+  bool ok = make_tensor_map(&p.x, a.x, a.R, a.K, NT, kBK, 1, 128) &&
+            make_tensor_map(&p.w1, a.W1, (uint64_t)a.G * a.N, a.K, box, kBK, 1, 128);
+  p.w3 = p.w1;
+  if (ok && gated) ok = make_tensor_map(&p.w3, a.W3, (uint64_t)a.G * a.N, a.K, box, kBK, 1, 128);
+  if (!ok) {
+    *why = "cuTensorMapEncodeTiled failed for a product operand";
+    return cudaErrorInvalidValue;
+  }
+  // row blocks: at most one per group with rows, and one per NT rows
+  const long long blocks = std::min<long long>(a.R, (long long)a.R / NT + std::min(a.G, a.R));
+  const long long tiles = blocks * p.nt;
+  // Few tiles: split K over a cluster while that leaves every CTA an SM of its
+  // own and at least two K-blocks.
+  p.split = 1;
+  while (p.split < 8 && tiles * p.split * 2 <= num_sms() && p.KB >= p.split * 4) p.split *= 2;
+  return gated ? launch_nt<NT, true>(p, tiles, st) : launch_nt<NT, false>(p, tiles, st);
+}
+
+}  // namespace
+
+cudaError_t launch_gemm_fp8(const Gemm8Args& a, cudaStream_t st, const char** why) {
+  const bool gated = a.W3 != nullptr;
+  GemmParams8 p{};
+  p.xe = a.xe;
+  p.w1e = a.W1e;
+  p.w3e = a.W3e;
+  p.offsets = a.offsets;
+  p.y = a.y;
+  p.y_bf16 = a.y_bf16;
+  p.G = a.G; p.R = a.R; p.N = a.N; p.K = a.K;
+  p.KB = (a.K + 127) / 128;
+  p.NB = (a.N + 127) / 128;
+  p.nt = gated ? (a.N + 63) / 64 : (a.N + 127) / 128;
+  p.status = a.status;
+  *why = "product launch";
+  // Rows per tile by the average group: small groups leave the weight stream
+  // in charge, so the ring holds weights; large ones are bound by the products.
+  const int avg = a.R / a.G;
+  if (avg <= 16) return launch_any<32>(p, gated, st, why, a);
+  if (avg <= 96) return launch_any<128>(p, gated, st, why, a);
+  return launch_any<240>(p, gated, st, why, a);
+}
+
+}  // namespace moe

@@ -211,6 +211,23 @@ cudaError_t launch_expert_ffn_fp8(const FfnArgs& a, const Fp8Weights& w, cudaStr
 cudaError_t launch_fp8_dequantize(const uint8_t* codes, const int8_t* exps, int G, int R, int K,
                                   uint16_t* out, int* status, cudaStream_t st);
 
+// bf16 rows x[idx[r]] (idx nullable: x[r]) -> E4M3 codes [R, K] and one exponent per
+// 128 columns [R, ceil(K/128)].
+cudaError_t launch_quantize_fp8(const uint16_t* x, int src_rows, const int32_t* idx, int R, int K,
+                                uint8_t* codes, int8_t* exps, int* status, cudaStream_t st);
+// Grouped products of such rows with E4M3 weights; W3 set: the gated form
+// (y is bf16 then).
+struct Gemm8Args {
+  const uint8_t *x, *W1, *W3;
+  const int8_t *xe, *W1e, *W3e;
+  const int32_t* offsets;   // nullable: one group of all rows
+  void* y;
+  int y_bf16;
+  int G, R, N, K;
+  int* status;
+};
+cudaError_t launch_gemm_fp8(const Gemm8Args& a, cudaStream_t st, const char** why);
+
 // dst[i] = src[idx[i]] for n rows of row_bytes (a multiple of 16) bytes.
 cudaError_t launch_gather_bytes(const void* src, int src_rows, const int32_t* idx, int n,
                                 int row_bytes, void* dst, int* status, cudaStream_t st);
