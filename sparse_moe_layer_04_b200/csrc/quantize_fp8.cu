@@ -31,78 +31,96 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-// Sixteen lanes own a block of 128 columns, eight columns (16 bytes) each; a
-// warp takes two neighbouring blocks of a row at a time, and kUnroll such
-// pairs are loaded before the first is used.
-constexpr int kUnroll = 4;
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
 
+// 32 bytes in one load (16-byte aligned addresses that are not 32-byte aligned
+// take two).
+__device__ __forceinline__ void load32(const uint16_t* p, bool wide, uint32_t (&w)[8]) {
+  if (wide) {
+    asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]),
+                   "=r"(w[6]), "=r"(w[7])
+                 : "l"(p));
+  } else {
+    const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
+    const uint4 b = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+    w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+    w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+  }
+}
+
+// A warp takes U chunks of 512 columns of one row: eight lanes own a block of
+// 128 columns, sixteen columns (32 bytes) each.  All U loads are issued before
+// the first is used.
+template <int U>
 __global__ void __launch_bounds__(kThreads) quantize_fp8_kernel(
     const uint16_t* __restrict__ x, int src_rows, const int32_t* __restrict__ idx, int R, int K,
-    uint8_t* __restrict__ codes, int8_t* __restrict__ exps, int* status) {
+    int KB, bool wide, uint8_t* __restrict__ codes, int8_t* __restrict__ exps, int* status) {
   ptx::pdl_launch_dependents();
   ptx::pdl_wait();
-  const int KB = (K + 127) / 128;
-  const int pairs = (KB + 1) / 2;               // 256-column units of a row
-  const long long units = (long long)R * pairs;
   const int lane = threadIdx.x & 31;
-  const long long warp = (blockIdx.x * (long long)kThreads + threadIdx.x) >> 5;
-  const long long nwarps = ((long long)gridDim.x * kThreads) >> 5;
+  const int r = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  if (r >= R) return;
+  const int col0 = blockIdx.y * (512 * U) + lane * 16;
+  const int s = idx ? idx[r] : r;
   int bad = 0;
-  for (long long u0 = warp * kUnroll; u0 < units; u0 += nwarps * kUnroll) {
-    uint4 v[kUnroll];
-    long long row[kUnroll];
-    int col[kUnroll];
+  const bool ok = s >= 0 && s < src_rows;
+  if (!ok) bad = kStBounds;
+  const uint16_t* src = x + (size_t)(ok ? s : 0) * K + col0;
+  uint32_t w[U][8];
 #pragma unroll
-    for (int i = 0; i < kUnroll; ++i) {
-      const long long u = u0 + i;
-      row[i] = u / pairs;
-      col[i] = (int)(u - row[i] * pairs) * 256 + lane * 8;
-      v[i] = make_uint4(0, 0, 0, 0);
-      if (u < units && col[i] < K) {
-        const int s = idx ? idx[row[i]] : (int)row[i];
-        if (s >= 0 && s < src_rows)
-          v[i] = *reinterpret_cast<const uint4*>(x + (size_t)s * K + col[i]);
-        else
-          bad |= kStBounds;
-      }
+  for (int i = 0; i < U; ++i) {
+    if (ok && col0 + 512 * i < K) {
+      load32(src + 512 * i, wide, w[i]);
+    } else {
+#pragma unroll
+      for (int q = 0; q < 8; ++q) w[i][q] = 0;
     }
+  }
 #pragma unroll
-    for (int i = 0; i < kUnroll; ++i) {
-      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-      // largest finite magnitude as bf16 bits (they order like the values)
-      uint32_t top = 0;
+  for (int i = 0; i < U; ++i) {
+    const int col = col0 + 512 * i;
+    // the largest magnitude of the block, as bf16 bits (they order like the values)
+    uint32_t t2 = 0;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
+    for (int q = 0; q < 8; ++q) t2 = max_u16x2(t2, w[i][q] & 0x7fff7fffu);
+    uint32_t top = max(t2 & 0xffffu, t2 >> 16);
 #pragma unroll
-        for (int s = 0; s < 32; s += 16) {
-          const uint32_t m = (w[q] >> s) & 0x7fffu;
-          if (m >= 0x7f80u) bad |= kStNonFinite;
-          else top = max(top, m);
-        }
+    for (int off = 4; off; off >>= 1) top = max(top, __shfl_xor_sync(kAll, top, off));
+    const bool odd = top >= 0x7f80u;   // a NaN or an infinity in this block
+    if (__any_sync(kAll, odd)) {
+      // the largest finite magnitude instead
+      if (odd) bad |= kStNonFinite;
+      top = 0;
+#pragma unroll
+      for (int q = 0; q < 16; ++q) {
+        const uint32_t m = (w[i][q / 2] >> (16 * (q & 1))) & 0x7fffu;
+        if (m < 0x7f80u) top = max(top, m);
       }
 #pragma unroll
-      for (int off = 8; off; off >>= 1) top = max(top, __shfl_xor_sync(kAll, top, off));
-      // p - 8 with p = (bits >> 7) - 127, one more when the fraction exceeds
-      // 0.75 (0x60 of 0x80): adding 0x1f carries into the exponent exactly then
-      int e = top ? max((int)((top + 0x1fu) >> 7) - 135, kQMinExp) : 0;
-      const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
-      uint32_t c[2];
+      for (int off = 4; off; off >>= 1) top = max(top, __shfl_xor_sync(kAll, top, off));
+    }
+    // p - 8 with p = (bits >> 7) - 127, one more when the fraction exceeds
+    // 0.75 (0x60 of 0x80): adding 0x1f carries into the exponent exactly then
+    const int e = top ? max((int)((top + 0x1fu) >> 7) - 135, kQMinExp) : 0;
+    const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+    uint32_t c[4];
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const uint32_t a = w[2 * q], b = w[2 * q + 1];
-        uint32_t lo = e4m3x2(bf_lo(a) * inv, bf_hi(a) * inv);
-        uint32_t hi = e4m3x2(bf_lo(b) * inv, bf_hi(b) * inv);
-        // infinities are marked like NaN (the conversion would saturate them)
-        if ((a & 0x7fffu) >= 0x7f80u) lo = (lo & 0xff00u) | 0x7fu;
-        if (((a >> 16) & 0x7fffu) >= 0x7f80u) lo = (lo & 0x00ffu) | 0x7f00u;
-        if ((b & 0x7fffu) >= 0x7f80u) hi = (hi & 0xff00u) | 0x7fu;
-        if (((b >> 16) & 0x7fffu) >= 0x7f80u) hi = (hi & 0x00ffu) | 0x7f00u;
-        c[q] = lo | (hi << 16);
-      }
-      if (u0 + i < units && col[i] < K) {
-        *reinterpret_cast<uint2*>(codes + (size_t)row[i] * K + col[i]) = make_uint2(c[0], c[1]);
-        if ((lane & 15) == 0) exps[(size_t)row[i] * KB + col[i] / 128] = (int8_t)e;
-      }
+    for (int q = 0; q < 4; ++q) {
+      const uint32_t a = w[i][2 * q], b = w[i][2 * q + 1];
+      c[q] = e4m3x2(bf_lo(a) * inv, bf_hi(a) * inv) |
+             (e4m3x2(bf_lo(b) * inv, bf_hi(b) * inv) << 16);
+    }
+    if (odd) {
+      // infinities are marked like NaN (the conversion saturates them)
+#pragma unroll
+      for (int q = 0; q < 16; ++q)
+        if (((w[i][q / 2] >> (16 * (q & 1))) & 0x7fffu) >= 0x7f80u)
+          c[q / 4] = (c[q / 4] & ~(0xffu << (8 * (q & 3)))) | (0x7fu << (8 * (q & 3)));
+    }
+    if (col < K) {
+      *reinterpret_cast<uint4*>(codes + (size_t)r * K + col) = make_uint4(c[0], c[1], c[2], c[3]);
+      if ((lane & 7) == 0) exps[(size_t)r * KB + (col >> 7)] = (int8_t)e;
     }
   }
   if (bad && status) atomicOr(status, bad);
@@ -112,13 +130,19 @@ __global__ void __launch_bounds__(kThreads) quantize_fp8_kernel(
 
 cudaError_t launch_quantize_fp8(const uint16_t* x, int src_rows, const int32_t* idx, int R, int K,
                                 uint8_t* codes, int8_t* exps, int* status, cudaStream_t st) {
-  const long long units = (long long)R * ((K + 255) / 256);
-  const int per_block = kThreads / 32 * kUnroll;
-  long long blocks = (units + per_block - 1) / per_block;
-  const long long cap = 8ll * num_sms();
-  if (blocks > cap) blocks = cap;
-  return launch_pdl(quantize_fp8_kernel, dim3((unsigned)blocks), dim3(kThreads), 0, st, x,
-                    src_rows, idx, R, K, codes, exps, status);
+  const int chunks = (K + 511) / 512;
+  const int warps = kThreads / 32;
+  const unsigned gx = (unsigned)((R + warps - 1) / warps);
+  // rows start on 32 bytes when the matrix does (K is a multiple of 16)
+  const bool wide = (reinterpret_cast<uintptr_t>(x) & 31u) == 0;
+  const int KB = (K + 127) / 128;
+  // A chunk per warp while that fits on the SMs at once (latency counts); else
+  // four, whose loads a warp has in flight together.
+  if ((long long)gx * chunks <= 4ll * num_sms())
+    return launch_pdl(quantize_fp8_kernel<1>, dim3(gx, chunks), dim3(kThreads), 0, st, x, src_rows,
+                      idx, R, K, KB, wide, codes, exps, status);
+  return launch_pdl(quantize_fp8_kernel<4>, dim3(gx, (chunks + 3) / 4), dim3(kThreads), 0, st, x,
+                    src_rows, idx, R, K, KB, wide, codes, exps, status);
 }
 
 }  // namespace moe
