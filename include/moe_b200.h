@@ -273,6 +273,35 @@ int moe_forward_fp8(const void* h, const float* Wr, const float* bias, const moe
                     const moe_dims_t* dims, float* out, int32_t* idx_out, float* w_out, void* ws,
                     size_t ws_bytes, moe_stream_t stream);
 
+/* ---- The layer for a few tokens -----------------------------------------
+ * moe_forward for 1 to 16 tokens (more: MOE_ERR_UNSUPPORTED; T = 0 enqueues
+ * nothing) in two kernels on `stream`: routing, then both expert products and
+ * the merge in one persistent kernel that reads each chosen expert's weights
+ * once.  The same layer, arguments, limits, workspace and errors as
+ * moe_forward; two differences in precision: the logits' sums run in another
+ * (fixed) order, and the gated activation enters the w2 product with 16
+ * significant bits instead of 8.  Capturable in a CUDA graph; no internal
+ * stream.  moe_ws_expert_counts and moe_ws_touched_experts hold for it too.
+ * Repeated calls give identical bits.  Calls that share a workspace must not
+ * overlap on the GPU; one workspace sized for the largest T may serve calls of
+ * this layer with any T (and with either kind of weights). */
+int moe_forward_few(const void* h, const float* Wr, const float* bias, const void* W1,
+                    const void* W3, const void* W2, const void* Ws1, const void* Ws3,
+                    const void* Ws2, const moe_dims_t* dims, float* out, int32_t* idx_out,
+                    float* w_out, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* moe_forward_few with FP8 expert weights (rules as moe_forward_fp8).  The
+ * codes enter the tensor core as they are; hidden rows and activations enter
+ * as sums of three and four E4M3 pieces, which hold a hidden value to within
+ * 2^-25 of the largest of its 128 neighbours (exactly, when it is not much
+ * smaller than that), and an activation to within 2^-16 of itself plus 2^-29
+ * of the largest of its 32 neighbours.  A non-finite activation gives NaN.
+ * An exponent outside [-117, 7] raises MOE_ERR_BOUNDS. */
+int moe_forward_few_fp8(const void* h, const float* Wr, const float* bias,
+                        const moe_fp8_weights_t* w8, const moe_dims_t* dims, float* out,
+                        int32_t* idx_out, float* w_out, void* ws, size_t ws_bytes,
+                        moe_stream_t stream);
+
 /* Decodes FP8 weights to bf16 with the same exact decoding the FP8 layer
  * uses: codes [G, R, K] (16-byte aligned), exps [G, ceil(R/128), ceil(K/128)]
  * -> out [G, R, K] bf16 (16-byte aligned), out[g, r, c] = e4m3(code) *

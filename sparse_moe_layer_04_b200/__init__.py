@@ -91,6 +91,8 @@ def _load() -> ctypes.CDLL:
         "moe_expert_ffn_fp8": (I, [P, P, P, W8, D, P, P, Z, P]),
         "moe_forward_fp8": (I, [P, P, P, W8, D, P, P, P, P, Z, P]),
         "moe_fp8_dequantize": (I, [P, P, I, I, I, P, P, P]),
+        "moe_forward_few": (I, [P, P, P, P, P, P, P, P, P, D, P, P, P, P, Z, P]),
+        "moe_forward_few_fp8": (I, [P, P, P, W8, D, P, P, P, P, Z, P]),
         "moe_quantize_fp8": (I, [P, I, P, I, I, P, P, P, P]),
         "moe_grouped_gemm_fp8": (I, [P, P, P, P, P, I, I, I, I, P, I, P, P]),
         "moe_gated_gemm_fp8": (I, [P, P, P, P, P, P, P, I, I, I, I, P, P, P]),
@@ -243,6 +245,51 @@ def moe_forward_fp8(h, Wr, bias, w8: moe_fp8_weights_t, d, out, ws, idx_out=None
                                 _ptr(w_out, torch.float32, "w_out"), wp, wn, _stream(stream)))
 
 
+def _few_shapes(h, Wr, bias, d, out, idx_out, w_out) -> None:
+    _shape(h, (d.T, d.D), "h")
+    _shape(Wr, (d.E, d.D), "Wr")
+    _shape(bias, (d.E,), "bias")
+    _shape(out, (d.T, d.D), "out")
+    for t, name in ((idx_out, "idx_out"), (w_out, "w_out")):
+        if t is not None:
+            _shape(t, (d.T, d.k), name)
+
+
+def moe_forward_few(h, Wr, bias, W1, W3, W2, Ws1, Ws3, Ws2, d, out, ws, idx_out=None, w_out=None,
+                    stream=None) -> None:
+    """moe_forward for at most 16 tokens, in two kernels (arguments as moe_forward)."""
+    _few_shapes(h, Wr, bias, d, out, idx_out, w_out)
+    for t, n, want in ((W1, "W1", (d.E, d.F, d.D)), (W3, "W3", (d.E, d.F, d.D)),
+                       (W2, "W2", (d.E, d.D, d.F))):
+        _shape(t, want, n)
+    if d.S:
+        for t, n, want in ((Ws1, "Ws1", (d.S, d.Fs, d.D)), (Ws3, "Ws3", (d.S, d.Fs, d.D)),
+                           (Ws2, "Ws2", (d.S, d.D, d.Fs))):
+            _shape(t, want, n)
+    wp, wn = _ws(ws)
+    bf = torch.bfloat16
+    args = (_ptr(h, bf, "h"), _ptr(Wr, torch.float32, "Wr"), _ptr(bias, torch.float32, "bias"),
+            _ptr(W1, bf, "W1"), _ptr(W3, bf, "W3"), _ptr(W2, bf, "W2"), _ptr(Ws1, bf, "Ws1"),
+            _ptr(Ws3, bf, "Ws3"), _ptr(Ws2, bf, "Ws2"), ctypes.byref(d),
+            _ptr(out, torch.float32, "out"), _ptr(idx_out, torch.int32, "idx_out"),
+            _ptr(w_out, torch.float32, "w_out"), wp, wn)
+    _same_device(h, Wr, bias, W1, W3, W2, *((Ws1, Ws3, Ws2) if d.S else ()), out, idx_out, w_out, ws)
+    _check(_lib.moe_forward_few(*args, _stream(stream)))
+
+
+def moe_forward_few_fp8(h, Wr, bias, w8: moe_fp8_weights_t, d, out, ws, idx_out=None, w_out=None,
+                        stream=None) -> None:
+    """moe_forward_fp8 for at most 16 tokens, in two kernels (arguments as moe_forward_fp8)."""
+    _few_shapes(h, Wr, bias, d, out, idx_out, w_out)
+    wp, wn = _ws(ws)
+    args = (_ptr(h, torch.bfloat16, "h"), _ptr(Wr, torch.float32, "Wr"),
+            _ptr(bias, torch.float32, "bias"), ctypes.byref(w8), ctypes.byref(d),
+            _ptr(out, torch.float32, "out"), _ptr(idx_out, torch.int32, "idx_out"),
+            _ptr(w_out, torch.float32, "w_out"), wp, wn)
+    _same_device(h, Wr, bias, out, idx_out, w_out, ws)
+    _check(_lib.moe_forward_few_fp8(*args, _stream(stream)))
+
+
 def moe_fp8_dequantize(codes, exps, out, ws=None, stream=None) -> None:
     """codes [G, R, K] (or [R, K]) E4M3, exps [G, ceil(R/128), ceil(K/128)]
     int8 -> out bf16 of the codes' shape."""
@@ -303,11 +350,10 @@ def _gemm_fp8_args(x, xe, W, We, out, offsets):
     return G, R, N, K
 
 
-def _weight_fp8(W, We, G: int, N: int, K: int, name: str):
+def _weight_fp8_shape(W, We, G: int, N: int, K: int, name: str) -> None:
     _shape(W, (N, K) if W.dim() == 2 and G == 1 else (G, N, K), name)
     _shape(We, (_blocks(N), _blocks(K)) if We.dim() == 2 and G == 1 else
            (G, _blocks(N), _blocks(K)), name + "e")
-    return _code_ptr(W, name), _ptr(We, torch.int8, name + "e")
 
 
 def moe_grouped_gemm_fp8(x, xe, W, We, y, offsets=None, ws=None, stream=None) -> None:
@@ -317,9 +363,10 @@ def moe_grouped_gemm_fp8(x, xe, W, We, y, offsets=None, ws=None, stream=None) ->
     G, R, N, K = _gemm_fp8_args(x, xe, W, We, y, offsets)
     if y.dtype not in (torch.float32, torch.bfloat16):
         raise TypeError(f"y: expected float32 or bfloat16, got {y.dtype}")
-    w, we = _weight_fp8(W, We, G, N, K, "W")
-    args = (_code_ptr(x, "x"), _ptr(xe, torch.int8, "xe"), _ptr(offsets, torch.int32, "offsets"), w,
-            we, G, R, N, K, _ptr(y, None, "y"), int(y.dtype == torch.bfloat16), _ws(ws)[0])
+    _weight_fp8_shape(W, We, G, N, K, "W")
+    args = (_code_ptr(x, "x"), _ptr(xe, torch.int8, "xe"), _ptr(offsets, torch.int32, "offsets"),
+            _code_ptr(W, "W"), _ptr(We, torch.int8, "We"), G, R, N, K, _ptr(y, None, "y"),
+            int(y.dtype == torch.bfloat16), _ws(ws)[0])
     _same_device(x, xe, W, We, y, offsets, ws)
     _check(_lib.moe_grouped_gemm_fp8(*args, _stream(stream)))
 
@@ -328,10 +375,11 @@ def moe_gated_gemm_fp8(x, xe, W1, W1e, W3, W3e, act, offsets=None, ws=None, stre
     """silu(x W1^T) * (x W3^T) per group -> act [R, N] bf16; operands as
     moe_grouped_gemm_fp8, W3 and W3e shaped like W1 and W1e."""
     G, R, N, K = _gemm_fp8_args(x, xe, W1, W1e, act, offsets)
-    w1, w1e = _weight_fp8(W1, W1e, G, N, K, "W1")
-    w3, w3e = _weight_fp8(W3, W3e, G, N, K, "W3")
-    args = (_code_ptr(x, "x"), _ptr(xe, torch.int8, "xe"), _ptr(offsets, torch.int32, "offsets"), w1,
-            w1e, w3, w3e, G, R, N, K, _ptr(act, torch.bfloat16, "act"), _ws(ws)[0])
+    _weight_fp8_shape(W1, W1e, G, N, K, "W1")
+    _weight_fp8_shape(W3, W3e, G, N, K, "W3")
+    args = (_code_ptr(x, "x"), _ptr(xe, torch.int8, "xe"), _ptr(offsets, torch.int32, "offsets"),
+            _code_ptr(W1, "W1"), _ptr(W1e, torch.int8, "W1e"), _code_ptr(W3, "W3"),
+            _ptr(W3e, torch.int8, "W3e"), G, R, N, K, _ptr(act, torch.bfloat16, "act"), _ws(ws)[0])
     _same_device(x, xe, W1, W1e, W3, W3e, act, offsets, ws)
     _check(_lib.moe_gated_gemm_fp8(*args, _stream(stream)))
 

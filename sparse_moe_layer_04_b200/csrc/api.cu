@@ -1,4 +1,5 @@
 // C ABI of the library: argument checks, workspace layout, launches.
+#include <algorithm>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -168,6 +169,9 @@ bool ws_layout(const moe_dims_t& d, WsLayout* L) {
   };
   L->status = take(256);
   L->ticket = take(256);
+  // counters of the few-token layer: zero between calls, so they stand where
+  // no other T of the same layer moves them
+  L->f_claim = take((64 + 2 + S + std::min<size_t>(E, kFewMaxT * k) + (D + 127) / 128) * 4);
   L->partials = take((size_t)sp.nsplit * T * E * 4);
   L->wr3 = take(sp.tensor && !sp.fused ? E * 3 * D * 2 : 0);
   L->idx = take(T * k * 4);
@@ -187,6 +191,27 @@ bool ws_layout(const moe_dims_t& d, WsLayout* L) {
   L->y = take((T * k + S * T) * D * 4);
   L->touched = take(4);
   L->gmask = take(T <= kPermBlockTokens ? E * (kPermBlockTokens / 32) * 4 : 0);
+  L->f_slots = L->f_mask = L->f_hq = L->f_hqe = L->f_act = L->f_exp = L->f_planes = 0;
+  if (T > 0 && T <= (size_t)kFewMaxT) {
+    const FewPlan p16 = few_plan(d, false), p8 = few_plan(d, true);
+    const size_t slots = p16.max_slots, most = slots - S;
+    // bytes of the activations (bf16 or codes) and of their exponents
+    const size_t act = std::max((most * F + S * Fs) * p16.PA * 2 + 16,
+                                (most * F + S * Fs) * p8.PA + 16) + 256;
+    const size_t ex = (most * ((F + 127) / 128) + S * ((Fs + 127) / 128)) * 4 * p8.TP + 256;
+    // planes of the down products: few_plan splits K only while there are
+    // fewer than 6 * 148 units, so at most twice that many units are split;
+    // the bound grows with T, so that a workspace serves every smaller T
+    const size_t planes =
+        std::max(slots, std::min<size_t>(8 * slots, 12 * kSplitTargetBlocks / p16.nd));
+    L->f_slots = take((64 + T * k + slots) * 4);
+    L->f_mask = take(slots * 4);
+    L->f_hq = take(3 * p8.TP * D);
+    L->f_hqe = take(T * ((D + 127) / 128));
+    L->f_act = take(act);
+    L->f_exp = take(ex);
+    L->f_planes = take(planes * T * D * 4);
+  }
   L->total = off;
   return true;
 }
@@ -501,6 +526,63 @@ int forward_impl(const void* h, const float* Wr, const float* bias, const Expert
   if (e != cudaSuccess) return cuda_fail(e, "combine launch");
   n += 1;
   g_launches = n;
+  return MOE_OK;
+}
+
+// The layer for a few tokens: two kernels on the caller's stream.
+int forward_few_impl(const void* h, const float* Wr, const float* bias, const ExpertWeights& wt,
+                     const moe_dims_t* dims, float* out, int32_t* idx_out, float* w_out, void* ws,
+                     size_t ws_bytes, moe_stream_t stream) {
+  MOE_CHECK_PTR(out);
+  if (idx_out && !aligned16(idx_out)) return fail(MOE_ERR_INVALID_ARG, "idx_out is not 16-byte aligned");
+  if (w_out && !aligned16(w_out)) return fail(MOE_ERR_INVALID_ARG, "w_out is not 16-byte aligned");
+  Ws w;
+  int rc;
+  if ((rc = check_ws(dims, ws, ws_bytes, &w))) return rc;
+  if ((rc = check_device())) return rc;
+  const FewPlan L = few_plan(*dims, wt.fp8);
+  const size_t most = L.max_slots - dims->S;
+  FewArgs a{};
+  a.d = *dims;
+  a.h = static_cast<const uint16_t*>(h);
+  a.Wr = Wr;
+  a.bias = bias;
+  a.W1 = wt.W1; a.W3 = wt.W3; a.W2 = wt.W2;
+  a.Ws1 = wt.Ws1; a.Ws3 = wt.Ws3; a.Ws2 = wt.Ws2;
+  a.w8 = wt.fp8 ? &wt.f8 : nullptr;
+  a.out = out;
+  a.idx = idx_out ? idx_out : w.at<int32_t>(w.L.idx);
+  a.w = w_out ? w_out : w.at<float>(w.L.w);
+  a.logits = w.at<float>(w.L.partials);
+  int32_t* slots = w.at<int32_t>(w.L.f_slots);
+  a.nslots = slots;
+  a.slot_of = slots + 64;
+  a.slot_expert = a.slot_of + dims->T * dims->k;
+  a.slot_mask = w.at<uint32_t>(w.L.f_mask);
+  a.counts = w.at<int32_t>(w.L.counts);
+  a.touched = w.at<int32_t>(w.L.touched);
+  a.ticket = w.at<int32_t>(w.L.f_claim);
+  a.claim = a.ticket + 64;
+  a.hq = w.at<uint8_t>(w.L.f_hq);
+  a.hqe = w.at<int8_t>(w.L.f_hqe);
+  // chosen experts' activations first, then the shared experts'
+  a.a_r = w.at<uint8_t>(w.L.f_act);
+  a.a_s = a.a_r + align256(most * L.PA * dims->F * (wt.fp8 ? 1 : 2));
+  a.ae_r = w.at<int8_t>(w.L.f_exp);
+  a.ae_s = a.ae_r + most * L.TP * 4 * ((dims->F + 127) / 128);
+  a.planes = w.at<float>(w.L.f_planes);
+  a.status = w.status();
+  const char* why = "launch failed";
+  const cudaError_t e = launch_few(a, reinterpret_cast<cudaStream_t>(stream), &why);
+  if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "few-token layer: %s (%s)", why, cudaGetErrorString(e));
+  g_launches = 2;
+  return MOE_OK;
+}
+
+int check_few(const moe_dims_t* d) {
+  if (d->T > kFewMaxT)
+    return fail(MOE_ERR_UNSUPPORTED, "T = %d: at most %d tokens (moe_forward takes more)", d->T,
+                kFewMaxT);
   return MOE_OK;
 }
 
@@ -845,6 +927,39 @@ int moe_forward_fp8(const void* h, const float* Wr, const float* bias, const moe
   ExpertWeights wt;
   if ((rc = check_fp8_weights(w8, dims, &wt))) return rc;
   return forward_impl(h, Wr, bias, wt, dims, out, idx_out, w_out, ws, ws_bytes, stream);
+}
+
+int moe_forward_few(const void* h, const float* Wr, const float* bias, const void* W1,
+                    const void* W3, const void* W2, const void* Ws1, const void* Ws3,
+                    const void* Ws2, const moe_dims_t* dims, float* out, int32_t* idx_out,
+                    float* w_out, void* ws, size_t ws_bytes, moe_stream_t stream) {
+  int rc = begin(dims);
+  if (rc) return rc;
+  if ((rc = check_few(dims))) return rc;
+  if (dims->T == 0) return MOE_OK;
+  MOE_CHECK_PTR(h);
+  MOE_CHECK_PTR(Wr);
+  MOE_CHECK_PTR(bias);
+  ExpertWeights wt;
+  if ((rc = check_bf16_weights(W1, W3, W2, Ws1, Ws3, Ws2, dims, &wt))) return rc;
+  return forward_few_impl(h, Wr, bias, wt, dims, out, idx_out, w_out, ws, ws_bytes, stream);
+}
+
+int moe_forward_few_fp8(const void* h, const float* Wr, const float* bias,
+                        const moe_fp8_weights_t* w8, const moe_dims_t* dims, float* out,
+                        int32_t* idx_out, float* w_out, void* ws, size_t ws_bytes,
+                        moe_stream_t stream) {
+  int rc = begin(dims);
+  if (rc) return rc;
+  if ((rc = check_few(dims))) return rc;
+  if ((rc = check_fp8_dims(dims))) return rc;
+  if (dims->T == 0) return MOE_OK;
+  MOE_CHECK_PTR(h);
+  MOE_CHECK_PTR(Wr);
+  MOE_CHECK_PTR(bias);
+  ExpertWeights wt;
+  if ((rc = check_fp8_weights(w8, dims, &wt))) return rc;
+  return forward_few_impl(h, Wr, bias, wt, dims, out, idx_out, w_out, ws, ws_bytes, stream);
 }
 
 int moe_fp8_dequantize(const void* codes, const int8_t* exps, int G, int R, int K, void* out,

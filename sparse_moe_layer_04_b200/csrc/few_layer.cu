@@ -1,0 +1,1046 @@
+// The whole layer for a few tokens (T <= 16) in two kernels.
+//
+// With few tokens the layer is its weight stream: each chosen expert's three
+// matrices are read once and used for one or two tokens.  What can be lost is
+// time in which the stream stands still, so the second kernel is persistent
+// and one queue of tiles covers both expert products:
+//
+//   few_router_kernel   logits (fp32 FMAs), and in the block that finishes
+//                       last the selection, the weights and the list of
+//                       "slots": the shared experts, then the chosen experts
+//                       in increasing order.  FP8: the hidden rows are also
+//                       split into three E4M3 pieces here.
+//   few_ffn_kernel      tiles claimed in order from a counter:
+//     gate/up  (slot, up to 64 features): act = silu(W1 h) * (W3 h) for every
+//              token, kept for the tokens that chose the expert
+//     down     (slot, 128 output rows, part of K): y = W2 act, written to a
+//              plane of its own; whoever completes the last plane of 128
+//              output rows adds the planes in the order of moe_combine
+// The shared experts' gate/up tiles need no routing, so this kernel starts on
+// them while the first one runs (programmatic dependent launch).
+//
+// The weights are the M = 128 operand of the tensor core, straight from
+// memory by TMA, and the tokens the N operand: all T tokens against every
+// chosen expert, since 16 columns cost no more than one.  A column depends on
+// its own token alone, so what an expert computes for a token that did not
+// choose it is dropped, whatever it is.
+//
+// Precision.  bf16 weights: hidden rows enter as they are; an activation
+// enters as two bf16 pieces (its rounding and what that leaves, 16 bits
+// together), in columns of their own that the epilogue adds in fp32.  FP8
+// weights: the codes enter as they are, with their block exponents as the
+// tensor core's scales, and the other operand is a sum of E4M3 pieces, each
+// holding 4 bits of what the ones before it leave, with a scale 2^4 lower.  A
+// bf16 value has 8 bits, so two pieces hold it and a third reaches values far
+// below their block's largest (E4M3's subnormal step is 2^-17.8 of it: three
+// pieces leave 2^-25.8); four hold an activation to 2^-16 of itself.  The
+// pieces cost columns, not weight bytes.
+#include <algorithm>
+#include <climits>
+
+#include <cuda_bf16.h>
+
+#include "ffn_common.cuh"
+#include "fp8_convert.cuh"
+#include "route_order.cuh"
+#include "sm100_scaled.cuh"
+
+namespace moe {
+namespace {
+
+constexpr unsigned kAll = 0xffffffffu;
+constexpr int kRouterThreads = 512;
+constexpr int kRouterWarps = kRouterThreads / 32;
+constexpr int kRouterExperts = 4;        // experts per router block
+constexpr int kPiecesH = 3, kPiecesA = 4;
+constexpr int kPieceMinExp = -115;       // the last piece's exponent stays an E8M0 value
+
+// ---------------------------------------------------------------------------
+// kernel 1: router, selection, slots
+// ---------------------------------------------------------------------------
+struct FewRoute {
+  const uint16_t* h;
+  const float *Wr, *bias;
+  int T, D, E, k;
+  float scale;
+  float* logits;          // [T, E]
+  int32_t* idx;           // [T, k]
+  float* w;               // [T, k]
+  int32_t* slot_of;       // [T, k] chosen-expert slot of each pair, -1 for none
+  int32_t* slot_expert;   // [slots]
+  uint32_t* slot_mask;    // [slots] bit t: token t chose it
+  int32_t* nslots;        // chosen experts
+  int32_t* counts;        // [E] pairs per expert
+  int32_t* ticket;        // zero between calls
+  int* status;
+  int router_blocks;
+  // FP8: pieces of the hidden rows [kPiecesH * TP, D] and exponents [TP, KB]
+  uint8_t* hq;
+  int8_t* hqe;
+  int TP;
+};
+
+// Sums v[i] over the warp for all i: lane l ends with the sums of v[i] whose
+// index is congruent to it, in v[0 .. N/32 - 1] (N >= 32), or the sum of
+// v[l % N] in v[0] (N < 32).
+template <int N>
+__device__ __forceinline__ void warp_sums(float (&v)[N], int lane) {
+  int n = N;
+#pragma unroll
+  for (int off = 16; off; off >>= 1) {
+    if (n > 1) {
+      // keep the half of the values whose index matches this lane's bit
+      n >>= 1;
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i) {
+        if (i < n) {
+          const bool upper = lane & off;
+          const float send = upper ? v[i] : v[i + n];
+          const float keep = upper ? v[i + n] : v[i];
+          v[i] = keep + __shfl_xor_sync(kAll, send, off);
+        }
+      }
+    } else {
+      v[0] += __shfl_xor_sync(kAll, v[0], off);
+    }
+  }
+}
+
+// fp32 score of a logit, as moe_route computes it.
+__device__ __forceinline__ float score(float logit) {
+  return __double2float_rn(1.0 / (1.0 + exp(-(double)logit)));
+}
+
+// The pieces of one block of 128 (or 32) values held by a warp: piece p's
+// codes of each value, given the block's exponent.
+__device__ __forceinline__ uint32_t piece_code(float& rest, float inv, float unit) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.f), "f"(rest * inv));
+  const uint32_t code = r & 0xffu;
+  // value of the code, exactly: E4M3 -> f16 -> f32
+  uint32_t h2;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(r));
+  float val;
+  asm("{\n\t.reg .f16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.f32.f16 %0, a;\n\t}" : "=f"(val) : "r"(h2));
+  rest -= val * unit;
+  return code;
+}
+
+__device__ __forceinline__ float pow2f(int e) {   // e in [-126, 127]
+  return __uint_as_float((uint32_t)(e + 127) << 23);
+}
+
+// Smallest e >= kPieceMinExp with top <= 448 * 2^e (0 for a block of zeros).
+__device__ __forceinline__ int block_exp(float top) {
+  const uint32_t u = __float_as_uint(top);
+  if (u == 0) return 0;
+  // 448 = 1.75 * 2^8: one exponent more when the fraction exceeds 0.75
+  return max((int)((u + 0x1fffffu) >> 23) - 135, kPieceMinExp);
+}
+
+template <int TT>
+__device__ __forceinline__ void router_logits_block(const FewRoute& p, float* s_part) {
+  const int e0 = blockIdx.x * kRouterExperts;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float acc[kRouterExperts * TT];
+#pragma unroll
+  for (int i = 0; i < kRouterExperts * TT; ++i) acc[i] = 0.f;
+  for (int d = threadIdx.x * 4; d < p.D; d += kRouterThreads * 4) {
+    float4 wv[kRouterExperts];
+#pragma unroll
+    for (int i = 0; i < kRouterExperts; ++i)
+      wv[i] = e0 + i < p.E ? *reinterpret_cast<const float4*>(p.Wr + (size_t)(e0 + i) * p.D + d)
+                           : make_float4(0.f, 0.f, 0.f, 0.f);
+    uint2 hv[TT];
+#pragma unroll
+    for (int t = 0; t < TT; ++t)
+      hv[t] = t < p.T ? *reinterpret_cast<const uint2*>(p.h + (size_t)t * p.D + d)
+                      : make_uint2(0, 0);
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
+      const float a = __uint_as_float(hv[t].x << 16), b = __uint_as_float(hv[t].x & 0xffff0000u);
+      const float c = __uint_as_float(hv[t].y << 16), e = __uint_as_float(hv[t].y & 0xffff0000u);
+#pragma unroll
+      for (int i = 0; i < kRouterExperts; ++i) {
+        float& s = acc[t * kRouterExperts + i];
+        s = fmaf(a, wv[i].x, s);
+        s = fmaf(b, wv[i].y, s);
+        s = fmaf(c, wv[i].z, s);
+        s = fmaf(e, wv[i].w, s);
+      }
+    }
+  }
+  constexpr int N = kRouterExperts * TT;
+  warp_sums<N>(acc, lane);
+  // index of the sum a lane holds: its bits choose halves from the top down
+  constexpr int PER = N > 32 ? N / 32 : 1;
+  int at = 0;
+  {
+    int n = N;
+#pragma unroll
+    for (int off = 16; off; off >>= 1)
+      if (n > 1) {
+        n >>= 1;
+        if (lane & off) at += n;
+      }
+  }
+#pragma unroll
+  for (int i = 0; i < PER; ++i) s_part[warp * N + at + i] = acc[i];
+  __syncthreads();
+  for (int i = threadIdx.x; i < N; i += kRouterThreads) {
+    double v = 0.0;
+    for (int q = 0; q < kRouterWarps; ++q) v += (double)s_part[q * N + i];
+    const int t = i / kRouterExperts, e = e0 + i % kRouterExperts;
+    if (t < p.T && e < p.E) p.logits[(size_t)t * p.E + e] = (float)v;
+  }
+}
+
+// Selection for every token (a warp each), then the slots.  One block; s_ord
+// holds the keys' order [T][E].
+__device__ void select_and_list(const FewRoute& p, uint32_t* s_ord) {
+  __shared__ uint32_t s_mask[1024];
+  __shared__ int s_slot[1024];
+  __shared__ int s_cnt[32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int e = threadIdx.x; e < 1024; e += kRouterThreads) s_mask[e] = 0u;
+  bool bad = false;
+  for (int i = threadIdx.x; i < p.T * p.E; i += kRouterThreads) {
+    const float l = __ldcg(p.logits + i);
+    const float s = score(l);
+    const float key = __fadd_rn(s, p.bias[i % p.E]);
+    if (!isfinite(l) || !isfinite(key)) bad = true;
+    s_ord[i] = key_order(key);
+  }
+  if (__syncthreads_or(bad) && threadIdx.x == 0 && p.status) atomicOr(p.status, kStNonFinite);
+  const int t = warp;
+  int my_e = INT_MAX;
+  if (t < p.T) {
+    uint32_t* ord = s_ord + t * p.E;
+    float my_s = 0.f, sum = 0.f;
+    for (int j = 0; j < p.k; ++j) {
+      uint32_t bu = 0u;
+      int be = INT_MAX;
+      for (int e = lane; e < p.E; e += 32)
+        if (ord[e] > bu) {   // increasing e: ties keep the lower index
+          bu = ord[e];
+          be = e;
+        }
+      warp_best(bu, be);
+      // no key is left when some were NaN: the slot stays empty
+      const bool ok = bu != 0u;
+      const float s = ok ? score(__ldcg(p.logits + (size_t)t * p.E + be)) : 0.f;
+      __syncwarp();
+      if (ok && lane == 0) ord[be] = 0u;
+      __syncwarp();
+      if (lane == j && ok) {
+        my_e = be;
+        my_s = s;
+      }
+      sum = j == 0 ? s : __fadd_rn(sum, s);
+    }
+    if (lane < p.k) {
+      p.idx[t * p.k + lane] = my_e;
+      p.w[t * p.k + lane] = __fmul_rn(__fdiv_rn(my_s, sum), p.scale);
+      if (my_e != INT_MAX) atomicOr(&s_mask[my_e], 1u << t);
+    }
+  }
+  __syncthreads();
+  for (int g = warp; g < 32; g += kRouterWarps) {
+    const unsigned b = __ballot_sync(kAll, s_mask[g * 32 + lane] != 0u);
+    if (lane == 0) s_cnt[g] = __popc(b);
+  }
+  __syncthreads();
+  for (int g = warp; g < 32; g += kRouterWarps) {
+    const int e = g * 32 + lane;
+    const uint32_t m = s_mask[e];
+    const unsigned b = __ballot_sync(kAll, m != 0u);
+    int base = 0;
+    for (int q = 0; q < g; ++q) base += s_cnt[q];
+    const int slot = base + __popc(b & ((1u << lane) - 1u));
+    s_slot[e] = slot;
+    if (m) {
+      p.slot_expert[slot] = e;
+      p.slot_mask[slot] = m;
+    }
+    if (e < p.E) p.counts[e] = __popc(m);
+    if (g == 31 && lane == 31) *p.nslots = slot + (m != 0u);
+  }
+  __syncthreads();
+  if (t < p.T && lane < p.k) p.slot_of[t * p.k + lane] = my_e != INT_MAX ? s_slot[my_e] : -1;
+}
+
+// One warp: the three pieces of 128 columns of a hidden row.
+__device__ __forceinline__ void split_hidden(const FewRoute& p, int unit, int lane) {
+  const int KB = (p.D + 127) / 128;
+  const int t = unit / KB, kb = unit - t * KB;
+  const int col = kb * 128 + lane * 4;
+  uint2 raw = make_uint2(0, 0);
+  if (col < p.D) raw = *reinterpret_cast<const uint2*>(p.h + (size_t)t * p.D + col);
+  float v[4] = {__uint_as_float(raw.x << 16), __uint_as_float(raw.x & 0xffff0000u),
+                __uint_as_float(raw.y << 16), __uint_as_float(raw.y & 0xffff0000u)};
+  float top = 0.f;
+  bool odd[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    odd[i] = !isfinite(v[i]);
+    if (odd[i]) v[i] = 0.f;
+    top = fmaxf(top, fabsf(v[i]));
+  }
+  top = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(top)));
+  const int e = block_exp(top);
+  if (lane == 0) p.hqe[t * KB + kb] = (int8_t)e;
+#pragma unroll
+  for (int q = 0; q < kPiecesH; ++q) {
+    const float inv = pow2f(4 * q - e), unit2 = pow2f(e - 4 * q);
+    uint32_t c = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t code = piece_code(v[i], inv, unit2);
+      c |= (odd[i] ? 0x7fu : code) << (8 * i);
+    }
+    if (col < p.D) *reinterpret_cast<uint32_t*>(p.hq + (size_t)(q * p.TP + t) * p.D + col) = c;
+  }
+}
+
+template <int TT>
+__global__ void __launch_bounds__(kRouterThreads) few_router_kernel(const FewRoute p) {
+  extern __shared__ uint32_t s_dyn[];
+  ptx::pdl_wait();
+  // From here on everything before this call is complete and visible, which
+  // the next kernel relies on before its own wait: it must not be let go
+  // earlier.
+  ptx::pdl_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if ((int)blockIdx.x >= p.router_blocks) {
+    const int unit = ((int)blockIdx.x - p.router_blocks) * kRouterWarps + warp;
+    if (unit < p.T * ((p.D + 127) / 128)) split_hidden(p, unit, lane);
+    return;
+  }
+  router_logits_block<TT>(p, reinterpret_cast<float*>(s_dyn));
+  // the block that finishes last selects
+  __shared__ int s_last;
+  __syncthreads();
+  if (threadIdx.x == 0) s_last = ptx::atom_add_acq_rel_gpu(p.ticket, 1) == p.router_blocks - 1;
+  __syncthreads();
+  if (!s_last) return;
+  select_and_list(p, s_dyn);
+  if (threadIdx.x == 0) *p.ticket = 0;   // for the next call
+}
+
+// ---------------------------------------------------------------------------
+// kernel 2: both expert products and the merge
+// ---------------------------------------------------------------------------
+constexpr int kAStage = 128 * 128;       // 128 weight rows x 128 bytes of K
+constexpr int kBStage = 8192;
+constexpr int kAStages = 9, kBStages = 8;
+constexpr int kRing = kAStages * kAStage + kBStages * kBStage;
+constexpr int kAccCols = 64;             // one accumulator (N <= 64)
+constexpr int kSfSlot = 32;              // scale columns of one slot: 4 weights, 4 x 4 tokens
+constexpr uint32_t kTmemCols = 256;      // 2 accumulators + 2 scale slots
+constexpr int kQueue = 4;
+
+struct alignas(64) FewFfn {
+  CUtensorMap x;                         // hidden rows (bf16) or their pieces, box NX x 128 B
+  CUtensorMap act_r, act_s;              // activations [slots * PA, F], box PA x 128 B
+  CUtensorMap w1_r, w3_r, w1_s, w3_s;    // [E * F, D], box 16 rows
+  CUtensorMap w2_r, w2_s;                // [E * D, F], box 128 rows
+  const int8_t *e1_r, *e3_r, *e2_r, *e1_s, *e3_s, *e2_s;
+  int T, D, F, k, S, Fs;
+  int TP;                // token rows per piece
+  int NX, PA;            // token operand rows: gate/up, down
+  int fpt;               // features per gate/up tile (64, 32 or 16)
+  int sub;               // K-blocks per stage of a gate/up tile
+  int parts;             // K parts of a down unit
+  int nd;                // blocks of 128 output rows
+  int ntr, nts;          // gate/up tiles per chosen / shared slot
+  int max_slots;         // S + the most experts the call can choose
+  // routing (written by the first kernel)
+  const int32_t *idx, *slot_of, *slot_expert, *nslots;
+  const uint32_t* slot_mask;
+  const float* w;
+  const int8_t* hqe;     // FP8: exponents of the hidden rows [T, KB]
+  // activations, their exponents (FP8: one per 32 features, [slots, TP, 4 * KB])
+  uint8_t *a_r, *a_s;
+  int8_t *ae_r, *ae_s;
+  float* planes;         // [slot * parts + part][T][D]
+  float* out;
+  int32_t* claim;        // claim counter, exit ticket, then per-slot counts, then
+                         // per-output-block tickets; zero between calls
+  int32_t* touched;
+  int* status;
+};
+
+struct Unit {
+  int down;              // 0 gate/up, 1 down, -1 end
+  int slot;              // shared slots first
+  int at;                // first feature, or output block
+  int part;
+  int expert;            // row of the weight arrays
+};
+
+struct FewShared {
+  uint64_t a_full[kAStages], a_empty[kAStages];
+  uint64_t b_full[kBStages], b_empty[kBStages];
+  uint64_t sf_full[2], sf_empty[2];
+  uint64_t acc_full[2], acc_empty[2];
+  uint64_t q_full[kQueue], q_empty[kQueue];
+  uint64_t drain;
+  Unit q[kQueue];
+  uint32_t tmem_base;
+  int abort, bad, last, exit_last;
+  float act[64 * 17];    // FP8: activations of a tile [feature][token]
+};
+
+constexpr int few_smem() { return 1024 + kRing + (int)sizeof(FewShared); }
+
+// The tile queue seen by one consuming warp.
+struct QueueReader {
+  int slot = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ bool next(FewShared& ss, Unit& u, volatile int* abort, int lane) {
+    if (__any_sync(kAll, !ptx::mbar_wait(&ss.q_full[slot], phase, abort))) return false;
+    const volatile Unit& q = ss.q[slot];
+    u.down = q.down; u.slot = q.slot; u.at = q.at; u.part = q.part; u.expert = q.expert;
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive_after_reads(&ss.q_empty[slot]);
+    if (++slot == kQueue) { slot = 0; phase ^= 1u; }
+    return u.down >= 0;
+  }
+};
+
+// K-blocks [k0, k1) of a unit, of EB elements each.
+template <int EB>
+__device__ __forceinline__ void unit_k(const FewFfn& p, const Unit& u, int* k0, int* k1) {
+  if (u.down) {
+    const int kb = ((u.slot < p.S ? p.Fs : p.F) + EB - 1) / EB;
+    *k0 = kb * u.part / p.parts;
+    *k1 = kb * (u.part + 1) / p.parts;
+  } else {
+    *k0 = 0;
+    *k1 = (p.D + EB - 1) / EB;
+  }
+}
+
+__device__ __forceinline__ int32_t* slot_count(const FewFfn& p, int slot) { return p.claim + 2 + slot; }
+__device__ __forceinline__ int32_t* out_ticket(const FewFfn& p, int d) {
+  return p.claim + 2 + p.max_slots + d;
+}
+// Arrivals after which a slot's activations are complete: four epilogue warps a tile.
+__device__ __forceinline__ int slot_target(const FewFfn& p, int slot) {
+  return 4 * (slot < p.S ? p.nts : p.ntr);
+}
+
+// Barrier of the four epilogue warps alone.
+__device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+// Waits, whole warp, until a slot's activations are stored; every lane acquires.
+__device__ __forceinline__ bool slot_wait(const FewFfn& p, int slot, volatile int* abort) {
+  return !__any_sync(kAll, !ptx::counter_wait(slot_count(p, slot), slot_target(p, slot), abort));
+}
+
+// Four E8M0 bytes from exponents q[0 .. n-1] (n >= 1, the others count as 0);
+// outside [lo, hi] raises *bad.
+__device__ __forceinline__ uint32_t scale_word(const int8_t* q, int n, bool check, bool* bad) {
+  uint32_t w = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (i < n) w |= (uint32_t)(uint8_t)q[i] << (8 * i);
+  if (check)
+    *bad |= (__vcmpgts4(w, 0x07070707u) | __vcmplts4(w, 0x8b8b8b8bu)) != 0;
+  return __vadd4(w, 0x7f7f7f7fu);
+}
+
+template <bool FP8>
+__global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __grid_constant__ FewFfn p) {
+  constexpr int EB = FP8 ? 128 : 64;     // K elements of 128 bytes
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = ptx::smem_addr(smem_raw);
+  // the token ring follows the weight ring, so a product that reads 128 rows
+  // of a smaller tile stays inside the rings
+  uint8_t* ring_a = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+  uint8_t* ring_b = ring_a + kAStages * kAStage;
+  FewShared& ss = *reinterpret_cast<FewShared*>(ring_a + kRing);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (warp == 2) {
+    ptx::tmem_alloc(&ss.tmem_base, kTmemCols);
+    ptx::tmem_relinquish();
+  }
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kAStages; ++i) { ptx::mbar_init(&ss.a_full[i], 1); ptx::mbar_init(&ss.a_empty[i], 1); }
+    for (int i = 0; i < kBStages; ++i) { ptx::mbar_init(&ss.b_full[i], 1); ptx::mbar_init(&ss.b_empty[i], 1); }
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(&ss.sf_full[i], 4);
+      ptx::mbar_init(&ss.sf_empty[i], 1);
+      ptx::mbar_init(&ss.acc_full[i], 1);
+      ptx::mbar_init(&ss.acc_empty[i], 4);
+    }
+    for (int i = 0; i < kQueue; ++i) {
+      ptx::mbar_init(&ss.q_full[i], 1);
+      ptx::mbar_init(&ss.q_empty[i], 1 + 1 + 4 + (FP8 ? 4 : 0));
+    }
+    ptx::mbar_init(&ss.drain, 1);
+    ss.abort = 0;
+    ss.bad = 0;
+    ptx::fence_barrier_init();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = ss.tmem_base;
+  volatile int* abort = &ss.abort;
+  const int shared_tiles = p.S * p.nts;
+
+  if (warp == 0) {
+    // ---------------- weight producer and tile claimer ----------------
+    if (ptx::elect_one()) {
+      const uint64_t policy = ptx::l2_policy_evict_first();
+      int stage = 0, qs = 0, routed = -1;
+      uint32_t phase = 0, qphase = 0, issued = 0, parity = 0;
+      int tile = atomicAdd(p.claim, 1);
+      for (;;) {
+        Unit u{0, 0, 0, 0, 0};
+        if (tile < shared_tiles) {
+          u.slot = tile / p.nts;
+          u.at = (tile - u.slot * p.nts) * p.fpt;
+          u.expert = u.slot;
+        } else {
+          if (routed < 0) {
+            ptx::pdl_wait();             // the list of chosen experts
+            routed = __ldcg(p.nslots);
+          }
+          int r = tile - shared_tiles;
+          if (r < routed * p.ntr) {
+            const int s = r / p.ntr;
+            u.slot = p.S + s;
+            u.at = (r - s * p.ntr) * p.fpt;
+          } else {
+            r -= routed * p.ntr;
+            const int per = p.nd * p.parts;
+            u.slot = r / per;
+            u.down = u.slot < p.S + routed ? 1 : -1;
+            r -= u.slot * per;
+            u.part = r / p.nd;
+            u.at = r - u.part * p.nd;
+          }
+          if (u.down >= 0)
+            u.expert = u.slot < p.S ? u.slot : __ldcg(p.slot_expert + u.slot - p.S);
+        }
+        if (!ptx::mbar_wait(&ss.q_empty[qs], qphase ^ 1u, abort)) break;
+        ss.q[qs] = u;
+        ptx::mbar_arrive(&ss.q_full[qs]);
+        if (++qs == kQueue) { qs = 0; qphase ^= 1u; }
+        if (u.down < 0) break;
+        const int next = atomicAdd(p.claim, 1);   // its latency hides under this tile
+        const bool sh = u.slot < p.S;
+        int k0, k1;
+        unit_k<EB>(p, u, &k0, &k1);
+        bool ok = true;
+        if (u.down) {
+          const CUtensorMap* m = sh ? &p.w2_s : &p.w2_r;
+          const int row = u.expert * p.D + u.at * 128;
+          for (int kb = k0; kb < k1; ++kb) {
+            if (!ptx::mbar_wait(&ss.a_empty[stage], phase ^ 1u, abort)) { ok = false; break; }
+            ptx::mbar_arrive_expect_tx(&ss.a_full[stage], kAStage);
+            ptx::tma_load_2d_hint(ring_a + stage * kAStage, m, &ss.a_full[stage], kb * EB, row, policy);
+            issued |= 1u << stage;
+            parity = (parity & ~(1u << stage)) | (phase << stage);
+            if (++stage == kAStages) { stage = 0; phase ^= 1u; }
+          }
+        } else {
+          const CUtensorMap* m1 = sh ? &p.w1_s : &p.w1_r;
+          const CUtensorMap* m3 = sh ? &p.w3_s : &p.w3_r;
+          const int row = u.expert * (sh ? p.Fs : p.F) + u.at;
+          const int boxes = p.fpt / 16;
+          for (int kb = k0; kb < k1; kb += p.sub) {
+            if (!ptx::mbar_wait(&ss.a_empty[stage], phase ^ 1u, abort)) { ok = false; break; }
+            const int n = min(p.sub, k1 - kb);
+            ptx::mbar_arrive_expect_tx(&ss.a_full[stage], n * boxes * 4096);
+            uint8_t* dst = ring_a + stage * kAStage;
+            for (int i = 0; i < n; ++i)
+              for (int j = 0; j < boxes; ++j, dst += 4096) {
+                ptx::tma_load_2d_hint(dst, m1, &ss.a_full[stage], (kb + i) * EB, row + j * 16, policy);
+                ptx::tma_load_2d_hint(dst + 2048, m3, &ss.a_full[stage], (kb + i) * EB, row + j * 16, policy);
+              }
+            issued |= 1u << stage;
+            parity = (parity & ~(1u << stage)) | (phase << stage);
+            if (++stage == kAStages) { stage = 0; phase ^= 1u; }
+          }
+        }
+        if (!ok) break;
+        tile = next;
+      }
+      for (int s = 0; s < kAStages; ++s)
+        if (issued & (1u << s)) ffn::wait_drain(&ss.a_full[s], (parity >> s) & 1u, abort);
+    }
+  } else if (warp == 1) {
+    // ---------------- token / activation producer ----------------
+    QueueReader q;
+    Unit u;
+    bool waited = false;
+    int stage = 0;
+    uint32_t phase = 0, issued = 0, parity = 0;
+    while (q.next(ss, u, abort, lane)) {
+      const bool sh = u.slot < p.S;
+      if (!waited && (FP8 || u.down || !sh)) {
+        ptx::pdl_wait();
+        waited = true;
+      }
+      if (u.down) {
+        if (!slot_wait(p, u.slot, abort)) break;
+        ptx::fence_proxy_async_global();
+      }
+      int k0, k1;
+      unit_k<EB>(p, u, &k0, &k1);
+      const CUtensorMap* m = u.down ? (sh ? &p.act_s : &p.act_r) : &p.x;
+      const int row = u.down ? (sh ? u.slot : u.slot - p.S) * p.PA : 0;
+      const int bytes = (u.down ? p.PA : p.NX) * 128;
+      const int sub = u.down ? 1 : p.sub;
+      bool ok = true;
+      if (ptx::elect_one()) {
+        for (int kb = k0; kb < k1; kb += sub) {
+          if (!ptx::mbar_wait(&ss.b_empty[stage], phase ^ 1u, abort)) { ok = false; break; }
+          const int n = min(sub, k1 - kb);
+          ptx::mbar_arrive_expect_tx(&ss.b_full[stage], n * bytes);
+          for (int i = 0; i < n; ++i)
+            ptx::tma_load_2d(ring_b + stage * kBStage + i * bytes, m, &ss.b_full[stage],
+                             (kb + i) * EB, row);
+          issued |= 1u << stage;
+          parity = (parity & ~(1u << stage)) | (phase << stage);
+          if (++stage == kBStages) { stage = 0; phase ^= 1u; }
+        }
+      }
+      if (__any_sync(kAll, !ok)) break;
+    }
+    if (issued)
+      for (int s = 0; s < kBStages; ++s)
+        if (issued & (1u << s)) ffn::wait_drain(&ss.b_full[s], (parity >> s) & 1u, abort);
+  } else if (warp == 2) {
+    // ---------------- MMA issuer ----------------
+    QueueReader q;
+    Unit u;
+    int as = 0, bs = 0, buf = 0, slot = 0;
+    uint32_t aph = 0, bph = 0, cph = 0, sph = 0;
+    while (q.next(ss, u, abort, lane)) {
+      int k0, k1;
+      unit_k<EB>(p, u, &k0, &k1);
+      const int sub = u.down ? 1 : p.sub;
+      const int n = u.down ? p.PA : p.NX;
+      const uint32_t idesc = FP8 ? ptx::idesc_mxf8(128, n) : ptx::idesc_bf16_f32(128, n);
+      const int a_bytes = u.down ? kAStage : p.fpt * 2 * 128;
+      const int b_bytes = n * 128;
+      bool ok = true;
+      if (ptx::elect_one()) {
+        ok = ptx::mbar_wait(&ss.acc_empty[buf], cph ^ 1u, abort);
+        const uint32_t acc = tmem + buf * kAccCols;
+        for (int kb = k0; ok && kb < k1; kb += sub) {
+          if (!ptx::mbar_wait(&ss.b_full[bs], bph, abort)) { ok = false; break; }
+          if (!ptx::mbar_wait(&ss.a_full[as], aph, abort)) { ok = false; break; }
+          const int m = min(sub, k1 - kb);
+          uint32_t sa = ptx::smem_addr(ring_a + as * kAStage);
+          uint32_t sb = ptx::smem_addr(ring_b + bs * kBStage);
+          for (int i = 0; i < m; ++i, sa += a_bytes, sb += b_bytes) {
+            const int kk = kb + i;
+            if (FP8 && (kk == k0 || (kk & 3) == 0) &&
+                !ptx::mbar_wait(&ss.sf_full[slot], sph, abort)) { ok = false; break; }
+            ptx::tc_fence_after();
+            const uint64_t da = ptx::smem_desc_sw128(sa), db = ptx::smem_desc_sw128(sb);
+            if (FP8) {
+              const uint32_t sfa = tmem + 2 * kAccCols + slot * kSfSlot;
+              // gate/up: one word per row covers four K-blocks; down: one word per
+              // row and K-block covers its four steps of 32
+              const uint32_t sfb = sfa + 4 + (u.down ? (kk & 3) * 4 : 0);
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                ptx::mma_mxf8_ss(acc, da + 2 * k, db + 2 * k,
+                                 idesc | ptx::idesc_sf_byte(kk & 3, u.down ? k : kk & 3), sfa, sfb,
+                                 kk > k0 || k > 0);
+              if ((kk & 3) == 3 || kk == k1 - 1) {
+                ptx::mma_commit(&ss.sf_empty[slot]);
+                if (++slot == 2) { slot = 0; sph ^= 1u; }
+              }
+            } else {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                ptx::mma_f16_ss(acc, da + 2 * k, db + 2 * k, idesc, kk > k0 || k > 0);
+            }
+          }
+          if (!ok) break;
+          ptx::mma_commit(&ss.a_empty[as]);
+          ptx::mma_commit(&ss.b_empty[bs]);
+          if (++as == kAStages) { as = 0; aph ^= 1u; }
+          if (++bs == kBStages) { bs = 0; bph ^= 1u; }
+        }
+        if (ok) ptx::mma_commit(&ss.acc_full[buf]);
+      }
+      if (++buf == 2) { buf = 0; cph ^= 1u; }
+      if (__any_sync(kAll, !ok)) break;
+    }
+    // nothing of this CTA is in flight when its tensor memory is freed
+    if (ptx::elect_one()) {
+      ptx::mma_commit(&ss.drain);
+      ffn::wait_drain(&ss.drain, 0, abort);
+    }
+  } else if (warp >= 4 && warp < 8) {
+    // ---------------- epilogue ----------------
+    const int qt = warp & 3;
+    const uint32_t lanes = (uint32_t)(qt * 32) << 16;
+    QueueReader q;
+    Unit u;
+    bool waited = false;
+    int buf = 0;
+    uint32_t cph = 0;
+    while (q.next(ss, u, abort, lane)) {
+      const bool sh = u.slot < p.S;
+      if (!waited && (u.down || !sh)) {
+        ptx::pdl_wait();
+        waited = true;
+      }
+      const uint32_t mask = sh ? (1u << p.T) - 1u : __ldcg(p.slot_mask + u.slot - p.S);
+      int k0, k1;
+      unit_k<EB>(p, u, &k0, &k1);
+      if (__any_sync(kAll, !ptx::mbar_wait(&ss.acc_full[buf], cph, abort))) break;
+      ptx::tc_fence_after();
+      const uint32_t acc = tmem + buf * kAccCols + lanes;
+      // the token columns, pieces added: v[t] is this lane's weight row
+      const int pieces = u.down ? (FP8 ? kPiecesA : 2) : (FP8 ? kPiecesH : 1);
+      const bool rows = u.down || qt * 16 < p.fpt;   // this warp's rows belong to the tile
+      float v[16];
+#pragma unroll
+      for (int t = 0; t < 16; ++t) v[t] = 0.f;
+      if (rows && k1 > k0) {
+        // smallest piece first
+        for (int c = pieces - 1; c >= 0; --c) {
+          uint32_t r[16];
+          ptx::tmem_ld_x16(acc + c * p.TP, r);
+          ptx::tmem_wait_ld();
+#pragma unroll
+          for (int t = 0; t < 16; ++t) v[t] += __uint_as_float(r[t]);
+        }
+      }
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&ss.acc_empty[buf]);
+      if (++buf == 2) { buf = 0; cph ^= 1u; }
+
+      if (!u.down) {
+        const int F = sh ? p.Fs : p.F;
+        const bool up = lane >= 16;
+        const int f = u.at + qt * 16 + (lane & 15);
+        const size_t row0 = (size_t)(sh ? u.slot : u.slot - p.S) * p.PA;
+        // lanes 0-15 finish the even tokens, lanes 16-31 the odd ones
+#pragma unroll
+        for (int t = 0; t < 16; t += 2) {
+          const float got = __shfl_xor_sync(kAll, up ? v[t] : v[t + 1], 16);
+          const float gate = up ? got : v[t], mul = up ? v[t + 1] : got;
+          const float a = f < F ? gate / (1.0f + expf(-gate)) * mul : 0.f;
+          const int tt = t + (up ? 1 : 0);
+          if (FP8) {
+            ss.act[(qt * 16 + (lane & 15)) * 17 + tt] = a;
+          } else if (rows && f < F && ((mask >> tt) & 1u)) {
+            const __nv_bfloat16 hi = __float2bfloat16_rn(a);
+            const float hf = __bfloat162float(hi);
+            __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(sh ? p.a_s : p.a_r) +
+                                 (row0 + tt) * F + f;
+            dst[0] = hi;
+            dst[(size_t)p.TP * F] = __float2bfloat16_rn(isfinite(hf) ? a - hf : 0.f);
+          }
+        }
+        if (FP8) {
+          // 32 features of a token per warp and round: exponent, then the pieces
+          epi_sync();
+          int8_t* ae = sh ? p.ae_s : p.ae_r;
+          const int stride = (F + 127) / 128 * 4;   // exponents of a row
+          for (int i = qt; i < p.T * (p.fpt / 32); i += 4) {
+            const int t = i % p.T, b = i / p.T;
+            if (!((mask >> t) & 1u)) continue;
+            float a = ss.act[(b * 32 + lane) * 17 + t];
+            const bool odd = !isfinite(a);
+            if (odd) a = 0.f;
+            const float top = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(fabsf(a))));
+            const int e = block_exp(top);
+            const int fb = u.at + b * 32;
+            if (fb >= F) continue;
+            if (lane == 0)
+              ae[((size_t)(sh ? u.slot : u.slot - p.S) * p.TP + t) * stride + fb / 32] = (int8_t)e;
+            uint8_t* dst = (sh ? p.a_s : p.a_r) + (row0 + t) * F + fb + lane;
+#pragma unroll
+            for (int c = 0; c < kPiecesA; ++c) {
+              const uint32_t code = piece_code(a, pow2f(4 * c - e), pow2f(e - 4 * c));
+              if (fb + lane < F) dst[(size_t)c * p.TP * F] = (uint8_t)(odd ? 0x7fu : code);
+            }
+          }
+          epi_sync();   // the tile's activations are read: the next may be written
+        }
+        // the stores become visible to the whole GPU and to TMA, then the count
+        ptx::fence_proxy_async_global();
+        __threadfence();
+        __syncwarp();
+        if (lane == 0) atomicAdd(slot_count(p, u.slot), 1);
+      } else {
+        const int d = u.at * 128 + qt * 32 + lane;
+        float* plane = p.planes + (size_t)(u.slot * p.parts + u.part) * p.T * p.D + d;
+        if (d < p.D) {
+#pragma unroll
+          for (int t = 0; t < 16; ++t)
+            if ((mask >> t) & 1u) plane[(size_t)t * p.D] = v[t];
+        }
+        __threadfence();
+        epi_sync();
+        if (qt == 0 && lane == 0) {
+          const int all = (p.S + __ldcg(p.nslots)) * p.parts;
+          const int got = ptx::atom_add_acq_rel_gpu(out_ticket(p, u.at), 1);
+          ss.last = got == all - 1;
+          if (ss.last) *out_ticket(p, u.at) = 0;
+        }
+        epi_sync();
+        if (ss.last) {
+          __threadfence();
+          // moe_combine's order: shared experts, then the token's choices
+          if (d < p.D) {
+            const size_t ps = (size_t)p.T * p.D;
+            for (int t = 0; t < p.T; ++t) {
+              const float* src = p.planes + (size_t)t * p.D + d;
+              float o = 0.f;
+              for (int i = 0; i < p.S * p.parts; ++i) o += __ldcg(src + i * ps);
+              for (int j = 0; j < p.k; ++j) {
+                const int s = __ldcg(p.slot_of + t * p.k + j);
+                if (s < 0) continue;
+                float y = 0.f;
+                for (int i = 0; i < p.parts; ++i)
+                  y += __ldcg(src + ((size_t)(p.S + s) * p.parts + i) * ps);
+                o = fmaf(__ldcg(p.w + t * p.k + j), y, o);
+              }
+              p.out[(size_t)t * p.D + d] = o;
+            }
+          }
+        }
+      }
+    }
+  } else if (FP8 && warp >= 8) {
+    // ---------------- scale writers ----------------
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const int KBD = (p.D + 127) / 128;
+    QueueReader q;
+    Unit u;
+    bool waited = false, bad = false;
+    int slot = 0;
+    uint32_t sph = 0;
+    while (q.next(ss, u, abort, lane)) {
+      if (!waited) {
+        ptx::pdl_wait();
+        waited = true;
+      }
+      const bool sh = u.slot < p.S;
+      const int F = sh ? p.Fs : p.F, KBF = (F + 127) / 128;
+      if (u.down && !slot_wait(p, u.slot, abort)) break;
+      int k0, k1;
+      unit_k<EB>(p, u, &k0, &k1);
+      const int8_t* we;
+      const int KB = u.down ? KBF : KBD;
+      if (u.down) {
+        we = (sh ? p.e2_s : p.e2_r) + ((size_t)u.expert * KBD + u.at) * KB;
+      } else {
+        we = (lane & 16 ? (sh ? p.e3_s : p.e3_r) : (sh ? p.e1_s : p.e1_r)) +
+             ((size_t)u.expert * KBF + u.at / 128) * KB;
+      }
+      const int8_t* ae = (sh ? p.ae_s : p.ae_r) +
+                         (size_t)(sh ? u.slot : u.slot - p.S) * p.TP * (KBF * 4);
+      bool ok = true;
+      for (int s = k0 / 4; s * 4 < k1; ++s) {
+        uint32_t wa[4], wx[4][2];
+        wa[0] = wa[1] = wa[2] = wa[3] = scale_word(we + 4 * s, KB - 4 * s, true, &bad);
+        // token words: gate/up, one per row (the bytes are K-blocks); down, one
+        // per row and K-block (the bytes are its steps of 32); N <= 64 rows
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int row = j * 32 + lane, c = row / p.TP, t = row - c * p.TP;
+            wx[i][j] = 0x7f7f7f7fu;      // rows of no token: any valid scale
+            if (t >= p.T || c >= (u.down ? kPiecesA : kPiecesH)) continue;
+            if (!u.down) {
+              if (i == 0) wx[i][j] = scale_word(p.hqe + t * KBD + 4 * s, KBD - 4 * s, false, &bad);
+            } else if (4 * s + i < KBF) {
+              // exponents past the last feature count as 0 (their codes are zero)
+              const int kb = 4 * s + i;
+              wx[i][j] = scale_word(ae + (size_t)t * (KBF * 4) + 4 * kb, (F + 31) / 32 - 4 * kb,
+                                    false, &bad);
+            }
+            wx[i][j] = __vsub4(wx[i][j], 0x04040404u * c);
+          }
+        }
+        if (__any_sync(kAll, !ptx::mbar_wait(&ss.sf_empty[slot], sph ^ 1u, abort))) { ok = false; break; }
+        ptx::tc_fence_after();
+        const uint32_t dst = tmem + 2 * kAccCols + slot * kSfSlot + lanes;
+        ptx::tmem_st_x4(dst, wa);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (i == 0 || u.down) ptx::tmem_st_x2(dst + 4 + 4 * i, wx[i][0], wx[i][1]);
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&ss.sf_full[slot]);
+        if (++slot == 2) { slot = 0; sph ^= 1u; }
+      }
+      if (!ok) break;
+    }
+    if (bad) ss.bad = 1;
+  }
+
+  __syncthreads();
+  if (warp == 2) ptx::tmem_dealloc(tmem, kTmemCols);
+  ptx::pdl_launch_dependents();
+  if (threadIdx.x == 0) {
+    if (p.status) {
+      if (ss.abort) atomicOr(p.status, kStTimeout);
+      if (ss.bad) atomicOr(p.status, kStBounds);
+    }
+    // the last CTA leaves the claim counter and the slot counts zero
+    __threadfence();
+    ss.exit_last = atomicAdd(p.claim + 1, 1) == (int)gridDim.x - 1;
+  }
+  __syncthreads();
+  if (ss.exit_last) {
+    __threadfence();
+    for (int i = threadIdx.x; i < p.max_slots; i += blockDim.x) *slot_count(p, i) = 0;
+    if (threadIdx.x == 0) {
+      *p.touched = __ldcg(p.nslots);
+      p.claim[0] = 0;
+      p.claim[1] = 0;
+    }
+  }
+}
+
+template <int TT>
+cudaError_t launch_few_router(const FewRoute& r, int blocks, cudaStream_t st) {
+  const int part = kRouterWarps * kRouterExperts * TT * 4;
+  const int keys = r.T * r.E * 4;
+  static std::atomic<uint64_t> smem_set{0};
+  const cudaError_t e = set_smem_once(few_router_kernel<TT>, std::max(part, kFewMaxT * 1024 * 4), smem_set);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(few_router_kernel<TT>, dim3(blocks), dim3(kRouterThreads),
+                    (size_t)std::max(part, keys), st, r);
+}
+
+}  // namespace
+
+// How a call is cut into tiles.
+FewPlan few_plan(const moe_dims_t& d, bool fp8) {
+  FewPlan L{};
+  L.TP = fp8 ? (d.T <= 4 ? 4 : d.T <= 8 ? 8 : 16) : (d.T <= 8 ? 8 : 16);
+  L.NX = fp8 ? (kPiecesH * L.TP + 15) / 16 * 16 : 16;
+  L.PA = (fp8 ? kPiecesA : 2) * L.TP;
+  const int most = std::min(d.E, d.T * d.k);     // chosen experts at most
+  L.max_slots = d.S + most;
+  const int Fs = d.S > 0 ? d.Fs : 0;
+  auto tiles = [&](int fpt) {
+    return (long long)d.S * ((Fs + fpt - 1) / fpt) + (long long)most * ((d.F + fpt - 1) / fpt);
+  };
+  // Features per gate/up tile: 64 fill the 128 weight rows of a product.  When
+  // that leaves fewer than two tiles per SM, 32 (and with bf16 weights 16)
+  // spread the weight stream over more SMs; the rows they leave unused cost
+  // tensor time that the stream does not need.
+  L.fpt = 64;
+  while (L.fpt > (fp8 ? 32 : 16) && tiles(L.fpt) < 2 * kSplitTargetBlocks) L.fpt /= 2;
+  // K-blocks per stage: the stage stays 16 KB of weights, within the token stage
+  L.sub = std::max(1, std::min(64 / L.fpt, kBStage / (L.NX * 128)));
+  if (L.sub == 3) L.sub = 2;
+  L.nd = (d.D + 127) / 128;
+  const int eb = fp8 ? 128 : 64;
+  const int kb = std::min((d.F + eb - 1) / eb, d.S > 0 ? (Fs + eb - 1) / eb : 1 << 30);
+  // K parts of a down unit: until there are six units per SM or a part has
+  // fewer than four K-blocks
+  L.parts = 1;
+  while (L.parts < 8 && (long long)L.nd * L.parts * L.max_slots < 6 * kSplitTargetBlocks &&
+         kb >= 8 * L.parts)
+    L.parts *= 2;
+  return L;
+}
+
+cudaError_t launch_few(const FewArgs& a, cudaStream_t st, const char** why) {
+  const moe_dims_t& d = a.d;
+  const bool fp8 = a.w8 != nullptr;
+  const FewPlan L = few_plan(d, fp8);
+  const int Fs = d.S > 0 ? d.Fs : 0;
+
+  FewRoute r{};
+  r.h = a.h; r.Wr = a.Wr; r.bias = a.bias;
+  r.T = d.T; r.D = d.D; r.E = d.E; r.k = d.k; r.scale = d.scale;
+  r.logits = a.logits;
+  r.idx = a.idx; r.w = a.w;
+  r.slot_of = a.slot_of; r.slot_expert = a.slot_expert; r.slot_mask = a.slot_mask;
+  r.nslots = a.nslots; r.counts = a.counts;
+  r.ticket = a.ticket;
+  r.status = a.status;
+  r.router_blocks = (d.E + kRouterExperts - 1) / kRouterExperts;
+  r.hq = a.hq; r.hqe = a.hqe; r.TP = L.TP;
+  const int units = fp8 ? d.T * ((d.D + 127) / 128) : 0;
+  const int blocks = r.router_blocks + (units + kRouterWarps - 1) / kRouterWarps;
+
+  FewFfn f{};
+  const int es = fp8 ? 1 : 2, eb = 128 / es;
+  const void *W1 = fp8 ? (const void*)a.w8->W1 : a.W1, *W3 = fp8 ? (const void*)a.w8->W3 : a.W3;
+  const void *W2 = fp8 ? (const void*)a.w8->W2 : a.W2;
+  const void *S1 = fp8 ? (const void*)a.w8->Ws1 : a.Ws1, *S3 = fp8 ? (const void*)a.w8->Ws3 : a.Ws3;
+  const void *S2 = fp8 ? (const void*)a.w8->Ws2 : a.Ws2;
+  auto map = [&](CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint32_t box) {
+    return make_tensor_map(m, base, rows, cols, box, eb, es, 128);
+  };
+  const int most = L.max_slots - d.S;
+  bool ok = (fp8 ? map(&f.x, a.hq, kPiecesH * L.TP, d.D, L.NX) : map(&f.x, a.h, d.T, d.D, L.NX)) &&
+            map(&f.act_r, a.a_r, (uint64_t)most * L.PA, d.F, L.PA) &&
+            map(&f.w1_r, W1, (uint64_t)d.E * d.F, d.D, 16) &&
+            map(&f.w3_r, W3, (uint64_t)d.E * d.F, d.D, 16) &&
+            map(&f.w2_r, W2, (uint64_t)d.E * d.D, d.F, 128);
+  f.act_s = f.act_r; f.w1_s = f.w1_r; f.w3_s = f.w3_r; f.w2_s = f.w2_r;
+  if (ok && d.S > 0)
+    ok = map(&f.act_s, a.a_s, (uint64_t)d.S * L.PA, Fs, L.PA) &&
+         map(&f.w1_s, S1, (uint64_t)d.S * Fs, d.D, 16) &&
+         map(&f.w3_s, S3, (uint64_t)d.S * Fs, d.D, 16) &&
+         map(&f.w2_s, S2, (uint64_t)d.S * d.D, Fs, 128);
+  if (!ok) {
+    *why = "cuTensorMapEncodeTiled failed for an expert operand";
+    return cudaErrorInvalidValue;
+  }
+  if (fp8) {
+    f.e1_r = a.w8->W1e; f.e3_r = a.w8->W3e; f.e2_r = a.w8->W2e;
+    f.e1_s = a.w8->Ws1e; f.e3_s = a.w8->Ws3e; f.e2_s = a.w8->Ws2e;
+  }
+  f.T = d.T; f.D = d.D; f.F = d.F; f.k = d.k; f.S = d.S; f.Fs = Fs;
+  f.TP = L.TP; f.NX = L.NX; f.PA = L.PA;
+  f.fpt = L.fpt; f.sub = L.sub; f.parts = L.parts; f.nd = L.nd;
+  f.ntr = (d.F + L.fpt - 1) / L.fpt;
+  f.nts = (Fs + L.fpt - 1) / L.fpt;
+  f.max_slots = L.max_slots;
+  f.idx = a.idx; f.slot_of = a.slot_of; f.slot_expert = a.slot_expert; f.nslots = a.nslots;
+  f.slot_mask = a.slot_mask;
+  f.w = a.w;
+  f.hqe = a.hqe;
+  f.a_r = a.a_r; f.a_s = a.a_s; f.ae_r = a.ae_r; f.ae_s = a.ae_s;
+  f.planes = a.planes;
+  f.out = a.out;
+  f.claim = a.claim;
+  f.touched = a.touched;
+  f.status = a.status;
+
+  *why = "router launch";
+  cudaError_t e = d.T <= 1   ? launch_few_router<1>(r, blocks, st)
+                  : d.T <= 2 ? launch_few_router<2>(r, blocks, st)
+                  : d.T <= 4 ? launch_few_router<4>(r, blocks, st)
+                  : d.T <= 8 ? launch_few_router<8>(r, blocks, st)
+                             : launch_few_router<16>(r, blocks, st);
+  if (e != cudaSuccess) return e;
+  *why = "expert launch";
+  static std::atomic<uint64_t> set16{0}, set8{0};
+  e = fp8 ? set_smem_once(few_ffn_kernel<true>, few_smem(), set8)
+          : set_smem_once(few_ffn_kernel<false>, few_smem(), set16);
+  if (e != cudaSuccess) return e;
+  const long long gu = (long long)d.S * f.nts + (long long)most * f.ntr;
+  const long long dn = (long long)L.max_slots * L.nd * L.parts;
+  const int grid = (int)std::min<long long>(num_sms(), gu + dn);
+  return fp8 ? launch_pdl(few_ffn_kernel<true>, dim3(grid), dim3(384), few_smem(), st, f)
+             : launch_pdl(few_ffn_kernel<false>, dim3(grid), dim3(256), few_smem(), st, f);
+}
+
+}  // namespace moe

@@ -60,6 +60,8 @@ struct WsLayout {
   size_t status, ticket, partials, wr3, idx, w, counts, offsets, perm, inv, blk_base, counters,
       counters_s, xperm,
       act_r, act_s, y, touched, gmask, total;
+  // the few-token layer: its counters, and for T <= kFewMaxT its scratch
+  size_t f_claim, f_slots, f_mask, f_hq, f_hqe, f_act, f_exp, f_planes;
 };
 bool ws_layout(const moe_dims_t& d, WsLayout* out);
 
@@ -227,6 +229,37 @@ struct Gemm8Args {
   int* status;
 };
 cudaError_t launch_gemm_fp8(const Gemm8Args& a, cudaStream_t st, const char** why);
+
+// The layer for at most kFewMaxT tokens (few_layer.cu).
+constexpr int kFewMaxT = 16;
+struct FewPlan {
+  int TP;          // token rows per operand piece
+  int NX, PA;      // rows of the token operand: gate/up, down
+  int max_slots;   // shared experts + the most experts the call can choose
+  int fpt;         // features per gate/up tile
+  int sub;         // K-blocks per stage of a gate/up tile
+  int nd, parts;   // output blocks of 128 rows; K parts of a down unit
+};
+FewPlan few_plan(const moe_dims_t& d, bool fp8);
+struct FewArgs {
+  moe_dims_t d;
+  const uint16_t* h;
+  const float *Wr, *bias;
+  const uint16_t *W1, *W3, *W2, *Ws1, *Ws3, *Ws2;
+  const Fp8Weights* w8;    // set: FP8 weights, the six above unused
+  float* out;
+  int32_t* idx;
+  float* w;
+  // workspace
+  float* logits;           // [T, E]
+  int32_t *slot_of, *slot_expert, *nslots, *counts, *touched, *ticket, *claim;
+  uint32_t* slot_mask;
+  uint8_t *hq, *a_r, *a_s;
+  int8_t *hqe, *ae_r, *ae_s;
+  float* planes;
+  int* status;
+};
+cudaError_t launch_few(const FewArgs& a, cudaStream_t st, const char** why);
 
 // dst[i] = src[idx[i]] for n rows of row_bytes (a multiple of 16) bytes.
 cudaError_t launch_gather_bytes(const void* src, int src_rows, const int32_t* idx, int n,

@@ -35,7 +35,7 @@ __host__ __device__ constexpr uint32_t idesc_sf_byte(uint32_t a_byte, uint32_t b
 // D[tmem] (+)= (A * sfa) (B * sfb)^T over K = 32 E4M3 elements; one thread.
 // Scale factors: row r of A has its E8M0 byte in TMEM lane r % 32 (repeated in
 // each of the four lane quarters), column sfa + r / 32; B's rows the same
-// way from sfb.
+// way from sfb.  Both column addresses are multiples of four.
 __device__ __forceinline__ void mma_mxf8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                             uint32_t idesc, uint32_t sfa, uint32_t sfb,
                                             uint32_t accumulate) {
@@ -48,10 +48,15 @@ __device__ __forceinline__ void mma_mxf8_ss(uint32_t d_tmem, uint64_t a_desc, ui
       : "memory");
 }
 
-// 32 lanes x 32 bits, 1, 4 or 8 consecutive columns: thread i of the warp
+// 32 lanes x 32 bits, 1, 2, 4 or 8 consecutive columns: thread i of the warp
 // writes TMEM lane (base lane + i).
 __device__ __forceinline__ void tmem_st_x1(uint32_t taddr, uint32_t r) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(r)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st_x2(uint32_t taddr, uint32_t r0, uint32_t r1) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1, %2};" ::"r"(taddr), "r"(r0),
+               "r"(r1)
                : "memory");
 }
 __device__ __forceinline__ void tmem_st_x4(uint32_t taddr, const uint32_t* r) {
