@@ -279,7 +279,7 @@ int moe_forward_fp8(const void* h, const float* Wr, const float* bias, const moe
  * the merge in one persistent kernel that reads each chosen expert's weights
  * once.  The same layer, arguments, limits, workspace and errors as
  * moe_forward; two differences in precision: the logits' sums run in another
- * (fixed) order, and the gated activation enters the w2 product with 16
+ * (fixed) order, and the gated activation enters the w2 product with its 24
  * significant bits instead of 8.  Capturable in a CUDA graph; no internal
  * stream.  moe_ws_expert_counts and moe_ws_touched_experts hold for it too.
  * Repeated calls give identical bits.  Calls that share a workspace must not

@@ -198,7 +198,7 @@ bool ws_layout(const moe_dims_t& d, WsLayout* L) {
     // bytes of the activations (bf16 or codes) and of their exponents
     const size_t act = std::max((most * F + S * Fs) * p16.PA * 2 + 16,
                                 (most * F + S * Fs) * p8.PA + 16) + 256;
-    const size_t ex = (most * ((F + 127) / 128) + S * ((Fs + 127) / 128)) * 4 * p8.TP + 256;
+    const size_t ex = (most * ((F + 127) / 128) + S * ((Fs + 127) / 128)) * 4 * T + 256;
     // planes of the down products: few_plan splits K only while there are
     // fewer than 6 * 148 units, so at most twice that many units are split;
     // the bound grows with T, so that a workspace serves every smaller T
@@ -206,7 +206,7 @@ bool ws_layout(const moe_dims_t& d, WsLayout* L) {
         std::max(slots, std::min<size_t>(8 * slots, 12 * kSplitTargetBlocks / p16.nd));
     L->f_slots = take((64 + T * k + slots) * 4);
     L->f_mask = take(slots * 4);
-    L->f_hq = take(3 * p8.TP * D);
+    L->f_hq = take(3 * T * D);
     L->f_hqe = take(T * ((D + 127) / 128));
     L->f_act = take(act);
     L->f_exp = take(ex);
@@ -569,7 +569,7 @@ int forward_few_impl(const void* h, const float* Wr, const float* bias, const Ex
   a.a_r = w.at<uint8_t>(w.L.f_act);
   a.a_s = a.a_r + align256(most * L.PA * dims->F * (wt.fp8 ? 1 : 2));
   a.ae_r = w.at<int8_t>(w.L.f_exp);
-  a.ae_s = a.ae_r + most * L.TP * 4 * ((dims->F + 127) / 128);
+  a.ae_s = a.ae_r + most * (size_t)dims->T * 4 * ((dims->F + 127) / 128);
   a.planes = w.at<float>(w.L.f_planes);
   a.status = w.status();
   const char* why = "launch failed";

@@ -26,15 +26,20 @@
 // choose it is dropped, whatever it is.
 //
 // Precision.  bf16 weights: hidden rows enter as they are; an activation
-// enters as two bf16 pieces (its rounding and what that leaves, 16 bits
-// together), in columns of their own that the epilogue adds in fp32.  FP8
-// weights: the codes enter as they are, with their block exponents as the
-// tensor core's scales, and the other operand is a sum of E4M3 pieces, each
-// holding 4 bits of what the ones before it leave, with a scale 2^4 lower.  A
-// bf16 value has 8 bits, so two pieces hold it and a third reaches values far
-// below their block's largest (E4M3's subnormal step is 2^-17.8 of it: three
-// pieces leave 2^-25.8); four hold an activation to 2^-16 of itself.  The
-// pieces cost columns, not weight bytes.
+// enters as three bf16 pieces (its rounding, and twice what is left: all 24
+// bits), in columns of their own that the epilogue adds in fp32.  FP8 weights:
+// the codes enter as they are, with their block exponents as the tensor
+// core's scales, and the other operand is a sum of E4M3 pieces, each holding 4
+// bits of what the ones before it leave, with a scale 2^4 lower.  A bf16 value
+// has 8 bits, so two pieces hold it and a third reaches values far below their
+// block's largest (E4M3's subnormal step is 2^-17.8 of it: three pieces leave
+// 2^-25.8); four hold an activation to 2^-16 of itself.  The pieces cost
+// columns, not weight bytes.
+//
+// The tensor core's bf16 form cuts off its running sum at each step of 16,
+// which over K = 6144 adds up to 1.5e-5 of the result (measured).  K-blocks
+// therefore take turns over as many accumulators as fit in tensor memory, and
+// the epilogue adds those in fp32.
 #include <algorithm>
 #include <climits>
 
@@ -52,7 +57,8 @@ constexpr unsigned kAll = 0xffffffffu;
 constexpr int kRouterThreads = 512;
 constexpr int kRouterWarps = kRouterThreads / 32;
 constexpr int kRouterExperts = 4;        // experts per router block
-constexpr int kPiecesH = 3, kPiecesA = 4;
+constexpr int kPiecesH = 3, kPiecesA = 4;   // E4M3 pieces of a hidden value, an activation
+constexpr int kPiecesB = 3;                 // bf16 pieces of an activation
 constexpr int kPieceMinExp = -115;       // the last piece's exponent stays an E8M0 value
 
 // ---------------------------------------------------------------------------
@@ -74,10 +80,9 @@ struct FewRoute {
   int32_t* ticket;        // zero between calls
   int* status;
   int router_blocks;
-  // FP8: pieces of the hidden rows [kPiecesH * TP, D] and exponents [TP, KB]
+  // FP8: pieces of the hidden rows [kPiecesH * T, D] and exponents [T, KB]
   uint8_t* hq;
   int8_t* hqe;
-  int TP;
 };
 
 // Sums v[i] over the warp for all i: lane l ends with the sums of v[i] whose
@@ -298,7 +303,7 @@ __device__ __forceinline__ void split_hidden(const FewRoute& p, int unit, int la
       const uint32_t code = piece_code(v[i], inv, unit2);
       c |= (odd[i] ? 0x7fu : code) << (8 * i);
     }
-    if (col < p.D) *reinterpret_cast<uint32_t*>(p.hq + (size_t)(q * p.TP + t) * p.D + col) = c;
+    if (col < p.D) *reinterpret_cast<uint32_t*>(p.hq + (size_t)(q * p.T + t) * p.D + col) = c;
   }
 }
 
@@ -334,9 +339,14 @@ constexpr int kAStage = 128 * 128;       // 128 weight rows x 128 bytes of K
 constexpr int kBStage = 8192;
 constexpr int kAStages = 9, kBStages = 8;
 constexpr int kRing = kAStages * kAStage + kBStages * kBStage;
-constexpr int kAccCols = 64;             // one accumulator (N <= 64)
 constexpr int kSfSlot = 32;              // scale columns of one slot: 4 weights, 4 x 4 tokens
-constexpr uint32_t kTmemCols = 256;      // 2 accumulators + 2 scale slots
+constexpr uint32_t kTmemCols = 512;
+// TMEM columns of one of the two accumulator sets; the scale slots follow.  The
+// epilogue reads 16 columns from a piece's first one, at most 10 beyond the
+// set, which are still columns of this CTA.
+__host__ __device__ constexpr int acc_cols(bool fp8) { return fp8 ? 192 : 240; }
+// Accumulators of a set for a token operand of n rows.
+__device__ __forceinline__ int acc_count(bool fp8, int n) { return min(16, acc_cols(fp8) / n); }
 constexpr int kQueue = 4;
 
 struct alignas(64) FewFfn {
@@ -346,10 +356,10 @@ struct alignas(64) FewFfn {
   CUtensorMap w2_r, w2_s;                // [E * D, F], box 128 rows
   const int8_t *e1_r, *e3_r, *e2_r, *e1_s, *e3_s, *e2_s;
   int T, D, F, k, S, Fs;
-  int TP;                // token rows per piece
   int NX, PA;            // token operand rows: gate/up, down
-  int fpt;               // features per gate/up tile (64, 32 or 16)
-  int sub;               // K-blocks per stage of a gate/up tile
+  // features per gate/up tile (64, 32 or 16) and K-blocks per stage of one,
+  // of a chosen and of a shared expert
+  int fpt_r, fpt_s, sub_r, sub_s;
   int parts;             // K parts of a down unit
   int nd;                // blocks of 128 output rows
   int ntr, nts;          // gate/up tiles per chosen / shared slot
@@ -359,7 +369,7 @@ struct alignas(64) FewFfn {
   const uint32_t* slot_mask;
   const float* w;
   const int8_t* hqe;     // FP8: exponents of the hidden rows [T, KB]
-  // activations, their exponents (FP8: one per 32 features, [slots, TP, 4 * KB])
+  // activations, their exponents (FP8: one per 32 features, [slots, T, 4 * KB])
   uint8_t *a_r, *a_s;
   int8_t *ae_r, *ae_s;
   float* planes;         // [slot * parts + part][T][D]
@@ -502,7 +512,7 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
         Unit u{0, 0, 0, 0, 0};
         if (tile < shared_tiles) {
           u.slot = tile / p.nts;
-          u.at = (tile - u.slot * p.nts) * p.fpt;
+          u.at = (tile - u.slot * p.nts) * p.fpt_s;
           u.expert = u.slot;
         } else {
           if (routed < 0) {
@@ -513,7 +523,7 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
           if (r < routed * p.ntr) {
             const int s = r / p.ntr;
             u.slot = p.S + s;
-            u.at = (r - s * p.ntr) * p.fpt;
+            u.at = (r - s * p.ntr) * p.fpt_r;
           } else {
             r -= routed * p.ntr;
             const int per = p.nd * p.parts;
@@ -551,10 +561,10 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
           const CUtensorMap* m1 = sh ? &p.w1_s : &p.w1_r;
           const CUtensorMap* m3 = sh ? &p.w3_s : &p.w3_r;
           const int row = u.expert * (sh ? p.Fs : p.F) + u.at;
-          const int boxes = p.fpt / 16;
-          for (int kb = k0; kb < k1; kb += p.sub) {
+          const int boxes = (sh ? p.fpt_s : p.fpt_r) / 16, sub = sh ? p.sub_s : p.sub_r;
+          for (int kb = k0; kb < k1; kb += sub) {
             if (!ptx::mbar_wait(&ss.a_empty[stage], phase ^ 1u, abort)) { ok = false; break; }
-            const int n = min(p.sub, k1 - kb);
+            const int n = min(sub, k1 - kb);
             ptx::mbar_arrive_expect_tx(&ss.a_full[stage], n * boxes * 4096);
             uint8_t* dst = ring_a + stage * kAStage;
             for (int i = 0; i < n; ++i)
@@ -595,7 +605,7 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
       const CUtensorMap* m = u.down ? (sh ? &p.act_s : &p.act_r) : &p.x;
       const int row = u.down ? (sh ? u.slot : u.slot - p.S) * p.PA : 0;
       const int bytes = (u.down ? p.PA : p.NX) * 128;
-      const int sub = u.down ? 1 : p.sub;
+      const int sub = u.down ? 1 : sh ? p.sub_s : p.sub_r;
       bool ok = true;
       if (ptx::elect_one()) {
         for (int kb = k0; kb < k1; kb += sub) {
@@ -624,15 +634,18 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
     while (q.next(ss, u, abort, lane)) {
       int k0, k1;
       unit_k<EB>(p, u, &k0, &k1);
-      const int sub = u.down ? 1 : p.sub;
+      const bool sh = u.slot < p.S;
+      const int sub = u.down ? 1 : sh ? p.sub_s : p.sub_r;
       const int n = u.down ? p.PA : p.NX;
+      const int nacc = acc_count(FP8, n);
       const uint32_t idesc = FP8 ? ptx::idesc_mxf8(128, n) : ptx::idesc_bf16_f32(128, n);
-      const int a_bytes = u.down ? kAStage : p.fpt * 2 * 128;
+      const int a_bytes = u.down ? kAStage : (sh ? p.fpt_s : p.fpt_r) * 2 * 128;
       const int b_bytes = n * 128;
       bool ok = true;
       if (ptx::elect_one()) {
         ok = ptx::mbar_wait(&ss.acc_empty[buf], cph ^ 1u, abort);
-        const uint32_t acc = tmem + buf * kAccCols;
+        uint32_t acc = tmem + buf * acc_cols(FP8);
+        int turn = 0;
         for (int kb = k0; ok && kb < k1; kb += sub) {
           if (!ptx::mbar_wait(&ss.b_full[bs], bph, abort)) { ok = false; break; }
           if (!ptx::mbar_wait(&ss.a_full[as], aph, abort)) { ok = false; break; }
@@ -646,7 +659,7 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
             ptx::tc_fence_after();
             const uint64_t da = ptx::smem_desc_sw128(sa), db = ptx::smem_desc_sw128(sb);
             if (FP8) {
-              const uint32_t sfa = tmem + 2 * kAccCols + slot * kSfSlot;
+              const uint32_t sfa = tmem + 2 * acc_cols(FP8) + slot * kSfSlot;
               // gate/up: one word per row covers four K-blocks; down: one word per
               // row and K-block covers its four steps of 32
               const uint32_t sfb = sfa + 4 + (u.down ? (kk & 3) * 4 : 0);
@@ -654,7 +667,7 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
               for (int k = 0; k < 4; ++k)
                 ptx::mma_mxf8_ss(acc, da + 2 * k, db + 2 * k,
                                  idesc | ptx::idesc_sf_byte(kk & 3, u.down ? k : kk & 3), sfa, sfb,
-                                 kk > k0 || k > 0);
+                                 kk - k0 >= nacc || k > 0);
               if ((kk & 3) == 3 || kk == k1 - 1) {
                 ptx::mma_commit(&ss.sf_empty[slot]);
                 if (++slot == 2) { slot = 0; sph ^= 1u; }
@@ -662,7 +675,12 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
             } else {
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                ptx::mma_f16_ss(acc, da + 2 * k, db + 2 * k, idesc, kk > k0 || k > 0);
+                ptx::mma_f16_ss(acc, da + 2 * k, db + 2 * k, idesc, kk - k0 >= nacc || k > 0);
+            }
+            acc += n;
+            if (++turn == nacc) {
+              turn = 0;
+              acc -= nacc * n;
             }
           }
           if (!ok) break;
@@ -701,21 +719,31 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
       unit_k<EB>(p, u, &k0, &k1);
       if (__any_sync(kAll, !ptx::mbar_wait(&ss.acc_full[buf], cph, abort))) break;
       ptx::tc_fence_after();
-      const uint32_t acc = tmem + buf * kAccCols + lanes;
-      // the token columns, pieces added: v[t] is this lane's weight row
-      const int pieces = u.down ? (FP8 ? kPiecesA : 2) : (FP8 ? kPiecesH : 1);
-      const bool rows = u.down || qt * 16 < p.fpt;   // this warp's rows belong to the tile
+      const uint32_t acc = tmem + buf * acc_cols(FP8) + lanes;
+      // the token columns, pieces and accumulators added: v[t] is this lane's
+      // weight row
+      const int pieces = u.down ? (FP8 ? kPiecesA : kPiecesB) : (FP8 ? kPiecesH : 1);
+      const int n = u.down ? p.PA : p.NX;
+      const int used = min(acc_count(FP8, n), k1 - k0);
+      const int fpt = sh ? p.fpt_s : p.fpt_r;
+      const bool rows = u.down || qt * 16 < fpt;     // this warp's rows belong to the tile
       float v[16];
 #pragma unroll
       for (int t = 0; t < 16; ++t) v[t] = 0.f;
-      if (rows && k1 > k0) {
-        // smallest piece first
-        for (int c = pieces - 1; c >= 0; --c) {
-          uint32_t r[16];
-          ptx::tmem_ld_x16(acc + c * p.TP, r);
-          ptx::tmem_wait_ld();
+      if (rows) {
+        for (int c = pieces - 1; c >= 0; --c) {        // smallest piece first
+          float s[16];
 #pragma unroll
-          for (int t = 0; t < 16; ++t) v[t] += __uint_as_float(r[t]);
+          for (int t = 0; t < 16; ++t) s[t] = 0.f;
+          for (int a = 0; a < used; ++a) {
+            uint32_t r[16];
+            ptx::tmem_ld_x16(acc + a * n + c * p.T, r);
+            ptx::tmem_wait_ld();
+#pragma unroll
+            for (int t = 0; t < 16; ++t) s[t] += __uint_as_float(r[t]);
+          }
+#pragma unroll
+          for (int t = 0; t < 16; ++t) v[t] += s[t];
         }
       }
       ptx::tc_fence_before();
@@ -738,12 +766,16 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
           if (FP8) {
             ss.act[(qt * 16 + (lane & 15)) * 17 + tt] = a;
           } else if (rows && f < F && ((mask >> tt) & 1u)) {
-            const __nv_bfloat16 hi = __float2bfloat16_rn(a);
-            const float hf = __bfloat162float(hi);
             __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(sh ? p.a_s : p.a_r) +
                                  (row0 + tt) * F + f;
-            dst[0] = hi;
-            dst[(size_t)p.TP * F] = __float2bfloat16_rn(isfinite(hf) ? a - hf : 0.f);
+            float rest = a;
+#pragma unroll
+            for (int c = 0; c < kPiecesB; ++c) {
+              const __nv_bfloat16 piece = __float2bfloat16_rn(rest);
+              dst[(size_t)c * p.T * F] = piece;
+              // an infinite piece is all there is
+              rest = __hisinf(piece) ? 0.f : rest - __bfloat162float(piece);
+            }
           }
         }
         if (FP8) {
@@ -751,7 +783,7 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
           epi_sync();
           int8_t* ae = sh ? p.ae_s : p.ae_r;
           const int stride = (F + 127) / 128 * 4;   // exponents of a row
-          for (int i = qt; i < p.T * (p.fpt / 32); i += 4) {
+          for (int i = qt; i < p.T * (fpt / 32); i += 4) {
             const int t = i % p.T, b = i / p.T;
             if (!((mask >> t) & 1u)) continue;
             float a = ss.act[(b * 32 + lane) * 17 + t];
@@ -762,12 +794,12 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
             const int fb = u.at + b * 32;
             if (fb >= F) continue;
             if (lane == 0)
-              ae[((size_t)(sh ? u.slot : u.slot - p.S) * p.TP + t) * stride + fb / 32] = (int8_t)e;
+              ae[((size_t)(sh ? u.slot : u.slot - p.S) * p.T + t) * stride + fb / 32] = (int8_t)e;
             uint8_t* dst = (sh ? p.a_s : p.a_r) + (row0 + t) * F + fb + lane;
 #pragma unroll
             for (int c = 0; c < kPiecesA; ++c) {
               const uint32_t code = piece_code(a, pow2f(4 * c - e), pow2f(e - 4 * c));
-              if (fb + lane < F) dst[(size_t)c * p.TP * F] = (uint8_t)(odd ? 0x7fu : code);
+              if (fb + lane < F) dst[(size_t)c * p.T * F] = (uint8_t)(odd ? 0x7fu : code);
             }
           }
           epi_sync();   // the tile's activations are read: the next may be written
@@ -845,7 +877,7 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
              ((size_t)u.expert * KBF + u.at / 128) * KB;
       }
       const int8_t* ae = (sh ? p.ae_s : p.ae_r) +
-                         (size_t)(sh ? u.slot : u.slot - p.S) * p.TP * (KBF * 4);
+                         (size_t)(sh ? u.slot : u.slot - p.S) * p.T * (KBF * 4);
       bool ok = true;
       for (int s = k0 / 4; s * 4 < k1; ++s) {
         uint32_t wa[4], wx[4][2];
@@ -856,9 +888,9 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
         for (int i = 0; i < 4; ++i) {
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const int row = j * 32 + lane, c = row / p.TP, t = row - c * p.TP;
+            const int row = j * 32 + lane, c = row / p.T, t = row - c * p.T;
             wx[i][j] = 0x7f7f7f7fu;      // rows of no token: any valid scale
-            if (t >= p.T || c >= (u.down ? kPiecesA : kPiecesH)) continue;
+            if (c >= (u.down ? kPiecesA : kPiecesH)) continue;
             if (!u.down) {
               if (i == 0) wx[i][j] = scale_word(p.hqe + t * KBD + 4 * s, KBD - 4 * s, false, &bad);
             } else if (4 * s + i < KBF) {
@@ -872,7 +904,7 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
         }
         if (__any_sync(kAll, !ptx::mbar_wait(&ss.sf_empty[slot], sph ^ 1u, abort))) { ok = false; break; }
         ptx::tc_fence_after();
-        const uint32_t dst = tmem + 2 * kAccCols + slot * kSfSlot + lanes;
+        const uint32_t dst = tmem + 2 * acc_cols(FP8) + slot * kSfSlot + lanes;
         ptx::tmem_st_x4(dst, wa);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -928,24 +960,32 @@ cudaError_t launch_few_router(const FewRoute& r, int blocks, cudaStream_t st) {
 // How a call is cut into tiles.
 FewPlan few_plan(const moe_dims_t& d, bool fp8) {
   FewPlan L{};
-  L.TP = fp8 ? (d.T <= 4 ? 4 : d.T <= 8 ? 8 : 16) : (d.T <= 8 ? 8 : 16);
-  L.NX = fp8 ? (kPiecesH * L.TP + 15) / 16 * 16 : 16;
-  L.PA = (fp8 ? kPiecesA : 2) * L.TP;
+  auto round16 = [](int n) { return (n + 15) / 16 * 16; };
+  L.NX = fp8 ? round16(kPiecesH * d.T) : 16;
+  L.PA = round16((fp8 ? kPiecesA : kPiecesB) * d.T);
   const int most = std::min(d.E, d.T * d.k);     // chosen experts at most
   L.max_slots = d.S + most;
   const int Fs = d.S > 0 ? d.Fs : 0;
-  auto tiles = [&](int fpt) {
-    return (long long)d.S * ((Fs + fpt - 1) / fpt) + (long long)most * ((d.F + fpt - 1) / fpt);
-  };
   // Features per gate/up tile: 64 fill the 128 weight rows of a product.  When
   // that leaves fewer than two tiles per SM, 32 (and with bf16 weights 16)
   // spread the weight stream over more SMs; the rows they leave unused cost
-  // tensor time that the stream does not need.
-  L.fpt = 64;
-  while (L.fpt > (fp8 ? 32 : 16) && tiles(L.fpt) < 2 * kSplitTargetBlocks) L.fpt /= 2;
+  // tensor time that the stream does not need.  The shared experts' tiles run
+  // while the routing is still being made, so they are to keep every SM busy
+  // by themselves: about a tile per SM.
+  const int least = fp8 ? 32 : 16;
+  auto tiles = [](int experts, int F, int fpt) { return (long long)experts * ((F + fpt - 1) / fpt); };
+  L.fpt_s = L.fpt_r = 64;
+  while (L.fpt_s > least && tiles(d.S, Fs, L.fpt_s) < kSplitTargetBlocks * 3 / 4) L.fpt_s /= 2;
+  while (L.fpt_r > least && tiles(d.S, Fs, L.fpt_s) + tiles(most, d.F, L.fpt_r) < 2 * kSplitTargetBlocks)
+    L.fpt_r /= 2;
   // K-blocks per stage: the stage stays 16 KB of weights, within the token stage
-  L.sub = std::max(1, std::min(64 / L.fpt, kBStage / (L.NX * 128)));
-  if (L.sub == 3) L.sub = 2;
+  auto sub = [&](int fpt) {
+    int n = 64 / fpt;
+    while (n > 1 && n * L.NX * 128 > kBStage) n /= 2;
+    return n;
+  };
+  L.sub_r = sub(L.fpt_r);
+  L.sub_s = sub(L.fpt_s);
   L.nd = (d.D + 127) / 128;
   const int eb = fp8 ? 128 : 64;
   const int kb = std::min((d.F + eb - 1) / eb, d.S > 0 ? (Fs + eb - 1) / eb : 1 << 30);
@@ -974,7 +1014,7 @@ cudaError_t launch_few(const FewArgs& a, cudaStream_t st, const char** why) {
   r.ticket = a.ticket;
   r.status = a.status;
   r.router_blocks = (d.E + kRouterExperts - 1) / kRouterExperts;
-  r.hq = a.hq; r.hqe = a.hqe; r.TP = L.TP;
+  r.hq = a.hq; r.hqe = a.hqe;
   const int units = fp8 ? d.T * ((d.D + 127) / 128) : 0;
   const int blocks = r.router_blocks + (units + kRouterWarps - 1) / kRouterWarps;
 
@@ -988,7 +1028,7 @@ cudaError_t launch_few(const FewArgs& a, cudaStream_t st, const char** why) {
     return make_tensor_map(m, base, rows, cols, box, eb, es, 128);
   };
   const int most = L.max_slots - d.S;
-  bool ok = (fp8 ? map(&f.x, a.hq, kPiecesH * L.TP, d.D, L.NX) : map(&f.x, a.h, d.T, d.D, L.NX)) &&
+  bool ok = (fp8 ? map(&f.x, a.hq, kPiecesH * d.T, d.D, L.NX) : map(&f.x, a.h, d.T, d.D, L.NX)) &&
             map(&f.act_r, a.a_r, (uint64_t)most * L.PA, d.F, L.PA) &&
             map(&f.w1_r, W1, (uint64_t)d.E * d.F, d.D, 16) &&
             map(&f.w3_r, W3, (uint64_t)d.E * d.F, d.D, 16) &&
@@ -1008,10 +1048,11 @@ cudaError_t launch_few(const FewArgs& a, cudaStream_t st, const char** why) {
     f.e1_s = a.w8->Ws1e; f.e3_s = a.w8->Ws3e; f.e2_s = a.w8->Ws2e;
   }
   f.T = d.T; f.D = d.D; f.F = d.F; f.k = d.k; f.S = d.S; f.Fs = Fs;
-  f.TP = L.TP; f.NX = L.NX; f.PA = L.PA;
-  f.fpt = L.fpt; f.sub = L.sub; f.parts = L.parts; f.nd = L.nd;
-  f.ntr = (d.F + L.fpt - 1) / L.fpt;
-  f.nts = (Fs + L.fpt - 1) / L.fpt;
+  f.NX = L.NX; f.PA = L.PA;
+  f.fpt_r = L.fpt_r; f.fpt_s = L.fpt_s; f.sub_r = L.sub_r; f.sub_s = L.sub_s;
+  f.parts = L.parts; f.nd = L.nd;
+  f.ntr = (d.F + L.fpt_r - 1) / L.fpt_r;
+  f.nts = (Fs + L.fpt_s - 1) / L.fpt_s;
   f.max_slots = L.max_slots;
   f.idx = a.idx; f.slot_of = a.slot_of; f.slot_expert = a.slot_expert; f.nslots = a.nslots;
   f.slot_mask = a.slot_mask;

@@ -233,11 +233,11 @@ cudaError_t launch_gemm_fp8(const Gemm8Args& a, cudaStream_t st, const char** wh
 // The layer for at most kFewMaxT tokens (few_layer.cu).
 constexpr int kFewMaxT = 16;
 struct FewPlan {
-  int TP;          // token rows per operand piece
   int NX, PA;      // rows of the token operand: gate/up, down
   int max_slots;   // shared experts + the most experts the call can choose
-  int fpt;         // features per gate/up tile
-  int sub;         // K-blocks per stage of a gate/up tile
+  // features per gate/up tile and K-blocks per stage of one, of a chosen and
+  // of a shared expert
+  int fpt_r, fpt_s, sub_r, sub_s;
   int nd, parts;   // output blocks of 128 rows; K parts of a down unit
 };
 FewPlan few_plan(const moe_dims_t& d, bool fp8);
