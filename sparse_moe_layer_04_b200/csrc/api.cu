@@ -171,7 +171,7 @@ bool ws_layout(const moe_dims_t& d, WsLayout* L) {
   L->ticket = take(256);
   // counters of the few-token layer: zero between calls, so they stand where
   // no other T of the same layer moves them
-  L->f_claim = take((64 + 2 + S + std::min<size_t>(E, kFewMaxT * k) + (D + 127) / 128) * 4);
+  L->f_claim = take((64 + 3 + S + std::min<size_t>(E, kFewMaxT * k) + (D + 127) / 128) * 4);
   L->partials = take((size_t)sp.nsplit * T * E * 4);
   L->wr3 = take(sp.tensor && !sp.fused ? E * 3 * D * 2 : 0);
   L->idx = take(T * k * 4);

@@ -83,6 +83,7 @@ struct FewRoute {
   // FP8: pieces of the hidden rows [kPiecesH * T, D] and exponents [T, KB]
   uint8_t* hq;
   int8_t* hqe;
+  int32_t* hq_ready;      // counts the blocks that wrote them
 };
 
 // Sums v[i] over the warp for all i: lane l ends with the sums of v[i] whose
@@ -221,7 +222,6 @@ __device__ void select_and_list(const FewRoute& p, uint32_t* s_ord) {
   int my_e = INT_MAX;
   if (t < p.T) {
     uint32_t* ord = s_ord + t * p.E;
-    float my_s = 0.f, sum = 0.f;
     for (int j = 0; j < p.k; ++j) {
       uint32_t bu = 0u;
       int be = INT_MAX;
@@ -232,17 +232,13 @@ __device__ void select_and_list(const FewRoute& p, uint32_t* s_ord) {
         }
       warp_best(bu, be);
       // no key is left when some were NaN: the slot stays empty
-      const bool ok = bu != 0u;
-      const float s = ok ? score(__ldcg(p.logits + (size_t)t * p.E + be)) : 0.f;
-      __syncwarp();
-      if (ok && lane == 0) ord[be] = 0u;
-      __syncwarp();
-      if (lane == j && ok) {
-        my_e = be;
-        my_s = s;
-      }
-      sum = j == 0 ? s : __fadd_rn(sum, s);
+      if (bu && lane == (be & 31)) ord[be] = 0u;   // read again by this lane alone
+      if (bu && lane == j) my_e = be;
     }
+    // the scores of the chosen, a lane each, and their sum in slot order
+    const float my_s = my_e != INT_MAX ? score(__ldcg(p.logits + (size_t)t * p.E + my_e)) : 0.f;
+    float sum = __shfl_sync(kAll, my_s, 0);
+    for (int j = 1; j < p.k; ++j) sum = __fadd_rn(sum, __shfl_sync(kAll, my_s, j));
     if (lane < p.k) {
       p.idx[t * p.k + lane] = my_e;
       p.w[t * p.k + lane] = __fmul_rn(__fdiv_rn(my_s, sum), p.scale);
@@ -319,6 +315,11 @@ __global__ void __launch_bounds__(kRouterThreads) few_router_kernel(const FewRou
   if ((int)blockIdx.x >= p.router_blocks) {
     const int unit = ((int)blockIdx.x - p.router_blocks) * kRouterWarps + warp;
     if (unit < p.T * ((p.D + 127) / 128)) split_hidden(p, unit, lane);
+    // the pieces become visible to the whole GPU and to TMA, then the count
+    ptx::fence_proxy_async_global();
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) atomicAdd(p.hq_ready, 1);
     return;
   }
   router_logits_block<TT>(p, reinterpret_cast<float*>(s_dyn));
@@ -374,8 +375,10 @@ struct alignas(64) FewFfn {
   int8_t *ae_r, *ae_s;
   float* planes;         // [slot * parts + part][T][D]
   float* out;
-  int32_t* claim;        // claim counter, exit ticket, then per-slot counts, then
-                         // per-output-block tickets; zero between calls
+  int32_t* claim;        // claim counter, exit ticket, blocks of pieces written, then
+                         // per-slot counts, then per-output-block tickets; zero
+                         // between calls
+  int hq_blocks;         // FP8: blocks that write the pieces of the hidden rows
   int32_t* touched;
   int* status;
 };
@@ -399,6 +402,8 @@ struct FewShared {
   uint32_t tmem_base;
   int abort, bad, last, exit_last;
   float act[64 * 17];    // FP8: activations of a tile [feature][token]
+  int tab_slot[kFewMaxT * 32];   // the tokens' choices: slot and weight
+  float tab_w[kFewMaxT * 32];
 };
 
 constexpr int few_smem() { return 1024 + kRing + (int)sizeof(FewShared); }
@@ -431,9 +436,9 @@ __device__ __forceinline__ void unit_k(const FewFfn& p, const Unit& u, int* k0, 
   }
 }
 
-__device__ __forceinline__ int32_t* slot_count(const FewFfn& p, int slot) { return p.claim + 2 + slot; }
+__device__ __forceinline__ int32_t* slot_count(const FewFfn& p, int slot) { return p.claim + 3 + slot; }
 __device__ __forceinline__ int32_t* out_ticket(const FewFfn& p, int d) {
-  return p.claim + 2 + p.max_slots + d;
+  return p.claim + 3 + p.max_slots + d;
 }
 // Arrivals after which a slot's activations are complete: four epilogue warps a tile.
 __device__ __forceinline__ int slot_target(const FewFfn& p, int slot) {
@@ -448,6 +453,12 @@ __device__ __forceinline__ bool slot_wait(const FewFfn& p, int slot, volatile in
   return !__any_sync(kAll, !ptx::counter_wait(slot_count(p, slot), slot_target(p, slot), abort));
 }
 
+// Waits, whole warp, until the hidden rows' pieces are written.  The blocks of
+// the first kernel that write them are all running before this kernel starts.
+__device__ __forceinline__ bool pieces_wait(const FewFfn& p, volatile int* abort) {
+  return !__any_sync(kAll, !ptx::counter_wait(p.claim + 2, p.hq_blocks, abort));
+}
+
 // Four E8M0 bytes from exponents q[0 .. n-1] (n >= 1, the others count as 0);
 // outside [lo, hi] raises *bad.
 __device__ __forceinline__ uint32_t scale_word(const int8_t* q, int n, bool check, bool* bad) {
@@ -458,6 +469,53 @@ __device__ __forceinline__ uint32_t scale_word(const int8_t* q, int n, bool chec
   if (check)
     *bad |= (__vcmpgts4(w, 0x07070707u) | __vcmplts4(w, 0x8b8b8b8bu)) != 0;
   return __vadd4(w, 0x7f7f7f7fu);
+}
+
+// out for 128 columns, from the planes of every slot: shared experts, then the
+// token's choices in their order (moe_combine's).  Four groups of 32 threads
+// take every fourth token, a thread four columns; eight loads are in flight
+// before the first is added.
+__device__ __forceinline__ void merge_block(const FewFfn& p, const FewShared& ss, int at, int tid) {
+  const int d = at * 128 + (tid & 31) * 4;
+  if (d >= p.D) return;
+  const size_t plane = (size_t)p.T * p.D;
+  const int n = (p.S + p.k) * p.parts;
+  for (int t = tid >> 5; t < p.T; t += 4) {
+    const float* src = p.planes + (size_t)t * p.D + d;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f), y = o;
+    int j = 0, part = 0;                 // the term being added
+    int lj = 0, lpart = 0;               // the term being loaded
+    for (int i0 = 0; i0 < n; i0 += 8) {
+      float4 r[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        r[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i0 + i < n) {
+          const int s = lj < p.S ? lj : p.S + ss.tab_slot[t * p.k + lj - p.S];
+          if (s >= (lj < p.S ? 0 : p.S))
+            r[i] = __ldcg(reinterpret_cast<const float4*>(src + ((size_t)s * p.parts + lpart) * plane));
+          if (++lpart == p.parts) { lpart = 0; ++lj; }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (i0 + i < n) {
+          y.x += r[i].x; y.y += r[i].y; y.z += r[i].z; y.w += r[i].w;
+          if (++part == p.parts) {
+            // an empty choice (NaN keys) adds nothing
+            const float c = j < p.S ? 1.f : ss.tab_slot[t * p.k + j - p.S] < 0 ? 0.f
+                                                                    : ss.tab_w[t * p.k + j - p.S];
+            o.x = fmaf(c, y.x, o.x); o.y = fmaf(c, y.y, o.y);
+            o.z = fmaf(c, y.z, o.z); o.w = fmaf(c, y.w, o.w);
+            y = make_float4(0.f, 0.f, 0.f, 0.f);
+            part = 0;
+            ++j;
+          }
+        }
+      }
+    }
+    *reinterpret_cast<float4*>(p.out + (size_t)t * p.D + d) = o;
+  }
 }
 
 template <bool FP8>
@@ -587,14 +645,19 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
     // ---------------- token / activation producer ----------------
     QueueReader q;
     Unit u;
-    bool waited = false;
+    bool waited = false, pieces = false;
     int stage = 0;
     uint32_t phase = 0, issued = 0, parity = 0;
     while (q.next(ss, u, abort, lane)) {
       const bool sh = u.slot < p.S;
-      if (!waited && (FP8 || u.down || !sh)) {
+      if (!waited && (u.down || !sh)) {
         ptx::pdl_wait();
         waited = true;
+      }
+      if (FP8 && !pieces) {
+        if (!pieces_wait(p, abort)) break;
+        ptx::fence_proxy_async_global();
+        pieces = true;
       }
       if (u.down) {
         if (!slot_wait(p, u.slot, abort)) break;
@@ -713,6 +776,10 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
       if (!waited && (u.down || !sh)) {
         ptx::pdl_wait();
         waited = true;
+        for (int i = threadIdx.x - 128; i < p.T * p.k; i += 128) {
+          ss.tab_slot[i] = __ldcg(p.slot_of + i);
+          ss.tab_w[i] = __ldcg(p.w + i);
+        }
       }
       const uint32_t mask = sh ? (1u << p.T) - 1u : __ldcg(p.slot_mask + u.slot - p.S);
       int k0, k1;
@@ -828,24 +895,7 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
         epi_sync();
         if (ss.last) {
           __threadfence();
-          // moe_combine's order: shared experts, then the token's choices
-          if (d < p.D) {
-            const size_t ps = (size_t)p.T * p.D;
-            for (int t = 0; t < p.T; ++t) {
-              const float* src = p.planes + (size_t)t * p.D + d;
-              float o = 0.f;
-              for (int i = 0; i < p.S * p.parts; ++i) o += __ldcg(src + i * ps);
-              for (int j = 0; j < p.k; ++j) {
-                const int s = __ldcg(p.slot_of + t * p.k + j);
-                if (s < 0) continue;
-                float y = 0.f;
-                for (int i = 0; i < p.parts; ++i)
-                  y += __ldcg(src + ((size_t)(p.S + s) * p.parts + i) * ps);
-                o = fmaf(__ldcg(p.w + t * p.k + j), y, o);
-              }
-              p.out[(size_t)t * p.D + d] = o;
-            }
-          }
+          merge_block(p, ss, u.at, threadIdx.x - 128);
         }
       }
     }
@@ -855,13 +905,13 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
     const int KBD = (p.D + 127) / 128;
     QueueReader q;
     Unit u;
-    bool waited = false, bad = false;
+    bool pieces = false, bad = false;
     int slot = 0;
     uint32_t sph = 0;
     while (q.next(ss, u, abort, lane)) {
-      if (!waited) {
-        ptx::pdl_wait();
-        waited = true;
+      if (!pieces) {
+        if (!pieces_wait(p, abort)) break;
+        pieces = true;
       }
       const bool sh = u.slot < p.S;
       const int F = sh ? p.Fs : p.F, KBF = (F + 127) / 128;
@@ -938,8 +988,7 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
     for (int i = threadIdx.x; i < p.max_slots; i += blockDim.x) *slot_count(p, i) = 0;
     if (threadIdx.x == 0) {
       *p.touched = __ldcg(p.nslots);
-      p.claim[0] = 0;
-      p.claim[1] = 0;
+      p.claim[0] = p.claim[1] = p.claim[2] = 0;
     }
   }
 }
@@ -989,12 +1038,16 @@ FewPlan few_plan(const moe_dims_t& d, bool fp8) {
   L.nd = (d.D + 127) / 128;
   const int eb = fp8 ? 128 : 64;
   const int kb = std::min((d.F + eb - 1) / eb, d.S > 0 ? (Fs + eb - 1) / eb : 1 << 30);
-  // K parts of a down unit: until there are six units per SM or a part has
-  // fewer than four K-blocks
+  // K parts of a down unit: until there are six units per SM, as long as a
+  // part has 16 K-blocks (shorter units end in less time than their
+  // epilogue takes); with fewer than two units per SM, down to four K-blocks
   L.parts = 1;
-  while (L.parts < 8 && (long long)L.nd * L.parts * L.max_slots < 6 * kSplitTargetBlocks &&
-         kb >= 8 * L.parts)
+  for (;;) {
+    const long long n = (long long)L.nd * L.parts * L.max_slots;
+    if (L.parts == 8 || n >= 6 * kSplitTargetBlocks) break;
+    if (kb < (n < 2 * kSplitTargetBlocks ? 8 : 32) * L.parts) break;
     L.parts *= 2;
+  }
   return L;
 }
 
@@ -1016,7 +1069,9 @@ cudaError_t launch_few(const FewArgs& a, cudaStream_t st, const char** why) {
   r.router_blocks = (d.E + kRouterExperts - 1) / kRouterExperts;
   r.hq = a.hq; r.hqe = a.hqe;
   const int units = fp8 ? d.T * ((d.D + 127) / 128) : 0;
-  const int blocks = r.router_blocks + (units + kRouterWarps - 1) / kRouterWarps;
+  const int hq_blocks = (units + kRouterWarps - 1) / kRouterWarps;
+  const int blocks = r.router_blocks + hq_blocks;
+  r.hq_ready = a.claim + 2;
 
   FewFfn f{};
   const int es = fp8 ? 1 : 2, eb = 128 / es;
@@ -1062,6 +1117,7 @@ cudaError_t launch_few(const FewArgs& a, cudaStream_t st, const char** why) {
   f.planes = a.planes;
   f.out = a.out;
   f.claim = a.claim;
+  f.hq_blocks = hq_blocks;
   f.touched = a.touched;
   f.status = a.status;
 
