@@ -32,6 +32,12 @@
 // and 16 of W3, so every warp's lanes 0-15 hold gates and lanes 16-31 the ups
 // of the same columns, which one shuffle per pair of rows brings together.
 //
+// Large groups run on pairs of CTAs (PAIR): one product of M = 256 weight rows,
+// 128 from each CTA, whose row operand is split between the two, so a CTA
+// stages half the rows per product.  Both CTAs' loads complete on the first
+// one's barriers, it issues the products, and their completion is signalled
+// to both; each CTA writes its own scales and stores its own output columns.
+//
 // Few tiles (one row through one matrix): a cluster of CTAs shares a tile,
 // each with its own range of K-blocks, and adds the partial tiles through
 // distributed shared memory in rank order, so results do not depend on timing.
@@ -54,7 +60,7 @@ constexpr int kSfSlotCols = 12;          // 4 columns for the weights, 8 for the
 constexpr unsigned kAll = 0xffffffffu;
 
 struct alignas(64) GemmParams8 {
-  CUtensorMap x;        // [R, K] codes, box NT x 128
+  CUtensorMap x;        // [R, K] codes, box XBOX x 128
   CUtensorMap w1, w3;   // [G * N, K] codes, box 128 (plain) or 16 (gated) x 128
   const int8_t* xe;     // [R, KB]
   const int8_t* w1e;    // [G, NB, KB]
@@ -63,7 +69,7 @@ struct alignas(64) GemmParams8 {
   void* y;
   int y_bf16;
   int G, R, N, K, KB, NB;
-  int nt;               // output column tiles of a group
+  int nt;               // output column tiles of a group (PAIR: pairs of them)
   int split;            // CTAs per tile (cluster size)
   int* status;
 };
@@ -80,9 +86,13 @@ struct Tile8 {
   int g, n0, row0, rows;     // group, first output column, first row, rows
 };
 
-template <int NT>
+template <int NT, bool PAIR>
 struct Cfg {
-  static constexpr int X_BYTES = NT * kBK;
+  // rows of one TMA box of the row operand, and of a stage's share of it: a
+  // tile loads only as many boxes as its rows need
+  static constexpr int XROWS = PAIR ? NT / 2 : NT;
+  static constexpr int XBOX = PAIR ? 24 : NT < 48 ? NT : 32;
+  static constexpr int X_BYTES = XROWS * kBK;
   static constexpr int STAGE = kWTile + X_BYTES;
   static constexpr int STAGES = (200 * 1024) / STAGE < kMaxStages ? (200 * 1024) / STAGE : kMaxStages;
   static constexpr int SF_COLS = 2 * kSfSlotCols;
@@ -90,6 +100,7 @@ struct Cfg {
                                         : 2 * NT + SF_COLS <= 256 ? 256
                                                                   : 512;
   static_assert(2 * NT + SF_COLS <= 512 && NT % 16 == 0 && NT <= 240, "tensor memory columns");
+  static_assert(XROWS % XBOX == 0 && XBOX % 8 == 0 && X_BYTES % 1024 == 0, "row boxes");
 };
 
 struct Shared8 {
@@ -103,12 +114,15 @@ struct Shared8 {
   GroupMap gm;
 };
 
-template <int NT>
+template <int NT, bool PAIR>
 constexpr int smem_bytes8() {
-  return 1024 + Cfg<NT>::STAGES * Cfg<NT>::STAGE + (int)sizeof(Shared8);
+  return 1024 + Cfg<NT, PAIR>::STAGES * Cfg<NT, PAIR>::STAGE + (int)sizeof(Shared8);
 }
 
 __device__ __forceinline__ int blocks_of(int rows, int nt) { return (rows + nt - 1) / nt; }
+
+// Rows of the product's row operand: the tile's, in steps of 16.
+__device__ __forceinline__ int mma_rows(int rows) { return max(16, (rows + 15) / 16 * 16); }
 
 // One warp: checks the offsets and counts each group's row blocks.  Offsets
 // that are not increasing within [0, R] give no tiles and raise kStBounds.
@@ -146,8 +160,9 @@ __device__ void build_groups(GroupMap& gm, const GemmParams8& p, int lane) {
 
 // Tile t: groups in order, then output column tiles, row blocks fastest (the
 // CTAs that run together share weight tiles through L2).
-template <int NT, bool GATED>
-__device__ __forceinline__ Tile8 tile_at(int t, const GroupMap& gm, const GemmParams8& p) {
+// `rank`: this CTA's half of a pair's columns.
+template <int NT, bool GATED, bool PAIR>
+__device__ __forceinline__ Tile8 tile_at(int t, const GroupMap& gm, const GemmParams8& p, int rank) {
   const int q = t / p.nt;
   int lo = 0, hi = p.G - 1;
   while (lo < hi) {
@@ -161,7 +176,7 @@ __device__ __forceinline__ Tile8 tile_at(int t, const GroupMap& gm, const GemmPa
   const int b = local % nb;
   Tile8 ti;
   ti.g = lo;
-  ti.n0 = (local / nb) * (GATED ? 64 : 128);
+  ti.n0 = (PAIR ? local / nb * 2 + rank : local / nb) * (GATED ? 64 : 128);
   ti.row0 = gm.off[lo] + b * per;
   ti.rows = max(0, min(per, rows - b * per));
   return ti;
@@ -219,9 +234,9 @@ __device__ __forceinline__ void store16(const GemmParams8& p, const Tile8& ti, i
   }
 }
 
-template <int NT, bool GATED>
+template <int NT, bool GATED, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_constant__ GemmParams8 p) {
-  using C = Cfg<NT>;
+  using C = Cfg<NT, PAIR>;
   constexpr int STAGES = C::STAGES;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = ptx::smem_addr(smem_raw);
@@ -231,19 +246,26 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
 
   ptx::pdl_launch_dependents();
   if (warp == 1) {
-    ptx::tmem_alloc(&ss.tmem_base, C::TMEM_COLS);
-    ptx::tmem_relinquish();
+    if (PAIR) {
+      ptx::tmem_alloc_pair(&ss.tmem_base, C::TMEM_COLS);
+      ptx::tmem_relinquish_pair();
+    } else {
+      ptx::tmem_alloc(&ss.tmem_base, C::TMEM_COLS);
+      ptx::tmem_relinquish();
+    }
   }
   if (threadIdx.x == 0) {
+    // a pair's products wait on the first CTA's barriers, which both CTAs' scale
+    // writers and epilogues arrive on
     for (int i = 0; i < STAGES; ++i) {
       ptx::mbar_init(&ss.full[i], 1);
       ptx::mbar_init(&ss.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      ptx::mbar_init(&ss.sf_full[i], 4);
+      ptx::mbar_init(&ss.sf_full[i], PAIR ? 8 : 4);
       ptx::mbar_init(&ss.sf_empty[i], 1);
       ptx::mbar_init(&ss.acc_full[i], 1);
-      ptx::mbar_init(&ss.acc_empty[i], 4);
+      ptx::mbar_init(&ss.acc_empty[i], PAIR ? 8 : 4);
     }
     ptx::mbar_init(&ss.drain, 1);
     ss.abort = 0;
@@ -257,17 +279,20 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
   if (warp == 2) build_groups<NT>(ss.gm, p, lane);
   ptx::tc_fence_before();
   __syncthreads();
+  if (PAIR) ptx::cluster_sync();   // the barriers of both CTAs are initialised
   ptx::tc_fence_after();
 
   const uint32_t tmem = ss.tmem_base;
   const uint32_t sf_base = tmem + 2 * NT;
   volatile int* abort = &ss.abort;
-  // a cluster of `split` CTAs works on the same tiles, each on its K-blocks
-  const int rank = p.split > 1 ? (int)ptx::cluster_rank() : 0;
-  const int first = blockIdx.x / p.split, step = gridDim.x / p.split;
+  // a cluster of `split` CTAs works on the same tiles, each on its K-blocks (or,
+  // as a pair, each on its columns of all of them)
+  const int rank = p.split > 1 || PAIR ? (int)ptx::cluster_rank() : 0;
+  const int team = PAIR ? 2 : p.split;
+  const int first = blockIdx.x / team, step = gridDim.x / team;
   const int total = ss.gm.total * p.nt;
-  const int kb0 = (int)((long long)p.KB * rank / p.split);
-  const int kb1 = (int)((long long)p.KB * (rank + 1) / p.split);
+  const int kb0 = PAIR ? 0 : (int)((long long)p.KB * rank / p.split);
+  const int kb1 = PAIR ? p.KB : (int)((long long)p.KB * (rank + 1) / p.split);
   // scale words cover K-blocks 4s .. 4s + 3
   const int s0 = kb0 / 4, s1 = kb1 > kb0 ? (kb1 + 3) / 4 : s0;
 
@@ -277,46 +302,81 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
       uint32_t phase = 0, issued = 0, parity = 0;
       bool ok = true;
       for (int t = first; ok && t < total; t += step) {
-        const Tile8 ti = tile_at<NT, GATED>(t, ss.gm, p);
+        const Tile8 ti = tile_at<NT, GATED, PAIR>(t, ss.gm, p, rank);
         const int wrow = ti.g * p.N + ti.n0;
+        const int n = mma_rows(ti.rows);
+        const int xn = PAIR ? n / 2 : n;           // rows this CTA stages
+        const int xrow = ti.row0 + (PAIR ? rank * xn : 0);
+        const int boxes = (xn + C::XBOX - 1) / C::XBOX;
+        const int bytes = kWTile + boxes * C::XBOX * kBK;
         for (int kb = kb0; kb < kb1; ++kb) {
           if (!ptx::mbar_wait(&ss.empty[stage], phase ^ 1u, abort)) { ok = false; break; }
           uint8_t* sw = ring + stage * C::STAGE;
           uint64_t* bar = &ss.full[stage];
-          ptx::mbar_arrive_expect_tx(bar, C::STAGE);
-          if (GATED) {
+          if (PAIR) {
+            const uint32_t lead = ptx::map_rank(bar, 0);
+            if (rank == 0) ptx::mbar_arrive_expect_tx(bar, 2 * bytes);
+            if (GATED) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              ptx::tma_load_2d(sw + j * 4096, &p.w1, bar, kb * kBK, wrow + j * 16);
-              ptx::tma_load_2d(sw + j * 4096 + 2048, &p.w3, bar, kb * kBK, wrow + j * 16);
+              for (int j = 0; j < 4; ++j) {
+                ptx::tma_load_2d_pair(sw + j * 4096, &p.w1, lead, kb * kBK, wrow + j * 16);
+                ptx::tma_load_2d_pair(sw + j * 4096 + 2048, &p.w3, lead, kb * kBK, wrow + j * 16);
+              }
+            } else {
+              ptx::tma_load_2d_pair(sw, &p.w1, lead, kb * kBK, wrow);
             }
+            for (int j = 0; j < boxes; ++j)
+              ptx::tma_load_2d_pair(sw + kWTile + j * C::XBOX * kBK, &p.x, lead, kb * kBK,
+                                    xrow + j * C::XBOX);
           } else {
-            ptx::tma_load_2d(sw, &p.w1, bar, kb * kBK, wrow);
+            ptx::mbar_arrive_expect_tx(bar, bytes);
+            if (GATED) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                ptx::tma_load_2d(sw + j * 4096, &p.w1, bar, kb * kBK, wrow + j * 16);
+                ptx::tma_load_2d(sw + j * 4096 + 2048, &p.w3, bar, kb * kBK, wrow + j * 16);
+              }
+            } else {
+              ptx::tma_load_2d(sw, &p.w1, bar, kb * kBK, wrow);
+            }
+            for (int j = 0; j < boxes; ++j)
+              ptx::tma_load_2d(sw + kWTile + j * C::XBOX * kBK, &p.x, bar, kb * kBK,
+                               xrow + j * C::XBOX);
           }
-          ptx::tma_load_2d(sw + kWTile, &p.x, bar, kb * kBK, ti.row0);
           issued |= 1u << stage;
           parity = (parity & ~(1u << stage)) | (phase << stage);
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
       }
+      // loads in flight end before the CTA does; a pair's second CTA sees its
+      // loads' stages released (their products have read them)
       for (int s = 0; s < STAGES; ++s)
-        if (issued & (1u << s)) ffn::wait_drain(&ss.full[s], (parity >> s) & 1u, abort);
+        if (issued & (1u << s)) {
+          if (!PAIR || rank == 0) ffn::wait_drain(&ss.full[s], (parity >> s) & 1u, abort);
+          else ffn::wait_drain(&ss.empty[s], (parity >> s) & 1u, abort);
+        }
     }
   } else if (warp == 1) {
-    if (ptx::elect_one()) {
+    if ((!PAIR || rank == 0) && ptx::elect_one()) {
+      auto commit = [](uint64_t* bar) {
+        if (PAIR) ptx::mma_commit_pair(bar); else ptx::mma_commit(bar);
+      };
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        return PAIR ? ptx::mbar_wait_cluster(bar, parity, abort) : ptx::mbar_wait(bar, parity, abort);
+      };
       int stage = 0, buf = 0, slot = 0;
       uint32_t phase = 0, aphase = 0, sphase = 0;
       bool ok = true;
       for (int t = first; ok && t < total; t += step) {
-        const Tile8 ti = tile_at<NT, GATED>(t, ss.gm, p);
-        const uint32_t idesc = ptx::idesc_mxf8(128, max(16, (ti.rows + 15) / 16 * 16));
-        if (!ptx::mbar_wait(&ss.acc_empty[buf], aphase ^ 1u, abort)) break;
+        const Tile8 ti = tile_at<NT, GATED, PAIR>(t, ss.gm, p, rank);
+        const uint32_t idesc = ptx::idesc_mxf8(PAIR ? 256 : 128, mma_rows(ti.rows));
+        if (!wait(&ss.acc_empty[buf], aphase ^ 1u)) break;
         const uint32_t acc = tmem + buf * NT;
         for (int kb = kb0; kb < kb1; ++kb) {
           if (kb == kb0 || (kb & 3) == 0) {
-            if (!ptx::mbar_wait(&ss.sf_full[slot], sphase, abort)) { ok = false; break; }
+            if (!wait(&ss.sf_full[slot], sphase)) { ok = false; break; }
           }
-          if (!ptx::mbar_wait(&ss.full[stage], phase, abort)) { ok = false; break; }
+          if (!wait(&ss.full[stage], phase)) { ok = false; break; }
           ptx::tc_fence_after();
           const uint32_t sw = ptx::smem_addr(ring + stage * C::STAGE);
           const uint64_t da = ptx::smem_desc_sw128(sw);
@@ -324,21 +384,25 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
           const uint32_t id = idesc | ptx::idesc_sf_byte(kb & 3, kb & 3);
           const uint32_t sfa = sf_base + slot * kSfSlotCols, sfb = sfa + 4;
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            ptx::mma_mxf8_ss(acc, da + 2 * k, db + 2 * k, id, sfa, sfb, kb > kb0 || k > 0);
-          ptx::mma_commit(&ss.empty[stage]);
+          for (int k = 0; k < 4; ++k) {
+            if (PAIR)
+              ptx::mma_mxf8_ss_pair(acc, da + 2 * k, db + 2 * k, id, sfa, sfb, kb > kb0 || k > 0);
+            else
+              ptx::mma_mxf8_ss(acc, da + 2 * k, db + 2 * k, id, sfa, sfb, kb > kb0 || k > 0);
+          }
+          commit(&ss.empty[stage]);
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
           if ((kb & 3) == 3 || kb == kb1 - 1) {
-            ptx::mma_commit(&ss.sf_empty[slot]);
+            commit(&ss.sf_empty[slot]);
             if (++slot == 2) { slot = 0; sphase ^= 1u; }
           }
         }
         if (!ok) break;
-        ptx::mma_commit(&ss.acc_full[buf]);
+        commit(&ss.acc_full[buf]);
         if (++buf == 2) { buf = 0; aphase ^= 1u; }
       }
-      // nothing of this CTA is in flight when its tensor memory is freed
-      ptx::mma_commit(&ss.drain);
+      // nothing is in flight when tensor memory is freed
+      commit(&ss.drain);
       ffn::wait_drain(&ss.drain, 0, abort);
     }
   } else if (warp < 6) {
@@ -346,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
     int buf = 0;
     uint32_t aphase = 0;
     for (int t = first; t < total; t += step) {
-      const Tile8 ti = tile_at<NT, GATED>(t, ss.gm, p);
+      const Tile8 ti = tile_at<NT, GATED, PAIR>(t, ss.gm, p, rank);
       if (__any_sync(kAll, !ptx::mbar_wait(&ss.acc_full[buf], aphase, abort))) break;
       ptx::tc_fence_after();
       const uint32_t acc = tmem + buf * NT + ((uint32_t)(q * 32) << 16);
@@ -369,7 +433,10 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
       }
       ptx::tc_fence_before();
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(&ss.acc_empty[buf]);
+      if (lane == 0) {
+        if (PAIR) ptx::mbar_arrive_cluster(ptx::map_rank(&ss.acc_empty[buf], 0));
+        else ptx::mbar_arrive(&ss.acc_empty[buf]);
+      }
       if (++buf == 2) { buf = 0; aphase ^= 1u; }
     }
   } else {
@@ -378,9 +445,10 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
     uint32_t sphase = 0;
     bool bad = false, ok = true;
     for (int t = first; ok && t < total; t += step) {
-      const Tile8 ti = tile_at<NT, GATED>(t, ss.gm, p);
+      const Tile8 ti = tile_at<NT, GATED, PAIR>(t, ss.gm, p, rank);
+      // (a pair's second tile may lie behind the last column: any scale will do)
       const int8_t* we = (GATED && (lane & 16) ? p.w3e : p.w1e) +
-                         ((size_t)ti.g * p.NB + ti.n0 / 128) * p.KB;
+                         ((size_t)ti.g * p.NB + min(ti.n0 / 128, p.NB - 1)) * p.KB;
       constexpr int XC = (NT + 31) / 32;
       for (int s = s0; s < s1; ++s) {
         uint32_t wa[4], wx[8] = {0, 0, 0, 0, 0, 0, 0, 0};
@@ -402,7 +470,10 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&ss.sf_full[slot]);
+        if (lane == 0) {
+          if (PAIR) ptx::mbar_arrive_cluster(ptx::map_rank(&ss.sf_full[slot], 0));
+          else ptx::mbar_arrive(&ss.sf_full[slot]);
+        }
         if (++slot == 2) { slot = 0; sphase ^= 1u; }
       }
     }
@@ -410,11 +481,12 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
   }
 
   __syncthreads();
-  if (p.split > 1) {
+  if (PAIR) ptx::cluster_sync();   // neither CTA leaves while the other uses its memory
+  if (!PAIR && p.split > 1) {
     // partial tiles -> outputs: rank r finishes the rows r, r + split, ...
     ptx::cluster_sync();
     if (first < total && !*abort) {
-      const Tile8 ti = tile_at<NT, GATED>(first, ss.gm, p);
+      const Tile8 ti = tile_at<NT, GATED, PAIR>(first, ss.gm, p, rank);
       const uint32_t part = ptx::smem_addr(ring);
       if (GATED) {
         for (int i = threadIdx.x; i < ti.rows * 64; i += kThreads) {
@@ -446,41 +518,45 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
     }
     ptx::cluster_sync();   // no CTA leaves while another reads its part
   }
-  if (warp == 1) ptx::tmem_dealloc(tmem, C::TMEM_COLS);
+  if (warp == 1) {
+    if (PAIR) ptx::tmem_dealloc_pair(tmem, C::TMEM_COLS);
+    else ptx::tmem_dealloc(tmem, C::TMEM_COLS);
+  }
   if (threadIdx.x == 0 && p.status) {
     if (ss.abort) atomicOr(p.status, kStTimeout);
     if (ss.bad) atomicOr(p.status, kStBounds);
   }
 }
 
-template <int NT, bool GATED>
+template <int NT, bool GATED, bool PAIR>
 cudaError_t launch_nt(const GemmParams8& p, long long tiles, cudaStream_t st) {
+  constexpr int smem = smem_bytes8<NT, PAIR>();
   static std::atomic<uint64_t> smem_set{0};
-  cudaError_t e = set_smem_once(gemm_fp8_kernel<NT, GATED>, smem_bytes8<NT>(), smem_set);
+  cudaError_t e = set_smem_once(gemm_fp8_kernel<NT, GATED, PAIR>, smem, smem_set);
   if (e != cudaSuccess) return e;
-  const int sms = num_sms();
-  const long long want = tiles * p.split;
+  const int team = PAIR ? 2 : p.split;
+  const long long want = tiles * team, sms = num_sms() / team * team;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(p.split > 1 ? want : want < sms ? want : sms));
+  cfg.gridDim = dim3((unsigned)(p.split > 1 ? want : std::min(want, sms)));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem_bytes8<NT>();
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = p.split;
+  attr[1].val.clusterDim.x = team;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, gemm_fp8_kernel<NT, GATED>, p);
+  return cudaLaunchKernelEx(&cfg, gemm_fp8_kernel<NT, GATED, PAIR>, p);
 }
 
-template <int NT>
+template <int NT, bool PAIR>
 cudaError_t launch_any(GemmParams8& p, bool gated, cudaStream_t st, const char** why,
                        const Gemm8Args& a) {
   const uint32_t box = gated ? 16 : 128;
-  bool ok = make_tensor_map(&p.x, a.x, a.R, a.K, NT, kBK, 1, 128) &&
+  bool ok = make_tensor_map(&p.x, a.x, a.R, a.K, Cfg<NT, PAIR>::XBOX, kBK, 1, 128) &&
             make_tensor_map(&p.w1, a.W1, (uint64_t)a.G * a.N, a.K, box, kBK, 1, 128);
   p.w3 = p.w1;
   if (ok && gated) ok = make_tensor_map(&p.w3, a.W3, (uint64_t)a.G * a.N, a.K, box, kBK, 1, 128);
@@ -488,14 +564,17 @@ cudaError_t launch_any(GemmParams8& p, bool gated, cudaStream_t st, const char**
     *why = "cuTensorMapEncodeTiled failed for a product operand";
     return cudaErrorInvalidValue;
   }
+  p.nt = gated ? (a.N + 63) / 64 : (a.N + 127) / 128;
+  if (PAIR) p.nt = (p.nt + 1) / 2;
   // row blocks: at most one per group with rows, and one per NT rows
   const long long blocks = std::min<long long>(a.R, (long long)a.R / NT + std::min(a.G, a.R));
   const long long tiles = blocks * p.nt;
   // Few tiles: split K over a cluster while that leaves every CTA an SM of its
   // own and at least two K-blocks.
   p.split = 1;
-  while (p.split < 8 && tiles * p.split * 2 <= num_sms() && p.KB >= p.split * 4) p.split *= 2;
-  return gated ? launch_nt<NT, true>(p, tiles, st) : launch_nt<NT, false>(p, tiles, st);
+  if (!PAIR)
+    while (p.split < 8 && tiles * p.split * 2 <= num_sms() && p.KB >= p.split * 4) p.split *= 2;
+  return gated ? launch_nt<NT, true, PAIR>(p, tiles, st) : launch_nt<NT, false, PAIR>(p, tiles, st);
 }
 
 }  // namespace
@@ -512,15 +591,15 @@ cudaError_t launch_gemm_fp8(const Gemm8Args& a, cudaStream_t st, const char** wh
   p.G = a.G; p.R = a.R; p.N = a.N; p.K = a.K;
   p.KB = (a.K + 127) / 128;
   p.NB = (a.N + 127) / 128;
-  p.nt = gated ? (a.N + 63) / 64 : (a.N + 127) / 128;
   p.status = a.status;
   *why = "product launch";
   // Rows per tile by the average group: small groups leave the weight stream
-  // in charge, so the ring holds weights; large ones are bound by the products.
+  // in charge, so the ring holds weights; large ones are bound by the products
+  // and by what the SMs read from L2, which pairs of CTAs halve for the rows.
   const int avg = a.R / a.G;
-  if (avg <= 16) return launch_any<32>(p, gated, st, why, a);
-  if (avg <= 96) return launch_any<128>(p, gated, st, why, a);
-  return launch_any<240>(p, gated, st, why, a);
+  if (avg <= 16) return launch_any<32, false>(p, gated, st, why, a);
+  if (avg <= 64) return launch_any<128, false>(p, gated, st, why, a);
+  return launch_any<240, true>(p, gated, st, why, a);
 }
 
 }  // namespace moe
