@@ -398,6 +398,7 @@ struct FewShared {
   uint64_t acc_full[2], acc_empty[2];
   uint64_t q_full[kQueue], q_empty[kQueue];
   uint64_t drain;
+  uint64_t epi;          // barrier of the four epilogue warps
   Unit q[kQueue];
   uint32_t tmem_base;
   int abort, bad, last, exit_last;
@@ -444,9 +445,6 @@ __device__ __forceinline__ int32_t* out_ticket(const FewFfn& p, int d) {
 __device__ __forceinline__ int slot_target(const FewFfn& p, int slot) {
   return 4 * (slot < p.S ? p.nts : p.ntr);
 }
-
-// Barrier of the four epilogue warps alone.
-__device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
 // Waits, whole warp, until a slot's activations are stored; every lane acquires.
 __device__ __forceinline__ bool slot_wait(const FewFfn& p, int slot, volatile int* abort) {
@@ -548,6 +546,7 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
       ptx::mbar_init(&ss.q_empty[i], 1 + 1 + 4 + (FP8 ? 4 : 0));
     }
     ptx::mbar_init(&ss.drain, 1);
+    ptx::mbar_init(&ss.epi, 4);
     ss.abort = 0;
     ss.bad = 0;
     ptx::fence_barrier_init();
@@ -768,6 +767,7 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
     const uint32_t lanes = (uint32_t)(qt * 32) << 16;
     QueueReader q;
     Unit u;
+    ptx::WarpBarrier epi{&ss.epi};
     bool waited = false;
     int buf = 0;
     uint32_t cph = 0;
@@ -847,7 +847,7 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
         }
         if (FP8) {
           // 32 features of a token per warp and round: exponent, then the pieces
-          epi_sync();
+          if (!epi.sync(abort, lane)) break;
           int8_t* ae = sh ? p.ae_s : p.ae_r;
           const int stride = (F + 127) / 128 * 4;   // exponents of a row
           for (int i = qt; i < p.T * (fpt / 32); i += 4) {
@@ -869,7 +869,8 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
               if (fb + lane < F) dst[(size_t)c * p.T * F] = (uint8_t)(odd ? 0x7fu : code);
             }
           }
-          epi_sync();   // the tile's activations are read: the next may be written
+          // the tile's activations are read: the next may be written
+          if (!epi.sync(abort, lane)) break;
         }
         // the stores become visible to the whole GPU and to TMA, then the count
         ptx::fence_proxy_async_global();
@@ -885,15 +886,15 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
             if ((mask >> t) & 1u) plane[(size_t)t * p.D] = v[t];
         }
         __threadfence();
-        epi_sync();
+        if (!epi.sync(abort, lane)) break;
         if (qt == 0 && lane == 0) {
           const int all = (p.S + __ldcg(p.nslots)) * p.parts;
           const int got = ptx::atom_add_acq_rel_gpu(out_ticket(p, u.at), 1);
           ss.last = got == all - 1;
           if (ss.last) *out_ticket(p, u.at) = 0;
         }
-        epi_sync();
-        if (ss.last) {
+        if (!epi.sync(abort, lane)) break;
+        if (*reinterpret_cast<volatile int*>(&ss.last)) {
           __threadfence();
           merge_block(p, ss, u.at, threadIdx.x - 128);
         }

@@ -24,10 +24,12 @@
 //   warp 1      TMEM allocator and MMA issuer (one elected thread)
 //   warps 2-5   epilogue: TMEM -> registers -> global; two accumulators, so
 //               a tile's epilogue overlaps the next tile's products
-//   warps 6-9   scale writers: the exponents of four K-blocks at a time, as
-//               32-bit words of four E8M0 bytes, into one of two TMEM slots;
-//               each of the four warps fills its lane quarter with the same
-//               words, as the tensor core expects them
+//   warps 6-9   scale writers: the exponents of sixteen K-blocks at a time,
+//               loaded a row per thread while the sixteen before them are in
+//               use, exchanged through shared memory, and written as 32-bit
+//               words of four E8M0 bytes into one of two TMEM slots; each of
+//               the four warps fills its lane quarter with the same words, as
+//               the tensor core expects them
 // Gated tiles hold 64 output columns: the 128 weight rows alternate 16 of W1
 // and 16 of W3, so every warp's lanes 0-15 hold gates and lanes 16-31 the ups
 // of the same columns, which one shuffle per pair of rows brings together.
@@ -108,9 +110,11 @@ struct Shared8 {
   uint64_t sf_full[2], sf_empty[2];
   uint64_t acc_full[2], acc_empty[2];
   uint64_t drain;
+  uint64_t sf_bar;             // barrier of the four scale warps
   uint32_t tmem_base;
   int abort;
   int bad;
+  uint32_t sf_rows[2][4][256]; // scale words of sixteen K-blocks [set][row]
   GroupMap gm;
 };
 
@@ -182,18 +186,24 @@ __device__ __forceinline__ Tile8 tile_at(int t, const GroupMap& gm, const GemmPa
   return ti;
 }
 
-// Four E8M0 bytes of one row: exponents 4s .. 4s + 3 of its KB.  -128 has no
-// E8M0 counterpart (its byte would be the NaN scale).
-__device__ __forceinline__ uint32_t sf_word(const int8_t* e, int s, int KB, bool* bad) {
-  uint32_t w = 0;
-  const int8_t* q = e + 4 * s;
-  if (((reinterpret_cast<uintptr_t>(q) & 3u) == 0) && 4 * s + 4 <= KB) {
-    w = *reinterpret_cast<const uint32_t*>(q);
-  } else {
+// Exponents q[0 .. n-1] (n <= 16) as they stand in memory, in words of four.
+// Any alignment: the aligned words that hold them are loaded and shifted.
+__device__ __forceinline__ void load_exps(const int8_t* q, int n, uint32_t (&w)[4]) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(q);
+  const uint32_t* base = reinterpret_cast<const uint32_t*>(at & ~(uintptr_t)3);
+  const int off = (int)(at & 3);
+  uint32_t v[5];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (4 * s + i < KB) w |= (uint32_t)(uint8_t)q[i] << (8 * i);
-  }
+  for (int i = 0; i < 5; ++i) v[i] = 4 * i - off < n ? __ldg(base + i) : 0u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(v[i], v[i + 1], 8 * off);
+}
+
+// Word i of n exponents -> E8M0 bytes.  -128 has no E8M0 counterpart (its byte
+// would be the NaN scale).
+__device__ __forceinline__ uint32_t scale_bytes(uint32_t w, int i, int n, bool* bad) {
+  const int left = n - 4 * i;
+  if (left < 4) w &= left > 0 ? (1u << (8 * left)) - 1u : 0u;
   *bad |= __vcmpeq4(w, 0x80808080u) != 0;
   return __vadd4(w, 0x7f7f7f7fu);
 }
@@ -268,6 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
       ptx::mbar_init(&ss.acc_empty[i], PAIR ? 8 : 4);
     }
     ptx::mbar_init(&ss.drain, 1);
+    ptx::mbar_init(&ss.sf_bar, 4);
     ss.abort = 0;
     ss.bad = 0;
     ptx::fence_barrier_init();
@@ -440,31 +451,76 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
       if (++buf == 2) { buf = 0; aphase ^= 1u; }
     }
   } else {
-    const int q = warp & 3;
-    int slot = 0;
+    constexpr int RPT = (NT + 127) / 128;      // rows per thread
+    constexpr int XC = (NT + 31) / 32;         // scale columns of the rows
+    const int tid = threadIdx.x - 192;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    ptx::WarpBarrier team_bar{&ss.sf_bar};
+    int slot = 0, sbuf = 0;
     uint32_t sphase = 0;
     bool bad = false, ok = true;
-    for (int t = first; ok && t < total; t += step) {
-      const Tile8 ti = tile_at<NT, GATED, PAIR>(t, ss.gm, p, rank);
-      // (a pair's second tile may lie behind the last column: any scale will do)
-      const int8_t* we = (GATED && (lane & 16) ? p.w3e : p.w1e) +
-                         ((size_t)ti.g * p.NB + min(ti.n0 / 128, p.NB - 1)) * p.KB;
-      constexpr int XC = (NT + 31) / 32;
-      for (int s = s0; s < s1; ++s) {
-        uint32_t wa[4], wx[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        wa[0] = wa[1] = wa[2] = wa[3] = sf_word(we, s, p.KB, &bad);
+    // chunk c: K-blocks 16 c .. 16 c + 15, scale sets 4 c .. 4 c + 3
+    const int c0 = s0 / 4, c1 = (s1 + 3) / 4;
+    uint32_t xw[RPT][4], ww[4];
+    auto load = [&](const Tile8& ti, int c) {
+      const int n = min(16, p.KB - 16 * c);
 #pragma unroll
-        for (int c = 0; c < XC; ++c)
-          if (c * 32 + lane < ti.rows)
-            wx[c] = sf_word(p.xe + (size_t)(ti.row0 + c * 32 + lane) * p.KB, s, p.KB, &bad);
+      for (int i = 0; i < RPT; ++i) {
+        const int r = tid + 128 * i;
+        if (r < ti.rows) load_exps(p.xe + (size_t)(ti.row0 + r) * p.KB + 16 * c, n, xw[i]);
+      }
+      // (a pair's second tile may lie behind the last column: any scale will do)
+      load_exps((GATED && (lane & 16) ? p.w3e : p.w1e) +
+                    ((size_t)ti.g * p.NB + min(ti.n0 / 128, p.NB - 1)) * p.KB + 16 * c,
+                n, ww);
+    };
+    int t = first, c = c0;
+    Tile8 ti{};
+    if (t < total) {
+      ti = tile_at<NT, GATED, PAIR>(t, ss.gm, p, rank);
+      load(ti, c);
+    }
+    while (ok && t < total) {
+      const int n = min(16, p.KB - 16 * c);
+      uint32_t wa[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) wa[i] = scale_bytes(ww[i], i, n, &bad);
+#pragma unroll
+      for (int i = 0; i < RPT; ++i) {
+        const int r = tid + 128 * i;
+        if (r < ti.rows) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) ss.sf_rows[sbuf][j][r] = scale_bytes(xw[i][j], j, n, &bad);
+        }
+      }
+      const int rows = ti.rows;
+      const int beg = max(4 * c, s0), end = min(4 * c + 4, s1);
+      const int cur = 4 * c;
+      // the next chunk's exponents are on their way while this one is used
+      if (++c == c1) {
+        c = c0;
+        t += step;
+        if (t < total) ti = tile_at<NT, GATED, PAIR>(t, ss.gm, p, rank);
+      }
+      if (t < total) load(ti, c);
+      if (!team_bar.sync(abort, lane)) break;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int s = cur + j;
+        if (s < beg || s >= end) continue;
+        uint32_t wx[8];
+#pragma unroll
+        for (int i = 0; i < XC; ++i) wx[i] = ss.sf_rows[sbuf][j][i * 32 + lane];
         if (__any_sync(kAll, !ptx::mbar_wait(&ss.sf_empty[slot], sphase ^ 1u, abort))) {
           ok = false;
           break;
         }
         ptx::tc_fence_after();
-        const uint32_t dst = sf_base + slot * kSfSlotCols + ((uint32_t)(q * 32) << 16);
-        ptx::tmem_st_x4(dst, wa);
-        if (XC > 4) ptx::tmem_st_x8(dst + 4, wx);
+        const uint32_t dst = sf_base + slot * kSfSlotCols + lanes;
+        const uint32_t w4[4] = {wa[j], wa[j], wa[j], wa[j]};
+        ptx::tmem_st_x4(dst, w4);
+        // (words of rows behind the tile's last are whatever stood there)
+        if (XC > 4 && rows > 128) ptx::tmem_st_x8(dst + 4, wx);
         else if (XC > 1) ptx::tmem_st_x4(dst + 4, wx);
         else ptx::tmem_st_x1(dst + 4, wx[0]);
         ptx::tmem_wait_st();
@@ -476,6 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
         }
         if (++slot == 2) { slot = 0; sphase ^= 1u; }
       }
+      sbuf ^= 1;
     }
     if (bad) ss.bad = 1;
   }

@@ -111,6 +111,22 @@ __device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const uint32_t* r) {
       : "memory");
 }
 
+// A barrier of a few warps whose wait is bounded: an mbarrier that one lane of
+// each warp arrives on.  False when the wait gave up (as mbar_wait).
+struct WarpBarrier {
+  uint64_t* bar;
+  uint32_t phase = 0;
+  __device__ __forceinline__ bool sync(volatile int* abort, int lane) {
+    __syncwarp();
+    if (lane == 0)
+      asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar))
+                   : "memory");
+    const bool ok = mbar_wait(bar, phase, abort);
+    phase ^= 1u;
+    return !__any_sync(0xffffffffu, !ok);
+  }
+};
+
 // ---------------------------------------------------------------------------
 // Clusters
 // ---------------------------------------------------------------------------
