@@ -120,9 +120,18 @@ def _check(rc: int) -> None:
         raise MoeError(rc, _lib.moe_last_error().decode())
 
 
+def _device() -> int:
+    """The current device's index (-2, which no tensor has, without a device)."""
+    try:
+        return torch._C._cuda_getDevice()
+    except (RuntimeError, AttributeError):
+        return -2
+
+
 def _stream(stream) -> int:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # the current stream's handle without building a torch.cuda.Stream (3 us a call)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return getattr(stream, "cuda_stream", stream)
 
 
@@ -245,49 +254,41 @@ def moe_forward_fp8(h, Wr, bias, w8: moe_fp8_weights_t, d, out, ws, idx_out=None
                                 _ptr(w_out, torch.float32, "w_out"), wp, wn, _stream(stream)))
 
 
-def _few_shapes(h, Wr, bias, d, out, idx_out, w_out) -> None:
-    _shape(h, (d.T, d.D), "h")
-    _shape(Wr, (d.E, d.D), "Wr")
-    _shape(bias, (d.E,), "bias")
-    _shape(out, (d.T, d.D), "out")
-    for t, name in ((idx_out, "idx_out"), (w_out, "w_out")):
-        if t is not None:
-            _shape(t, (d.T, d.k), name)
+def _few_routing(h, Wr, bias, d, dev):
+    return (_arg(h, torch.bfloat16, (d.T, d.D), dev, "h"),
+            _arg(Wr, torch.float32, (d.E, d.D), dev, "Wr"),
+            _arg(bias, torch.float32, (d.E,), dev, "bias"))
+
+
+def _few_outputs(d, out, idx_out, w_out, ws, dev):
+    return (_arg(out, torch.float32, (d.T, d.D), dev, "out"),
+            None if idx_out is None else _arg(idx_out, torch.int32, (d.T, d.k), dev, "idx_out"),
+            None if w_out is None else _arg(w_out, torch.float32, (d.T, d.k), dev, "w_out"),
+            *_ws_arg(ws, dev))
 
 
 def moe_forward_few(h, Wr, bias, W1, W3, W2, Ws1, Ws3, Ws2, d, out, ws, idx_out=None, w_out=None,
                     stream=None) -> None:
-    """moe_forward for at most 16 tokens, in two kernels (arguments as moe_forward)."""
-    _few_shapes(h, Wr, bias, d, out, idx_out, w_out)
-    for t, n, want in ((W1, "W1", (d.E, d.F, d.D)), (W3, "W3", (d.E, d.F, d.D)),
-                       (W2, "W2", (d.E, d.D, d.F))):
-        _shape(t, want, n)
-    if d.S:
-        for t, n, want in ((Ws1, "Ws1", (d.S, d.Fs, d.D)), (Ws3, "Ws3", (d.S, d.Fs, d.D)),
-                           (Ws2, "Ws2", (d.S, d.D, d.Fs))):
-            _shape(t, want, n)
-    wp, wn = _ws(ws)
-    bf = torch.bfloat16
-    args = (_ptr(h, bf, "h"), _ptr(Wr, torch.float32, "Wr"), _ptr(bias, torch.float32, "bias"),
-            _ptr(W1, bf, "W1"), _ptr(W3, bf, "W3"), _ptr(W2, bf, "W2"), _ptr(Ws1, bf, "Ws1"),
-            _ptr(Ws3, bf, "Ws3"), _ptr(Ws2, bf, "Ws2"), ctypes.byref(d),
-            _ptr(out, torch.float32, "out"), _ptr(idx_out, torch.int32, "idx_out"),
-            _ptr(w_out, torch.float32, "w_out"), wp, wn)
-    _same_device(h, Wr, bias, W1, W3, W2, *((Ws1, Ws3, Ws2) if d.S else ()), out, idx_out, w_out, ws)
-    _check(_lib.moe_forward_few(*args, _stream(stream)))
+    """moe_forward for at most 16 tokens, in two kernels (arguments as moe_forward;
+    Ws1, Ws3 and Ws2 are not looked at when d.S is 0)."""
+    dev = _device()
+    bf, E, D, F, S, Fs = torch.bfloat16, d.E, d.D, d.F, d.S, d.Fs
+    shared = (None, None, None) if not S else (_arg(Ws1, bf, (S, Fs, D), dev, "Ws1"),
+                                               _arg(Ws3, bf, (S, Fs, D), dev, "Ws3"),
+                                               _arg(Ws2, bf, (S, D, Fs), dev, "Ws2"))
+    _check(_lib.moe_forward_few(*_few_routing(h, Wr, bias, d, dev), _arg(W1, bf, (E, F, D), dev, "W1"),
+                                _arg(W3, bf, (E, F, D), dev, "W3"), _arg(W2, bf, (E, D, F), dev, "W2"),
+                                *shared, ctypes.byref(d),
+                                *_few_outputs(d, out, idx_out, w_out, ws, dev), _stream(stream)))
 
 
 def moe_forward_few_fp8(h, Wr, bias, w8: moe_fp8_weights_t, d, out, ws, idx_out=None, w_out=None,
                         stream=None) -> None:
     """moe_forward_fp8 for at most 16 tokens, in two kernels (arguments as moe_forward_fp8)."""
-    _few_shapes(h, Wr, bias, d, out, idx_out, w_out)
-    wp, wn = _ws(ws)
-    args = (_ptr(h, torch.bfloat16, "h"), _ptr(Wr, torch.float32, "Wr"),
-            _ptr(bias, torch.float32, "bias"), ctypes.byref(w8), ctypes.byref(d),
-            _ptr(out, torch.float32, "out"), _ptr(idx_out, torch.int32, "idx_out"),
-            _ptr(w_out, torch.float32, "w_out"), wp, wn)
-    _same_device(h, Wr, bias, out, idx_out, w_out, ws)
-    _check(_lib.moe_forward_few_fp8(*args, _stream(stream)))
+    dev = _device()
+    _check(_lib.moe_forward_few_fp8(*_few_routing(h, Wr, bias, d, dev), ctypes.byref(w8),
+                                    ctypes.byref(d), *_few_outputs(d, out, idx_out, w_out, ws, dev),
+                                    _stream(stream)))
 
 
 def moe_fp8_dequantize(codes, exps, out, ws=None, stream=None) -> None:
@@ -304,84 +305,94 @@ def moe_fp8_dequantize(codes, exps, out, ws=None, stream=None) -> None:
                                    _stream(stream)))
 
 
-def _same_device(first: torch.Tensor, *rest: Optional[torch.Tensor]) -> None:
-    """The kernels run on the current device: every tensor has to live there."""
-    dev = first.get_device()
-    if dev != torch.cuda.current_device():
-        raise ValueError(f"tensors on cuda:{dev}, but the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
-    for t in rest:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"tensors on cuda:{dev} and {t.device}: expected one device")
+def _arg(t: torch.Tensor, dtype, shape, dev: int, name: str) -> int:
+    """Address of a contiguous tensor of this type and shape on device `dev` (the
+    current one, which the kernels run on), or the error it deserves.  One test
+    per property on the way that every call takes: checks are most of a small
+    call's host time."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a tensor, got {type(t).__name__}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: expected a CUDA tensor")
+    raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{dev}")
 
 
-def _shape(t: torch.Tensor, want, name: str) -> None:
-    if tuple(t.shape) != tuple(want):
-        raise ValueError(f"{name}: expected shape {tuple(want)}, got {tuple(t.shape)}")
+def _codes(t: torch.Tensor, shape, dev: int, name: str) -> int:
+    """_arg of E4M3 codes, as either of their types."""
+    if t.dtype in _CODE_DTYPES:
+        return _arg(t, t.dtype, shape, dev, name)
+    raise TypeError(f"{name}: expected uint8 or float8_e4m3fn codes, got {t.dtype}")
 
 
-def _blocks(n: int) -> int:
-    return (n + 127) // 128
+def _ws_arg(ws: Optional[torch.Tensor], dev: int):
+    if ws is None:
+        return None, 0
+    n = ws.numel()
+    return _arg(ws, torch.uint8, (n,), dev, "ws"), n
 
 
 def moe_quantize_fp8(x, codes, exps, idx=None, ws=None, stream=None) -> None:
     """x [src, K] bf16 -> codes [R, K] E4M3 (uint8 or float8_e4m3fn) and exps
     [R, ceil(K/128)] int8 of the rows x[idx] (idx [R] int32; None: of x itself)."""
-    if x.dim() != 2 or codes.dim() != 2:
-        raise ValueError("x [src, K] and codes [R, K] expected")
-    R, K = codes.shape
-    _shape(codes, (x.shape[0] if idx is None else idx.numel(), x.shape[1]), "codes")
-    _shape(exps, (R, _blocks(K)), "exps")
-    args = (_ptr(x, torch.bfloat16, "x"), x.shape[0], _ptr(idx, torch.int32, "idx"), R, K,
-            _code_ptr(codes, "codes"), _ptr(exps, torch.int8, "exps"), _ws(ws)[0])
-    _same_device(x, codes, exps, idx, ws)
-    _check(_lib.moe_quantize_fp8(*args, _stream(stream)))
+    if x.dim() != 2:
+        raise ValueError("x [src, K] expected")
+    src, K = x.shape
+    R = src if idx is None else idx.numel()
+    dev = _device()
+    _check(_lib.moe_quantize_fp8(
+        _arg(x, torch.bfloat16, (src, K), dev, "x"), src,
+        None if idx is None else _arg(idx, torch.int32, (R,), dev, "idx"), R, K,
+        _codes(codes, (R, K), dev, "codes"),
+        _arg(exps, torch.int8, (R, (K + 127) // 128), dev, "exps"), _ws_arg(ws, dev)[0],
+        _stream(stream)))
 
 
-def _gemm_fp8_args(x, xe, W, We, out, offsets):
+def _product_sizes(x, W):
     if x.dim() != 2 or W.dim() not in (2, 3):
         raise ValueError("x [R, K] and W [G, N, K] (or [N, K]) expected")
     R, K = x.shape
     G, N = (1, W.shape[0]) if W.dim() == 2 else W.shape[:2]
-    _shape(xe, (R, _blocks(K)), "xe")
-    _shape(out, (R, N), "output")
-    if offsets is not None:
-        _shape(offsets, (G + 1,), "offsets")
-    return G, R, N, K
-
-
-def _weight_fp8_shape(W, We, G: int, N: int, K: int, name: str) -> None:
-    _shape(W, (N, K) if W.dim() == 2 and G == 1 else (G, N, K), name)
-    _shape(We, (_blocks(N), _blocks(K)) if We.dim() == 2 and G == 1 else
-           (G, _blocks(N), _blocks(K)), name + "e")
+    # weights may come as [N, K] and their exponents as [NB, KB] when there is one group
+    lead = () if W.dim() == 2 else (G,)
+    return G, R, N, K, lead, (*lead, (N + 127) // 128, (K + 127) // 128)
 
 
 def moe_grouped_gemm_fp8(x, xe, W, We, y, offsets=None, ws=None, stream=None) -> None:
     """x [R, K] codes with exponents xe [R, ceil(K/128)], W [G, N, K] codes with
     We [G, ceil(N/128), ceil(K/128)] -> y [R, N] fp32 or bf16 (its dtype chooses);
-    offsets [G + 1] int32 (None: one group of all rows)."""
-    G, R, N, K = _gemm_fp8_args(x, xe, W, We, y, offsets)
+    offsets [G + 1] int32 (None: one group of all rows).  With one group W and We
+    may come without the leading 1."""
+    G, R, N, K, lead, eshape = _product_sizes(x, W)
     if y.dtype not in (torch.float32, torch.bfloat16):
         raise TypeError(f"y: expected float32 or bfloat16, got {y.dtype}")
-    _weight_fp8_shape(W, We, G, N, K, "W")
-    args = (_code_ptr(x, "x"), _ptr(xe, torch.int8, "xe"), _ptr(offsets, torch.int32, "offsets"),
-            _code_ptr(W, "W"), _ptr(We, torch.int8, "We"), G, R, N, K, _ptr(y, None, "y"),
-            int(y.dtype == torch.bfloat16), _ws(ws)[0])
-    _same_device(x, xe, W, We, y, offsets, ws)
-    _check(_lib.moe_grouped_gemm_fp8(*args, _stream(stream)))
+    dev = _device()
+    _check(_lib.moe_grouped_gemm_fp8(
+        _codes(x, (R, K), dev, "x"), _arg(xe, torch.int8, (R, eshape[-1]), dev, "xe"),
+        None if offsets is None else _arg(offsets, torch.int32, (G + 1,), dev, "offsets"),
+        _codes(W, (*lead, N, K), dev, "W"), _arg(We, torch.int8, eshape, dev, "We"), G, R, N, K,
+        _arg(y, y.dtype, (R, N), dev, "y"), int(y.dtype is torch.bfloat16), _ws_arg(ws, dev)[0],
+        _stream(stream)))
 
 
 def moe_gated_gemm_fp8(x, xe, W1, W1e, W3, W3e, act, offsets=None, ws=None, stream=None) -> None:
     """silu(x W1^T) * (x W3^T) per group -> act [R, N] bf16; operands as
     moe_grouped_gemm_fp8, W3 and W3e shaped like W1 and W1e."""
-    G, R, N, K = _gemm_fp8_args(x, xe, W1, W1e, act, offsets)
-    _weight_fp8_shape(W1, W1e, G, N, K, "W1")
-    _weight_fp8_shape(W3, W3e, G, N, K, "W3")
-    args = (_code_ptr(x, "x"), _ptr(xe, torch.int8, "xe"), _ptr(offsets, torch.int32, "offsets"),
-            _code_ptr(W1, "W1"), _ptr(W1e, torch.int8, "W1e"), _code_ptr(W3, "W3"),
-            _ptr(W3e, torch.int8, "W3e"), G, R, N, K, _ptr(act, torch.bfloat16, "act"), _ws(ws)[0])
-    _same_device(x, xe, W1, W1e, W3, W3e, act, offsets, ws)
-    _check(_lib.moe_gated_gemm_fp8(*args, _stream(stream)))
+    G, R, N, K, lead, eshape = _product_sizes(x, W1)
+    dev = _device()
+    _check(_lib.moe_gated_gemm_fp8(
+        _codes(x, (R, K), dev, "x"), _arg(xe, torch.int8, (R, eshape[-1]), dev, "xe"),
+        None if offsets is None else _arg(offsets, torch.int32, (G + 1,), dev, "offsets"),
+        _codes(W1, (*lead, N, K), dev, "W1"), _arg(W1e, torch.int8, eshape, dev, "W1e"),
+        _codes(W3, (*lead, N, K), dev, "W3"), _arg(W3e, torch.int8, eshape, dev, "W3e"), G, R, N, K,
+        _arg(act, torch.bfloat16, (R, N), dev, "act"), _ws_arg(ws, dev)[0], _stream(stream)))
 
 
 def moe_gather_rows(src, idx, dst, ws=None, stream=None) -> None:

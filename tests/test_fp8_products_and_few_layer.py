@@ -123,32 +123,78 @@ def test_few_layer_counters_stand_still_over_T(mod):
     assert max(sizes) == sizes[-1]
 
 
-def test_binding_refusals(mod):
-    """Shapes and types are checked before any device is needed."""
-    bf, u8, i8 = torch.bfloat16, torch.uint8, torch.int8
-    x, c, e = torch.zeros(4, 256, dtype=bf), torch.zeros(4, 256, dtype=u8), torch.zeros(4, 2, dtype=i8)
-    with pytest.raises(ValueError, match="codes"):
-        mod.moe_quantize_fp8(x, c[:3], e)
-    with pytest.raises(ValueError, match="exps"):
-        mod.moe_quantize_fp8(x, c, e[:, :1])
-    with pytest.raises(TypeError, match="x"):
-        mod.moe_quantize_fp8(x.float(), c, e)
-    W, We, y = torch.zeros(3, 64, 256, dtype=u8), torch.zeros(3, 1, 2, dtype=i8), torch.zeros(4, 64)
-    off = torch.zeros(4, dtype=torch.int32)
-    with pytest.raises(ValueError, match="output"):
-        mod.moe_grouped_gemm_fp8(c, e, W, We, y[:, :32], offsets=off)
-    with pytest.raises(ValueError, match="offsets"):
-        mod.moe_grouped_gemm_fp8(c, e, W, We, y, offsets=off[:3])
-    with pytest.raises(ValueError, match="We"):
-        mod.moe_grouped_gemm_fp8(c, e, W, We[:2], y, offsets=off)
-    with pytest.raises(TypeError, match="y"):
-        mod.moe_grouped_gemm_fp8(c, e, W, We, y.half(), offsets=off)
-    with pytest.raises(ValueError, match="W3"):
-        mod.moe_gated_gemm_fp8(c, e, W, We, W[:2], We, y.to(bf), offsets=off)
-    d = mod.dims(T=4, D=256, E=8, F=64, k=2)
-    z = torch.zeros
-    with pytest.raises(ValueError, match="Wr"):
-        mod.moe_forward_few(z(4, 256, dtype=bf), z(8, 128), z(8), *([None] * 6), d, z(4, 256), None)
-    with pytest.raises(ValueError, match="out"):
-        mod.moe_forward_few_fp8(z(4, 256, dtype=bf), z(8, 256), z(8), mod.moe_fp8_weights_t(), d,
-                                z(4, 128), None)
+@pytest.fixture()
+def on_cpu(mod, monkeypatch):
+    """Lets host tensors pass for tensors of the current device, so that what is
+    wrong with one argument is reached; every call below is refused before the
+    library is entered."""
+    monkeypatch.setattr(mod, "_device", lambda: -1)
+    return mod
+
+
+def test_binding_refusals_quantize(on_cpu):
+    z, f = torch.zeros, on_cpu.moe_quantize_fp8
+    x, c, e = z(4, 256, dtype=torch.bfloat16), z(4, 256, dtype=torch.uint8), z(4, 2, dtype=torch.int8)
+    for args, kind, text in (((x, c[:3], e), ValueError, "codes"), ((x, c, e[:, :1]), ValueError, "exps"),
+                             ((x.float(), c, e), TypeError, "x: expected"),
+                             ((x, c.int(), e), TypeError, "codes"), ((x[0], c, e), ValueError, "x "),
+                             ((x.t().contiguous().t(), c, e), ValueError, "contiguous"),
+                             ((x, c, e, z(3, dtype=torch.int32)), ValueError, "codes"),
+                             ((x, c, e, z(4, dtype=torch.int64)), TypeError, "idx"),
+                             ((x, c, e, None, z(8)), TypeError, "ws"),
+                             ((x, c, None), AttributeError, "dtype")):
+        with pytest.raises(kind, match=text):
+            f(*args)
+
+
+def test_binding_refusals_products(on_cpu):
+    z, u8, i8 = torch.zeros, torch.uint8, torch.int8
+    c, e = z(4, 256, dtype=u8), z(4, 2, dtype=i8)
+    W, We, y = z(3, 64, 256, dtype=u8), z(3, 1, 2, dtype=i8), z(4, 64)
+    off = z(4, dtype=torch.int32)
+    for args, kw, kind, text in (
+            ((c, e, W, We, y[:, :32].contiguous()), dict(offsets=off), ValueError, "y: expected shape"),
+            ((c, e, W, We, y), dict(offsets=off[:3]), ValueError, "offsets"),
+            ((c, e, W, We, y), dict(offsets=off.long()), TypeError, "offsets"),
+            ((c, e, W, We[:2], y), dict(offsets=off), ValueError, "We"),
+            ((c, e[:, :1], W, We, y), dict(offsets=off), ValueError, "xe"),
+            ((c, e, W, We, y.half()), dict(offsets=off), TypeError, "y"),
+            ((c, e, W.short(), We, y), dict(offsets=off), TypeError, "W"),
+            ((c, e, W, We, y), dict(offsets=off, ws=z(256)), TypeError, "ws")):
+        with pytest.raises(kind, match=text):
+            on_cpu.moe_grouped_gemm_fp8(*args, **kw)
+    act = y.to(torch.bfloat16)
+    for args, kind, text in (((c, e, W, We, W[:2], We, act), ValueError, "W3"),
+                             ((c, e, W, We, W, We[:1], act), ValueError, "W3e"),
+                             ((c, e, W, We, W, We, y), TypeError, "act")):
+        with pytest.raises(kind, match=text):
+            on_cpu.moe_gated_gemm_fp8(*args, offsets=off)
+
+
+def test_binding_refusals_few_layer(on_cpu):
+    z, bf = torch.zeros, torch.bfloat16
+    d = on_cpu.dims(T=4, D=256, E=8, F=64, k=2)
+    h, Wr, bias, out = z(4, 256, dtype=bf), z(8, 256), z(8), z(4, 256)
+    W1, W2 = z(8, 64, 256, dtype=bf), z(8, 256, 64, dtype=bf)
+    S1, S2, ws = W1[:1], W2[:1], z(16, dtype=torch.uint8)
+    good = dict(h=h, Wr=Wr, bias=bias, W1=W1, W3=W1, W2=W2, Ws1=S1, Ws3=S1, Ws2=S2, d=d, out=out, ws=ws)
+    for change, kind, text in ((dict(h=h[:3]), ValueError, "h: "), (dict(Wr=Wr.to(bf)), TypeError, "Wr"),
+                               (dict(bias=bias[:4]), ValueError, "bias"), (dict(W2=W1), ValueError, "W2"),
+                               (dict(W3=W1.float()), TypeError, "W3"), (dict(Ws2=S1), ValueError, "Ws2"),
+                               (dict(out=out.to(bf)), TypeError, "out"),
+                               (dict(idx_out=z(4, 3, dtype=torch.int32)), ValueError, "idx_out"),
+                               (dict(w_out=z(4, 2, dtype=bf)), TypeError, "w_out"),
+                               (dict(ws=z(16)), TypeError, "ws")):
+        with pytest.raises(kind, match=text):
+            on_cpu.moe_forward_few(**{**good, **change})
+    q = on_cpu.moe_fp8_weights_t()
+    for change, kind, text in ((dict(h=h[:3]), ValueError, "h: "), (dict(out=out[:2]), ValueError, "out")):
+        kw = {**dict(h=h, Wr=Wr, bias=bias, w8=q, d=d, out=out, ws=ws), **change}
+        with pytest.raises(kind, match=text):
+            on_cpu.moe_forward_few_fp8(**kw)
+
+
+def test_binding_refuses_host_tensors(mod):
+    x = torch.zeros(4, 256, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        mod.moe_quantize_fp8(x, torch.zeros(4, 256, dtype=torch.uint8), torch.zeros(4, 2, dtype=torch.int8))
