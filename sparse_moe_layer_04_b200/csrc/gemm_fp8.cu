@@ -18,9 +18,12 @@
 // the epilogue holds one output column, and a warp stores 32 neighbouring
 // columns of a row at a time.
 //
-// CTA structure (320 threads, tiles taken round-robin):
-//   warp 0      TMA producer: weight tile (128 x 128 codes) and row tile
-//               (NT x 128 codes), 128-byte swizzled, into a ring of stages
+// CTA structure (352 threads, tiles taken round-robin):
+//   warp 0      weight producer: TMA of 128 x 128 codes a stage, 128-byte
+//               swizzled, into a deep ring (the weights come from HBM)
+//   warp 10     row producer: TMA of up to NT x 128 codes a stage into a ring
+//               of its own (the rows are read again for every column tile, so
+//               they come from L2)
 //   warp 1      TMEM allocator and MMA issuer (one elected thread)
 //   warps 2-5   epilogue: TMEM -> registers -> global; two accumulators, so
 //               a tile's epilogue overlaps the next tile's products
@@ -34,16 +37,11 @@
 // and 16 of W3, so every warp's lanes 0-15 hold gates and lanes 16-31 the ups
 // of the same columns, which one shuffle per pair of rows brings together.
 //
-// Large groups run on pairs of CTAs (PAIR): one product of M = 256 weight rows,
-// 128 from each CTA, whose row operand is split between the two, so a CTA
-// stages half the rows per product.  Both CTAs' loads complete on the first
-// one's barriers, it issues the products, and their completion is signalled
-// to both; each CTA writes its own scales and stores its own output columns.
-//
 // Few tiles (one row through one matrix): a cluster of CTAs shares a tile,
 // each with its own range of K-blocks, and adds the partial tiles through
 // distributed shared memory in rank order, so results do not depend on timing.
 #include <algorithm>
+#include <cmath>
 
 #include <cuda_bf16.h>
 
@@ -55,8 +53,9 @@ namespace {
 
 constexpr int kBK = 128;                 // K elements of a stage = one exponent
 constexpr int kWTile = 128 * kBK;        // weight tile bytes
-constexpr int kThreads = 320;
-constexpr int kMaxStages = 11;
+constexpr int kThreads = 352;
+constexpr int kMaxStages = 11;          // of either ring
+constexpr int kRingBytes = 208 * 1024;
 constexpr int kMaxG = 1024;
 constexpr int kSfSlotCols = 12;          // 4 columns for the weights, 8 for the rows
 constexpr unsigned kAll = 0xffffffffu;
@@ -71,7 +70,7 @@ struct alignas(64) GemmParams8 {
   void* y;
   int y_bf16;
   int G, R, N, K, KB, NB;
-  int nt;               // output column tiles of a group (PAIR: pairs of them)
+  int nt;               // output column tiles of a group
   int split;            // CTAs per tile (cluster size)
   int* status;
 };
@@ -88,25 +87,28 @@ struct Tile8 {
   int g, n0, row0, rows;     // group, first output column, first row, rows
 };
 
-template <int NT, bool PAIR>
+template <int NT>
 struct Cfg {
-  // rows of one TMA box of the row operand, and of a stage's share of it: a
-  // tile loads only as many boxes as its rows need
-  static constexpr int XROWS = PAIR ? NT / 2 : NT;
-  static constexpr int XBOX = PAIR ? 24 : NT < 48 ? NT : 32;
-  static constexpr int X_BYTES = XROWS * kBK;
-  static constexpr int STAGE = kWTile + X_BYTES;
-  static constexpr int STAGES = (200 * 1024) / STAGE < kMaxStages ? (200 * 1024) / STAGE : kMaxStages;
+  // rows of one TMA box of the row operand: a tile loads only as many boxes as
+  // its rows need
+  static constexpr int XBOX = NT % 48 == 0 ? 48 : 32;
+  static constexpr int X_BYTES = NT * kBK;
+  static constexpr int XST = NT > 64 ? 4 : 5;
+  static constexpr int WST = (kRingBytes - XST * X_BYTES) / kWTile < kMaxStages
+                                 ? (kRingBytes - XST * X_BYTES) / kWTile
+                                 : kMaxStages;
+  static constexpr int RING = WST * kWTile + XST * X_BYTES;
   static constexpr int SF_COLS = 2 * kSfSlotCols;
   static constexpr uint32_t TMEM_COLS = 2 * NT + SF_COLS <= 128   ? 128
                                         : 2 * NT + SF_COLS <= 256 ? 256
                                                                   : 512;
   static_assert(2 * NT + SF_COLS <= 512 && NT % 16 == 0 && NT <= 240, "tensor memory columns");
-  static_assert(XROWS % XBOX == 0 && XBOX % 8 == 0 && X_BYTES % 1024 == 0, "row boxes");
+  static_assert(NT % XBOX == 0 && XBOX % 8 == 0 && X_BYTES % 1024 == 0, "row boxes");
 };
 
 struct Shared8 {
-  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t w_full[kMaxStages], w_empty[kMaxStages];
+  uint64_t x_full[kMaxStages], x_empty[kMaxStages];
   uint64_t sf_full[2], sf_empty[2];
   uint64_t acc_full[2], acc_empty[2];
   uint64_t drain;
@@ -118,9 +120,9 @@ struct Shared8 {
   GroupMap gm;
 };
 
-template <int NT, bool PAIR>
+template <int NT>
 constexpr int smem_bytes8() {
-  return 1024 + Cfg<NT, PAIR>::STAGES * Cfg<NT, PAIR>::STAGE + (int)sizeof(Shared8);
+  return 1024 + Cfg<NT>::RING + (int)sizeof(Shared8);
 }
 
 __device__ __forceinline__ int blocks_of(int rows, int nt) { return (rows + nt - 1) / nt; }
@@ -162,29 +164,36 @@ __device__ void build_groups(GroupMap& gm, const GemmParams8& p, int lane) {
   }
 }
 
-// Tile t: groups in order, then output column tiles, row blocks fastest (the
-// CTAs that run together share weight tiles through L2).
-// `rank`: this CTA's half of a pair's columns.
-template <int NT, bool GATED, bool PAIR>
-__device__ __forceinline__ Tile8 tile_at(int t, const GroupMap& gm, const GemmParams8& p, int rank) {
-  const int q = t / p.nt;
-  int lo = 0, hi = p.G - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (gm.prefix[mid] <= q) lo = mid; else hi = mid - 1;
+// The tiles of one CTA (or team of CTAs): t, t + step, ...  Tiles are numbered
+// by group, then output column tile, row blocks fastest (the CTAs that run
+// together share weight tiles through L2).
+template <bool GATED>
+struct Walk {
+  int t, step, total;
+  int g = 0;
+  __device__ __forceinline__ Walk(const GroupMap& gm, const GemmParams8& p, int first, int st)
+      : t(first), step(st), total(gm.total * p.nt) {}
+  __device__ __forceinline__ bool more() const { return t < total; }
+  __device__ __forceinline__ void next() { t += step; }
+  // The tile t; successive calls come with rising t.
+  __device__ __forceinline__ Tile8 tile(const GroupMap& gm, const GemmParams8& p) {
+    while (t >= gm.prefix[g + 1] * p.nt) ++g;
+    const int rows = gm.off[g + 1] - gm.off[g];
+    const int nb = gm.prefix[g + 1] - gm.prefix[g];
+    int local = t - gm.prefix[g] * p.nt, b = 0, per = rows;
+    if (nb > 1) {                              // equal blocks, in steps of 16 rows
+      per = ((rows + nb - 1) / nb + 15) / 16 * 16;
+      b = local % nb;
+      local /= nb;
+    }
+    Tile8 ti;
+    ti.g = g;
+    ti.n0 = local * (GATED ? 64 : 128);
+    ti.row0 = gm.off[g] + b * per;
+    ti.rows = min(per, rows - b * per);
+    return ti;
   }
-  const int rows = gm.off[lo + 1] - gm.off[lo];
-  const int nb = blocks_of(rows, NT);
-  const int local = t - gm.prefix[lo] * p.nt;
-  const int per = (blocks_of(rows, nb) + 15) / 16 * 16;   // rows per block
-  const int b = local % nb;
-  Tile8 ti;
-  ti.g = lo;
-  ti.n0 = (PAIR ? local / nb * 2 + rank : local / nb) * (GATED ? 64 : 128);
-  ti.row0 = gm.off[lo] + b * per;
-  ti.rows = max(0, min(per, rows - b * per));
-  return ti;
-}
+};
 
 // Exponents q[0 .. n-1] (n <= 16) as they stand in memory, in words of four.
 // Any alignment: the aligned words that hold them are loaded and shifted.
@@ -244,38 +253,35 @@ __device__ __forceinline__ void store16(const GemmParams8& p, const Tile8& ti, i
   }
 }
 
-template <int NT, bool GATED, bool PAIR>
+template <int NT, bool GATED>
 __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_constant__ GemmParams8 p) {
-  using C = Cfg<NT, PAIR>;
-  constexpr int STAGES = C::STAGES;
+  using C = Cfg<NT>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = ptx::smem_addr(smem_raw);
   uint8_t* ring = smem_raw + (((raw + 1023u) & ~1023u) - raw);
-  Shared8& ss = *reinterpret_cast<Shared8*>(ring + STAGES * C::STAGE);
+  uint8_t* ring_x = ring + C::WST * kWTile;
+  Shared8& ss = *reinterpret_cast<Shared8*>(ring + C::RING);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   ptx::pdl_launch_dependents();
   if (warp == 1) {
-    if (PAIR) {
-      ptx::tmem_alloc_pair(&ss.tmem_base, C::TMEM_COLS);
-      ptx::tmem_relinquish_pair();
-    } else {
-      ptx::tmem_alloc(&ss.tmem_base, C::TMEM_COLS);
-      ptx::tmem_relinquish();
-    }
+    ptx::tmem_alloc(&ss.tmem_base, C::TMEM_COLS);
+    ptx::tmem_relinquish();
   }
   if (threadIdx.x == 0) {
-    // a pair's products wait on the first CTA's barriers, which both CTAs' scale
-    // writers and epilogues arrive on
-    for (int i = 0; i < STAGES; ++i) {
-      ptx::mbar_init(&ss.full[i], 1);
-      ptx::mbar_init(&ss.empty[i], 1);
+    for (int i = 0; i < C::WST; ++i) {
+      ptx::mbar_init(&ss.w_full[i], 1);
+      ptx::mbar_init(&ss.w_empty[i], 1);
+    }
+    for (int i = 0; i < C::XST; ++i) {
+      ptx::mbar_init(&ss.x_full[i], 1);
+      ptx::mbar_init(&ss.x_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      ptx::mbar_init(&ss.sf_full[i], PAIR ? 8 : 4);
+      ptx::mbar_init(&ss.sf_full[i], 4);
       ptx::mbar_init(&ss.sf_empty[i], 1);
       ptx::mbar_init(&ss.acc_full[i], 1);
-      ptx::mbar_init(&ss.acc_empty[i], PAIR ? 8 : 4);
+      ptx::mbar_init(&ss.acc_empty[i], 4);
     }
     ptx::mbar_init(&ss.drain, 1);
     ptx::mbar_init(&ss.sf_bar, 4);
@@ -290,138 +296,115 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
   if (warp == 2) build_groups<NT>(ss.gm, p, lane);
   ptx::tc_fence_before();
   __syncthreads();
-  if (PAIR) ptx::cluster_sync();   // the barriers of both CTAs are initialised
   ptx::tc_fence_after();
 
   const uint32_t tmem = ss.tmem_base;
   const uint32_t sf_base = tmem + 2 * NT;
   volatile int* abort = &ss.abort;
-  // a cluster of `split` CTAs works on the same tiles, each on its K-blocks (or,
-  // as a pair, each on its columns of all of them)
-  const int rank = p.split > 1 || PAIR ? (int)ptx::cluster_rank() : 0;
-  const int team = PAIR ? 2 : p.split;
-  const int first = blockIdx.x / team, step = gridDim.x / team;
-  const int total = ss.gm.total * p.nt;
-  const int kb0 = PAIR ? 0 : (int)((long long)p.KB * rank / p.split);
-  const int kb1 = PAIR ? p.KB : (int)((long long)p.KB * (rank + 1) / p.split);
+  // a cluster of `split` CTAs works on the same tile, each on its K-blocks
+  const int rank = p.split > 1 ? (int)ptx::cluster_rank() : 0;
+  const int first = blockIdx.x / p.split, step = gridDim.x / p.split;
+  Walk<GATED> walk(ss.gm, p, first, step);
+  const int kb0 = (int)((long long)p.KB * rank / p.split);
+  const int kb1 = (int)((long long)p.KB * (rank + 1) / p.split);
   // scale words cover K-blocks 4s .. 4s + 3
   const int s0 = kb0 / 4, s1 = kb1 > kb0 ? (kb1 + 3) / 4 : s0;
 
-  if (warp == 0) {
+  if (warp == 0 || warp == 10) {
+    const bool wside = warp == 0;
     if (ptx::elect_one()) {
+      // Both rings are filled the same way: `depth` stages, a stage's barriers
+      // at the same index.
+      uint64_t* full = wside ? ss.w_full : ss.x_full;
+      uint64_t* empty = wside ? ss.w_empty : ss.x_empty;
+      const int depth = wside ? C::WST : C::XST;
       int stage = 0;
       uint32_t phase = 0, issued = 0, parity = 0;
       bool ok = true;
-      for (int t = first; ok && t < total; t += step) {
-        const Tile8 ti = tile_at<NT, GATED, PAIR>(t, ss.gm, p, rank);
+      for (; ok && walk.more(); walk.next()) {
+        const Tile8 ti = walk.tile(ss.gm, p);
         const int wrow = ti.g * p.N + ti.n0;
-        const int n = mma_rows(ti.rows);
-        const int xn = PAIR ? n / 2 : n;           // rows this CTA stages
-        const int xrow = ti.row0 + (PAIR ? rank * xn : 0);
-        const int boxes = (xn + C::XBOX - 1) / C::XBOX;
-        const int bytes = kWTile + boxes * C::XBOX * kBK;
+        const int boxes = (mma_rows(ti.rows) + C::XBOX - 1) / C::XBOX;
+        const int bytes = wside ? kWTile : boxes * C::XBOX * kBK;
         for (int kb = kb0; kb < kb1; ++kb) {
-          if (!ptx::mbar_wait(&ss.empty[stage], phase ^ 1u, abort)) { ok = false; break; }
-          uint8_t* sw = ring + stage * C::STAGE;
-          uint64_t* bar = &ss.full[stage];
-          if (PAIR) {
-            const uint32_t lead = ptx::map_rank(bar, 0);
-            if (rank == 0) ptx::mbar_arrive_expect_tx(bar, 2 * bytes);
-            if (GATED) {
+          if (!ptx::mbar_wait(&empty[stage], phase ^ 1u, abort)) { ok = false; break; }
+          uint64_t* bar = &full[stage];
+          ptx::mbar_arrive_expect_tx(bar, bytes);
+          auto load = [&](void* dst, const CUtensorMap* m, int row) {
+            ptx::tma_load_2d(dst, m, bar, kb * kBK, row);
+          };
+          if (!wside) {
+            uint8_t* dst = ring_x + stage * C::X_BYTES;
+            for (int j = 0; j < boxes; ++j) load(dst + j * C::XBOX * kBK, &p.x, ti.row0 + j * C::XBOX);
+          } else if (GATED) {
+            uint8_t* dst = ring + stage * kWTile;
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                ptx::tma_load_2d_pair(sw + j * 4096, &p.w1, lead, kb * kBK, wrow + j * 16);
-                ptx::tma_load_2d_pair(sw + j * 4096 + 2048, &p.w3, lead, kb * kBK, wrow + j * 16);
-              }
-            } else {
-              ptx::tma_load_2d_pair(sw, &p.w1, lead, kb * kBK, wrow);
+            for (int j = 0; j < 4; ++j) {
+              load(dst + j * 4096, &p.w1, wrow + j * 16);
+              load(dst + j * 4096 + 2048, &p.w3, wrow + j * 16);
             }
-            for (int j = 0; j < boxes; ++j)
-              ptx::tma_load_2d_pair(sw + kWTile + j * C::XBOX * kBK, &p.x, lead, kb * kBK,
-                                    xrow + j * C::XBOX);
           } else {
-            ptx::mbar_arrive_expect_tx(bar, bytes);
-            if (GATED) {
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                ptx::tma_load_2d(sw + j * 4096, &p.w1, bar, kb * kBK, wrow + j * 16);
-                ptx::tma_load_2d(sw + j * 4096 + 2048, &p.w3, bar, kb * kBK, wrow + j * 16);
-              }
-            } else {
-              ptx::tma_load_2d(sw, &p.w1, bar, kb * kBK, wrow);
-            }
-            for (int j = 0; j < boxes; ++j)
-              ptx::tma_load_2d(sw + kWTile + j * C::XBOX * kBK, &p.x, bar, kb * kBK,
-                               xrow + j * C::XBOX);
+            load(ring + stage * kWTile, &p.w1, wrow);
           }
           issued |= 1u << stage;
           parity = (parity & ~(1u << stage)) | (phase << stage);
-          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+          if (++stage == depth) { stage = 0; phase ^= 1u; }
         }
       }
-      // loads in flight end before the CTA does; a pair's second CTA sees its
-      // loads' stages released (their products have read them)
-      for (int s = 0; s < STAGES; ++s)
-        if (issued & (1u << s)) {
-          if (!PAIR || rank == 0) ffn::wait_drain(&ss.full[s], (parity >> s) & 1u, abort);
-          else ffn::wait_drain(&ss.empty[s], (parity >> s) & 1u, abort);
-        }
+      // loads in flight end before the CTA does
+      for (int s = 0; s < depth; ++s)
+        if (issued & (1u << s)) ffn::wait_drain(&full[s], (parity >> s) & 1u, abort);
     }
   } else if (warp == 1) {
-    if ((!PAIR || rank == 0) && ptx::elect_one()) {
-      auto commit = [](uint64_t* bar) {
-        if (PAIR) ptx::mma_commit_pair(bar); else ptx::mma_commit(bar);
-      };
-      auto wait = [&](uint64_t* bar, uint32_t parity) {
-        return PAIR ? ptx::mbar_wait_cluster(bar, parity, abort) : ptx::mbar_wait(bar, parity, abort);
-      };
-      int stage = 0, buf = 0, slot = 0;
-      uint32_t phase = 0, aphase = 0, sphase = 0;
+    if (ptx::elect_one()) {
+      int ws = 0, xs = 0, buf = 0, slot = 0;
+      uint32_t wphase = 0, xphase = 0, aphase = 0, sphase = 0;
       bool ok = true;
-      for (int t = first; ok && t < total; t += step) {
-        const Tile8 ti = tile_at<NT, GATED, PAIR>(t, ss.gm, p, rank);
-        const uint32_t idesc = ptx::idesc_mxf8(PAIR ? 256 : 128, mma_rows(ti.rows));
-        if (!wait(&ss.acc_empty[buf], aphase ^ 1u)) break;
+      for (; ok && walk.more(); walk.next()) {
+        const Tile8 ti = walk.tile(ss.gm, p);
+        const uint32_t idesc = ptx::idesc_mxf8(128, mma_rows(ti.rows));
+        if (!ptx::mbar_wait(&ss.acc_empty[buf], aphase ^ 1u, abort)) break;
         const uint32_t acc = tmem + buf * NT;
         for (int kb = kb0; kb < kb1; ++kb) {
           if (kb == kb0 || (kb & 3) == 0) {
-            if (!wait(&ss.sf_full[slot], sphase)) { ok = false; break; }
+            if (!ptx::mbar_wait(&ss.sf_full[slot], sphase, abort)) { ok = false; break; }
           }
-          if (!wait(&ss.full[stage], phase)) { ok = false; break; }
+          if (!ptx::mbar_wait(&ss.x_full[xs], xphase, abort) ||
+              !ptx::mbar_wait(&ss.w_full[ws], wphase, abort)) {
+            ok = false;
+            break;
+          }
           ptx::tc_fence_after();
-          const uint32_t sw = ptx::smem_addr(ring + stage * C::STAGE);
-          const uint64_t da = ptx::smem_desc_sw128(sw);
-          const uint64_t db = ptx::smem_desc_sw128(sw + kWTile);
+          const uint64_t da = ptx::smem_desc_sw128(ptx::smem_addr(ring + ws * kWTile));
+          const uint64_t db = ptx::smem_desc_sw128(ptx::smem_addr(ring_x + xs * C::X_BYTES));
           const uint32_t id = idesc | ptx::idesc_sf_byte(kb & 3, kb & 3);
           const uint32_t sfa = sf_base + slot * kSfSlotCols, sfb = sfa + 4;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            if (PAIR)
-              ptx::mma_mxf8_ss_pair(acc, da + 2 * k, db + 2 * k, id, sfa, sfb, kb > kb0 || k > 0);
-            else
-              ptx::mma_mxf8_ss(acc, da + 2 * k, db + 2 * k, id, sfa, sfb, kb > kb0 || k > 0);
-          }
-          commit(&ss.empty[stage]);
-          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+          for (int k = 0; k < 4; ++k)
+            ptx::mma_mxf8_ss(acc, da + 2 * k, db + 2 * k, id, sfa, sfb, kb > kb0 || k > 0);
+          ptx::mma_commit(&ss.w_empty[ws]);
+          ptx::mma_commit(&ss.x_empty[xs]);
+          if (++ws == C::WST) { ws = 0; wphase ^= 1u; }
+          if (++xs == C::XST) { xs = 0; xphase ^= 1u; }
           if ((kb & 3) == 3 || kb == kb1 - 1) {
-            commit(&ss.sf_empty[slot]);
+            ptx::mma_commit(&ss.sf_empty[slot]);
             if (++slot == 2) { slot = 0; sphase ^= 1u; }
           }
         }
         if (!ok) break;
-        commit(&ss.acc_full[buf]);
+        ptx::mma_commit(&ss.acc_full[buf]);
         if (++buf == 2) { buf = 0; aphase ^= 1u; }
       }
       // nothing is in flight when tensor memory is freed
-      commit(&ss.drain);
+      ptx::mma_commit(&ss.drain);
       ffn::wait_drain(&ss.drain, 0, abort);
     }
   } else if (warp < 6) {
     const int q = warp & 3;              // TMEM lane quarter of this warp
     int buf = 0;
     uint32_t aphase = 0;
-    for (int t = first; t < total; t += step) {
-      const Tile8 ti = tile_at<NT, GATED, PAIR>(t, ss.gm, p, rank);
+    for (; walk.more(); walk.next()) {
+      const Tile8 ti = walk.tile(ss.gm, p);
       if (__any_sync(kAll, !ptx::mbar_wait(&ss.acc_full[buf], aphase, abort))) break;
       ptx::tc_fence_after();
       const uint32_t acc = tmem + buf * NT + ((uint32_t)(q * 32) << 16);
@@ -444,13 +427,10 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
       }
       ptx::tc_fence_before();
       __syncwarp();
-      if (lane == 0) {
-        if (PAIR) ptx::mbar_arrive_cluster(ptx::map_rank(&ss.acc_empty[buf], 0));
-        else ptx::mbar_arrive(&ss.acc_empty[buf]);
-      }
+      if (lane == 0) ptx::mbar_arrive(&ss.acc_empty[buf]);
       if (++buf == 2) { buf = 0; aphase ^= 1u; }
     }
-  } else {
+  } else if (warp < 10) {
     constexpr int RPT = (NT + 127) / 128;      // rows per thread
     constexpr int XC = (NT + 31) / 32;         // scale columns of the rows
     const int tid = threadIdx.x - 192;
@@ -469,18 +449,17 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
         const int r = tid + 128 * i;
         if (r < ti.rows) load_exps(p.xe + (size_t)(ti.row0 + r) * p.KB + 16 * c, n, xw[i]);
       }
-      // (a pair's second tile may lie behind the last column: any scale will do)
       load_exps((GATED && (lane & 16) ? p.w3e : p.w1e) +
-                    ((size_t)ti.g * p.NB + min(ti.n0 / 128, p.NB - 1)) * p.KB + 16 * c,
+                    ((size_t)ti.g * p.NB + ti.n0 / 128) * p.KB + 16 * c,
                 n, ww);
     };
-    int t = first, c = c0;
+    int c = c0;
     Tile8 ti{};
-    if (t < total) {
-      ti = tile_at<NT, GATED, PAIR>(t, ss.gm, p, rank);
+    if (walk.more()) {
+      ti = walk.tile(ss.gm, p);
       load(ti, c);
     }
-    while (ok && t < total) {
+    while (ok && walk.more()) {
       const int n = min(16, p.KB - 16 * c);
       uint32_t wa[4];
 #pragma unroll
@@ -499,10 +478,10 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
       // the next chunk's exponents are on their way while this one is used
       if (++c == c1) {
         c = c0;
-        t += step;
-        if (t < total) ti = tile_at<NT, GATED, PAIR>(t, ss.gm, p, rank);
+        walk.next();
+        if (walk.more()) ti = walk.tile(ss.gm, p);
       }
-      if (t < total) load(ti, c);
+      if (walk.more()) load(ti, c);
       if (!team_bar.sync(abort, lane)) break;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -526,10 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          if (PAIR) ptx::mbar_arrive_cluster(ptx::map_rank(&ss.sf_full[slot], 0));
-          else ptx::mbar_arrive(&ss.sf_full[slot]);
-        }
+        if (lane == 0) ptx::mbar_arrive(&ss.sf_full[slot]);
         if (++slot == 2) { slot = 0; sphase ^= 1u; }
       }
       sbuf ^= 1;
@@ -538,12 +514,12 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
   }
 
   __syncthreads();
-  if (PAIR) ptx::cluster_sync();   // neither CTA leaves while the other uses its memory
-  if (!PAIR && p.split > 1) {
+  if (p.split > 1) {
     // partial tiles -> outputs: rank r finishes the rows r, r + split, ...
     ptx::cluster_sync();
-    if (first < total && !*abort) {
-      const Tile8 ti = tile_at<NT, GATED, PAIR>(first, ss.gm, p, rank);
+    Walk<GATED> own(ss.gm, p, first, step);
+    if (own.more() && !*abort) {
+      const Tile8 ti = own.tile(ss.gm, p);
       const uint32_t part = ptx::smem_addr(ring);
       if (GATED) {
         for (int i = threadIdx.x; i < ti.rows * 64; i += kThreads) {
@@ -575,24 +551,20 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
     }
     ptx::cluster_sync();   // no CTA leaves while another reads its part
   }
-  if (warp == 1) {
-    if (PAIR) ptx::tmem_dealloc_pair(tmem, C::TMEM_COLS);
-    else ptx::tmem_dealloc(tmem, C::TMEM_COLS);
-  }
+  if (warp == 1) ptx::tmem_dealloc(tmem, C::TMEM_COLS);
   if (threadIdx.x == 0 && p.status) {
     if (ss.abort) atomicOr(p.status, kStTimeout);
     if (ss.bad) atomicOr(p.status, kStBounds);
   }
 }
 
-template <int NT, bool GATED, bool PAIR>
+template <int NT, bool GATED>
 cudaError_t launch_nt(const GemmParams8& p, long long tiles, cudaStream_t st) {
-  constexpr int smem = smem_bytes8<NT, PAIR>();
+  constexpr int smem = smem_bytes8<NT>();
   static std::atomic<uint64_t> smem_set{0};
-  cudaError_t e = set_smem_once(gemm_fp8_kernel<NT, GATED, PAIR>, smem, smem_set);
+  cudaError_t e = set_smem_once(gemm_fp8_kernel<NT, GATED>, smem, smem_set);
   if (e != cudaSuccess) return e;
-  const int team = PAIR ? 2 : p.split;
-  const long long want = tiles * team, sms = num_sms() / team * team;
+  const long long want = tiles * p.split, sms = num_sms();
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(p.split > 1 ? want : std::min(want, sms)));
   cfg.blockDim = dim3(kThreads);
@@ -602,18 +574,18 @@ cudaError_t launch_nt(const GemmParams8& p, long long tiles, cudaStream_t st) {
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = team;
+  attr[1].val.clusterDim.x = p.split;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, gemm_fp8_kernel<NT, GATED, PAIR>, p);
+  return cudaLaunchKernelEx(&cfg, gemm_fp8_kernel<NT, GATED>, p);
 }
 
-template <int NT, bool PAIR>
+template <int NT>
 cudaError_t launch_any(GemmParams8& p, bool gated, cudaStream_t st, const char** why,
                        const Gemm8Args& a) {
   const uint32_t box = gated ? 16 : 128;
-  bool ok = make_tensor_map(&p.x, a.x, a.R, a.K, Cfg<NT, PAIR>::XBOX, kBK, 1, 128) &&
+  bool ok = make_tensor_map(&p.x, a.x, a.R, a.K, Cfg<NT>::XBOX, kBK, 1, 128) &&
             make_tensor_map(&p.w1, a.W1, (uint64_t)a.G * a.N, a.K, box, kBK, 1, 128);
   p.w3 = p.w1;
   if (ok && gated) ok = make_tensor_map(&p.w3, a.W3, (uint64_t)a.G * a.N, a.K, box, kBK, 1, 128);
@@ -622,16 +594,14 @@ cudaError_t launch_any(GemmParams8& p, bool gated, cudaStream_t st, const char**
     return cudaErrorInvalidValue;
   }
   p.nt = gated ? (a.N + 63) / 64 : (a.N + 127) / 128;
-  if (PAIR) p.nt = (p.nt + 1) / 2;
   // row blocks: at most one per group with rows, and one per NT rows
   const long long blocks = std::min<long long>(a.R, (long long)a.R / NT + std::min(a.G, a.R));
   const long long tiles = blocks * p.nt;
   // Few tiles: split K over a cluster while that leaves every CTA an SM of its
   // own and at least two K-blocks.
   p.split = 1;
-  if (!PAIR)
-    while (p.split < 8 && tiles * p.split * 2 <= num_sms() && p.KB >= p.split * 4) p.split *= 2;
-  return gated ? launch_nt<NT, true, PAIR>(p, tiles, st) : launch_nt<NT, false, PAIR>(p, tiles, st);
+  while (p.split < 8 && tiles * p.split * 2 <= num_sms() && p.KB >= p.split * 4) p.split *= 2;
+  return gated ? launch_nt<NT, true>(p, tiles, st) : launch_nt<NT, false>(p, tiles, st);
 }
 
 }  // namespace
@@ -650,13 +620,18 @@ cudaError_t launch_gemm_fp8(const Gemm8Args& a, cudaStream_t st, const char** wh
   p.NB = (a.N + 127) / 128;
   p.status = a.status;
   *why = "product launch";
-  // Rows per tile by the average group: small groups leave the weight stream
-  // in charge, so the ring holds weights; large ones are bound by the products
-  // and by what the SMs read from L2, which pairs of CTAs halve for the rows.
-  const int avg = a.R / a.G;
-  if (avg <= 16) return launch_any<32, false>(p, gated, st, why, a);
-  if (avg <= 64) return launch_any<128, false>(p, gated, st, why, a);
-  return launch_any<240, true>(p, gated, st, why, a);
+  // Rows per tile.  240 (two accumulators of that width fill tensor memory) read
+  // the weights for the most rows; narrower tiles leave shared memory to the
+  // weights' ring.  So: the narrowest that cuts a group into no more blocks
+  // than 240 would, for groups two standard deviations above the average.
+  const int avg = (a.R + a.G - 1) / a.G;
+  const int top = a.G > 1 ? avg + (int)(2.f * sqrtf((float)avg)) : avg;
+  const int nb = (top + 239) / 240, need = (top + nb - 1) / nb;
+  if (need <= 32) return launch_any<32>(p, gated, st, why, a);
+  if (need <= 64) return launch_any<64>(p, gated, st, why, a);
+  if (need <= 96) return launch_any<96>(p, gated, st, why, a);
+  if (need <= 160) return launch_any<160>(p, gated, st, why, a);
+  return launch_any<240>(p, gated, st, why, a);
 }
 
 }  // namespace moe
