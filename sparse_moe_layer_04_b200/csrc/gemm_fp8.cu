@@ -98,6 +98,7 @@ struct Cfg {
                                  ? (kRingBytes - XST * X_BYTES) / kWTile
                                  : kMaxStages;
   static constexpr int RING = WST * kWTile + XST * X_BYTES;
+  static_assert(XST <= WST, "the weights' stages release the rows'");
   static constexpr int SF_COLS = 2 * kSfSlotCols;
   static constexpr uint32_t TMEM_COLS = 2 * NT + SF_COLS <= 128   ? 128
                                         : 2 * NT + SF_COLS <= 256 ? 256
@@ -107,8 +108,8 @@ struct Cfg {
 };
 
 struct Shared8 {
-  uint64_t w_full[kMaxStages], w_empty[kMaxStages];
-  uint64_t x_full[kMaxStages], x_empty[kMaxStages];
+  // of the weights' stages; a K-block's rows arrive on the same barrier
+  uint64_t full[kMaxStages], empty[kMaxStages];
   uint64_t sf_full[2], sf_empty[2];
   uint64_t acc_full[2], acc_empty[2];
   uint64_t drain;
@@ -270,12 +271,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
   }
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::WST; ++i) {
-      ptx::mbar_init(&ss.w_full[i], 1);
-      ptx::mbar_init(&ss.w_empty[i], 1);
-    }
-    for (int i = 0; i < C::XST; ++i) {
-      ptx::mbar_init(&ss.x_full[i], 1);
-      ptx::mbar_init(&ss.x_empty[i], 1);
+      ptx::mbar_init(&ss.full[i], 2);
+      ptx::mbar_init(&ss.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(&ss.sf_full[i], 4);
@@ -313,13 +310,12 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
   if (warp == 0 || warp == 10) {
     const bool wside = warp == 0;
     if (ptx::elect_one()) {
-      // Both rings are filled the same way: `depth` stages, a stage's barriers
-      // at the same index.
-      uint64_t* full = wside ? ss.w_full : ss.x_full;
-      uint64_t* empty = wside ? ss.w_empty : ss.x_empty;
-      const int depth = wside ? C::WST : C::XST;
-      int stage = 0;
-      uint32_t phase = 0, issued = 0, parity = 0;
+      // Both producers walk the weights' stages.  The row producer's own stage
+      // is free when the products of the K-block XST back are done, which that
+      // K-block's weight stage tells; since XST <= WST that barrier cannot have
+      // moved on by another phase.
+      int stage = 0, xs = 0, wait_at = 0, lag = wside ? C::WST : C::XST;
+      uint32_t phase = 0, wait_phase = 0, issued = 0, parity = 0;
       bool ok = true;
       for (; ok && walk.more(); walk.next()) {
         const Tile8 ti = walk.tile(ss.gm, p);
@@ -327,15 +323,22 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
         const int boxes = (mma_rows(ti.rows) + C::XBOX - 1) / C::XBOX;
         const int bytes = wside ? kWTile : boxes * C::XBOX * kBK;
         for (int kb = kb0; kb < kb1; ++kb) {
-          if (!ptx::mbar_wait(&empty[stage], phase ^ 1u, abort)) { ok = false; break; }
-          uint64_t* bar = &full[stage];
+          if (lag > 0) {
+            --lag;
+          } else {
+            if (!ptx::mbar_wait(&ss.empty[wait_at], wait_phase, abort)) { ok = false; break; }
+            if (++wait_at == C::WST) { wait_at = 0; wait_phase ^= 1u; }
+          }
+          uint64_t* bar = &ss.full[stage];
           ptx::mbar_arrive_expect_tx(bar, bytes);
           auto load = [&](void* dst, const CUtensorMap* m, int row) {
             ptx::tma_load_2d(dst, m, bar, kb * kBK, row);
           };
           if (!wside) {
-            uint8_t* dst = ring_x + stage * C::X_BYTES;
-            for (int j = 0; j < boxes; ++j) load(dst + j * C::XBOX * kBK, &p.x, ti.row0 + j * C::XBOX);
+            uint8_t* dst = ring_x + xs * C::X_BYTES;
+            if (++xs == C::XST) xs = 0;
+            for (int j = 0; j < boxes; ++j)
+              load(dst + j * C::XBOX * kBK, &p.x, ti.row0 + j * C::XBOX);
           } else if (GATED) {
             uint8_t* dst = ring + stage * kWTile;
 #pragma unroll
@@ -348,17 +351,17 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
           }
           issued |= 1u << stage;
           parity = (parity & ~(1u << stage)) | (phase << stage);
-          if (++stage == depth) { stage = 0; phase ^= 1u; }
+          if (++stage == C::WST) { stage = 0; phase ^= 1u; }
         }
       }
       // loads in flight end before the CTA does
-      for (int s = 0; s < depth; ++s)
-        if (issued & (1u << s)) ffn::wait_drain(&full[s], (parity >> s) & 1u, abort);
+      for (int s = 0; s < C::WST; ++s)
+        if (issued & (1u << s)) ffn::wait_drain(&ss.full[s], (parity >> s) & 1u, abort);
     }
   } else if (warp == 1) {
     if (ptx::elect_one()) {
       int ws = 0, xs = 0, buf = 0, slot = 0;
-      uint32_t wphase = 0, xphase = 0, aphase = 0, sphase = 0;
+      uint32_t phase = 0, aphase = 0, sphase = 0;
       bool ok = true;
       for (; ok && walk.more(); walk.next()) {
         const Tile8 ti = walk.tile(ss.gm, p);
@@ -369,11 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
           if (kb == kb0 || (kb & 3) == 0) {
             if (!ptx::mbar_wait(&ss.sf_full[slot], sphase, abort)) { ok = false; break; }
           }
-          if (!ptx::mbar_wait(&ss.x_full[xs], xphase, abort) ||
-              !ptx::mbar_wait(&ss.w_full[ws], wphase, abort)) {
-            ok = false;
-            break;
-          }
+          if (!ptx::mbar_wait(&ss.full[ws], phase, abort)) { ok = false; break; }
           ptx::tc_fence_after();
           const uint64_t da = ptx::smem_desc_sw128(ptx::smem_addr(ring + ws * kWTile));
           const uint64_t db = ptx::smem_desc_sw128(ptx::smem_addr(ring_x + xs * C::X_BYTES));
@@ -382,10 +381,9 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             ptx::mma_mxf8_ss(acc, da + 2 * k, db + 2 * k, id, sfa, sfb, kb > kb0 || k > 0);
-          ptx::mma_commit(&ss.w_empty[ws]);
-          ptx::mma_commit(&ss.x_empty[xs]);
-          if (++ws == C::WST) { ws = 0; wphase ^= 1u; }
-          if (++xs == C::XST) { xs = 0; xphase ^= 1u; }
+          ptx::mma_commit(&ss.empty[ws]);
+          if (++ws == C::WST) { ws = 0; phase ^= 1u; }
+          if (++xs == C::XST) xs = 0;
           if ((kb & 3) == 3 || kb == kb1 - 1) {
             ptx::mma_commit(&ss.sf_empty[slot]);
             if (++slot == 2) { slot = 0; sphase ^= 1u; }
