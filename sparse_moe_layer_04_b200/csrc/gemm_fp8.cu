@@ -93,7 +93,10 @@ struct Cfg {
   // its rows need
   static constexpr int XBOX = NT % 48 == 0 ? 48 : 32;
   static constexpr int X_BYTES = NT * kBK;
-  static constexpr int XST = NT > 64 ? 4 : 5;
+  // The rows come from L2, whose latency under this load takes five or six
+  // K-blocks to cover; six stages of weights keep HBM busy (5 + 6 instead of 4
+  // + 8 at NT = 160: see the figures below).
+  static constexpr int XST = NT > 160 ? 4 : NT > 144 ? 5 : 6;
   static constexpr int WST = (kRingBytes - XST * X_BYTES) / kWTile < kMaxStages
                                  ? (kRingBytes - XST * X_BYTES) / kWTile
                                  : kMaxStages;
@@ -131,8 +134,9 @@ __device__ __forceinline__ int blocks_of(int rows, int nt) { return (rows + nt -
 // Rows of the product's row operand: the tile's, in steps of 16.
 __device__ __forceinline__ int mma_rows(int rows) { return max(16, (rows + 15) / 16 * 16); }
 
-// One warp: checks the offsets and counts each group's row blocks.  Offsets
-// that are not increasing within [0, R] give no tiles and raise kStBounds.
+// One warp, offsets in gm.off: checks them and counts each group's row blocks.
+// Offsets that are not increasing within [0, R] give no tiles and raise
+// kStBounds.
 template <int NT>
 __device__ void build_groups(GroupMap& gm, const GemmParams8& p, int lane) {
   int carry = 0;
@@ -141,10 +145,7 @@ __device__ void build_groups(GroupMap& gm, const GemmParams8& p, int lane) {
     const int g = base + lane;
     int cnt = 0;
     if (g < p.G) {
-      const int a = p.offsets ? p.offsets[g] : 0;
-      const int b = p.offsets ? p.offsets[g + 1] : p.R;
-      gm.off[g] = a;
-      if (g == p.G - 1) gm.off[p.G] = b;
+      const int a = gm.off[g], b = gm.off[g + 1];
       if (a < 0 || b < a || b > p.R) bad = true;
       else cnt = blocks_of(b - a, NT);
     }
@@ -290,6 +291,9 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
     if (GATED) ptx::tma_prefetch_desc(&p.w3);
   }
   ptx::pdl_wait();
+  for (int i = threadIdx.x; i <= p.G; i += kThreads)
+    ss.gm.off[i] = p.offsets ? p.offsets[i] : i ? p.R : 0;
+  __syncthreads();
   if (warp == 2) build_groups<NT>(ss.gm, p, lane);
   ptx::tc_fence_before();
   __syncthreads();
@@ -628,6 +632,7 @@ cudaError_t launch_gemm_fp8(const Gemm8Args& a, cudaStream_t st, const char** wh
   if (need <= 32) return launch_any<32>(p, gated, st, why, a);
   if (need <= 64) return launch_any<64>(p, gated, st, why, a);
   if (need <= 96) return launch_any<96>(p, gated, st, why, a);
+  if (need <= 144) return launch_any<144>(p, gated, st, why, a);
   if (need <= 160) return launch_any<160>(p, gated, st, why, a);
   return launch_any<240>(p, gated, st, why, a);
 }
