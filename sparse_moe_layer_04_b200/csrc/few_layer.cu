@@ -339,6 +339,7 @@ __global__ void __launch_bounds__(kRouterThreads) few_router_kernel(const FewRou
 constexpr int kAStage = 128 * 128;       // 128 weight rows x 128 bytes of K
 constexpr int kBStage = 8192;
 constexpr int kAStages = 9, kBStages = 8;
+static_assert(kBStages <= kAStages, "the weights' stages release the tokens'");
 constexpr int kRing = kAStages * kAStage + kBStages * kBStage;
 constexpr int kSfSlot = 32;              // scale columns of one slot: 4 weights, 4 x 4 tokens
 constexpr uint32_t kTmemCols = 512;
@@ -392,8 +393,7 @@ struct Unit {
 };
 
 struct FewShared {
-  uint64_t a_full[kAStages], a_empty[kAStages];
-  uint64_t b_full[kBStages], b_empty[kBStages];
+  uint64_t full[kAStages], empty[kAStages];   // a stage's weights and tokens; its products done
   uint64_t sf_full[2], sf_empty[2];
   uint64_t acc_full[2], acc_empty[2];
   uint64_t q_full[kQueue], q_empty[kQueue];
@@ -533,8 +533,10 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
     ptx::tmem_relinquish();
   }
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kAStages; ++i) { ptx::mbar_init(&ss.a_full[i], 1); ptx::mbar_init(&ss.a_empty[i], 1); }
-    for (int i = 0; i < kBStages; ++i) { ptx::mbar_init(&ss.b_full[i], 1); ptx::mbar_init(&ss.b_empty[i], 1); }
+    for (int i = 0; i < kAStages; ++i) {
+      ptx::mbar_init(&ss.full[i], 2);
+      ptx::mbar_init(&ss.empty[i], 1);
+    }
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(&ss.sf_full[i], 4);
       ptx::mbar_init(&ss.sf_empty[i], 1);
@@ -607,9 +609,9 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
           const CUtensorMap* m = sh ? &p.w2_s : &p.w2_r;
           const int row = u.expert * p.D + u.at * 128;
           for (int kb = k0; kb < k1; ++kb) {
-            if (!ptx::mbar_wait(&ss.a_empty[stage], phase ^ 1u, abort)) { ok = false; break; }
-            ptx::mbar_arrive_expect_tx(&ss.a_full[stage], kAStage);
-            ptx::tma_load_2d_hint(ring_a + stage * kAStage, m, &ss.a_full[stage], kb * EB, row, policy);
+            if (!ptx::mbar_wait(&ss.empty[stage], phase ^ 1u, abort)) { ok = false; break; }
+            ptx::mbar_arrive_expect_tx(&ss.full[stage], kAStage);
+            ptx::tma_load_2d_hint(ring_a + stage * kAStage, m, &ss.full[stage], kb * EB, row, policy);
             issued |= 1u << stage;
             parity = (parity & ~(1u << stage)) | (phase << stage);
             if (++stage == kAStages) { stage = 0; phase ^= 1u; }
@@ -620,14 +622,14 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
           const int row = u.expert * (sh ? p.Fs : p.F) + u.at;
           const int boxes = (sh ? p.fpt_s : p.fpt_r) / 16, sub = sh ? p.sub_s : p.sub_r;
           for (int kb = k0; kb < k1; kb += sub) {
-            if (!ptx::mbar_wait(&ss.a_empty[stage], phase ^ 1u, abort)) { ok = false; break; }
+            if (!ptx::mbar_wait(&ss.empty[stage], phase ^ 1u, abort)) { ok = false; break; }
             const int n = min(sub, k1 - kb);
-            ptx::mbar_arrive_expect_tx(&ss.a_full[stage], n * boxes * 4096);
+            ptx::mbar_arrive_expect_tx(&ss.full[stage], n * boxes * 4096);
             uint8_t* dst = ring_a + stage * kAStage;
             for (int i = 0; i < n; ++i)
               for (int j = 0; j < boxes; ++j, dst += 4096) {
-                ptx::tma_load_2d_hint(dst, m1, &ss.a_full[stage], (kb + i) * EB, row + j * 16, policy);
-                ptx::tma_load_2d_hint(dst + 2048, m3, &ss.a_full[stage], (kb + i) * EB, row + j * 16, policy);
+                ptx::tma_load_2d_hint(dst, m1, &ss.full[stage], (kb + i) * EB, row + j * 16, policy);
+                ptx::tma_load_2d_hint(dst + 2048, m3, &ss.full[stage], (kb + i) * EB, row + j * 16, policy);
               }
             issued |= 1u << stage;
             parity = (parity & ~(1u << stage)) | (phase << stage);
@@ -638,15 +640,18 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
         tile = next;
       }
       for (int s = 0; s < kAStages; ++s)
-        if (issued & (1u << s)) ffn::wait_drain(&ss.a_full[s], (parity >> s) & 1u, abort);
+        if (issued & (1u << s)) ffn::wait_drain(&ss.full[s], (parity >> s) & 1u, abort);
     }
   } else if (warp == 1) {
     // ---------------- token / activation producer ----------------
     QueueReader q;
     Unit u;
+    // It walks the weights' stages.  Its own stage is free when the products of
+    // the stage kBStages back are done, which that weight stage tells; since
+    // kBStages <= kAStages that barrier cannot have moved on by another phase.
     bool waited = false, pieces = false;
-    int stage = 0;
-    uint32_t phase = 0, issued = 0, parity = 0;
+    int stage = 0, own = 0, wait_at = 0, lag = kBStages;
+    uint32_t phase = 0, wait_phase = 0, issued = 0, parity = 0;
     while (q.next(ss, u, abort, lane)) {
       const bool sh = u.slot < p.S;
       if (!waited && (u.down || !sh)) {
@@ -671,28 +676,36 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
       bool ok = true;
       if (ptx::elect_one()) {
         for (int kb = k0; kb < k1; kb += sub) {
-          if (!ptx::mbar_wait(&ss.b_empty[stage], phase ^ 1u, abort)) { ok = false; break; }
+          if (lag > 0) {
+            --lag;
+          } else {
+            if (!ptx::mbar_wait(&ss.empty[wait_at], wait_phase, abort)) { ok = false; break; }
+            if (++wait_at == kAStages) { wait_at = 0; wait_phase ^= 1u; }
+          }
           const int n = min(sub, k1 - kb);
-          ptx::mbar_arrive_expect_tx(&ss.b_full[stage], n * bytes);
+          ptx::mbar_arrive_expect_tx(&ss.full[stage], n * bytes);
           for (int i = 0; i < n; ++i)
-            ptx::tma_load_2d(ring_b + stage * kBStage + i * bytes, m, &ss.b_full[stage],
-                             (kb + i) * EB, row);
+            ptx::tma_load_2d(ring_b + own * kBStage + i * bytes, m, &ss.full[stage], (kb + i) * EB,
+                             row);
+          if (++own == kBStages) own = 0;
           issued |= 1u << stage;
           parity = (parity & ~(1u << stage)) | (phase << stage);
-          if (++stage == kBStages) { stage = 0; phase ^= 1u; }
+          if (++stage == kAStages) { stage = 0; phase ^= 1u; }
         }
       }
       if (__any_sync(kAll, !ok)) break;
     }
     if (issued)
-      for (int s = 0; s < kBStages; ++s)
-        if (issued & (1u << s)) ffn::wait_drain(&ss.b_full[s], (parity >> s) & 1u, abort);
+      for (int s = 0; s < kAStages; ++s)
+        if (issued & (1u << s)) ffn::wait_drain(&ss.full[s], (parity >> s) & 1u, abort);
   } else if (warp == 2) {
     // ---------------- MMA issuer ----------------
     QueueReader q;
     Unit u;
     int as = 0, bs = 0, buf = 0, slot = 0;
-    uint32_t aph = 0, bph = 0, cph = 0, sph = 0;
+    uint32_t aph = 0, cph = 0, sph = 0;
+    const uint64_t desc_a = ptx::smem_desc_sw128(ptx::smem_addr(ring_a));
+    const uint64_t desc_b = ptx::smem_desc_sw128(ptx::smem_addr(ring_b));
     while (q.next(ss, u, abort, lane)) {
       int k0, k1;
       unit_k<EB>(p, u, &k0, &k1);
@@ -701,25 +714,24 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
       const int n = u.down ? p.PA : p.NX;
       const int nacc = acc_count(FP8, n);
       const uint32_t idesc = FP8 ? ptx::idesc_mxf8(128, n) : ptx::idesc_bf16_f32(128, n);
-      const int a_bytes = u.down ? kAStage : (sh ? p.fpt_s : p.fpt_r) * 2 * 128;
-      const int b_bytes = n * 128;
+      // sizes of a K-block within its stage, in the descriptors' units of 16 bytes
+      const int a_step = (u.down ? kAStage : (sh ? p.fpt_s : p.fpt_r) * 2 * 128) >> 4;
+      const int b_step = n * 128 >> 4;
       bool ok = true;
       if (ptx::elect_one()) {
         ok = ptx::mbar_wait(&ss.acc_empty[buf], cph ^ 1u, abort);
         uint32_t acc = tmem + buf * acc_cols(FP8);
-        int turn = 0;
-        for (int kb = k0; ok && kb < k1; kb += sub) {
-          if (!ptx::mbar_wait(&ss.b_full[bs], bph, abort)) { ok = false; break; }
-          if (!ptx::mbar_wait(&ss.a_full[as], aph, abort)) { ok = false; break; }
-          const int m = min(sub, k1 - kb);
-          uint32_t sa = ptx::smem_addr(ring_a + as * kAStage);
-          uint32_t sb = ptx::smem_addr(ring_b + bs * kBStage);
-          for (int i = 0; i < m; ++i, sa += a_bytes, sb += b_bytes) {
-            const int kk = kb + i;
+        const uint32_t acc_end = acc + nacc * n;
+        uint32_t more = 0;               // 0 in the first turn over the accumulators
+        int kk = k0;
+        while (ok && kk < k1) {
+          if (!ptx::mbar_wait(&ss.full[as], aph, abort)) { ok = false; break; }
+          uint64_t da = desc_a + as * (kAStage >> 4), db = desc_b + bs * (kBStage >> 4);
+          const int end = min(kk + sub, k1);
+          for (; kk < end; ++kk, da += a_step, db += b_step) {
             if (FP8 && (kk == k0 || (kk & 3) == 0) &&
                 !ptx::mbar_wait(&ss.sf_full[slot], sph, abort)) { ok = false; break; }
             ptx::tc_fence_after();
-            const uint64_t da = ptx::smem_desc_sw128(sa), db = ptx::smem_desc_sw128(sb);
             if (FP8) {
               const uint32_t sfa = tmem + 2 * acc_cols(FP8) + slot * kSfSlot;
               // gate/up: one word per row covers four K-blocks; down: one word per
@@ -729,7 +741,7 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
               for (int k = 0; k < 4; ++k)
                 ptx::mma_mxf8_ss(acc, da + 2 * k, db + 2 * k,
                                  idesc | ptx::idesc_sf_byte(kk & 3, u.down ? k : kk & 3), sfa, sfb,
-                                 kk - k0 >= nacc || k > 0);
+                                 k > 0 ? 1u : more);
               if ((kk & 3) == 3 || kk == k1 - 1) {
                 ptx::mma_commit(&ss.sf_empty[slot]);
                 if (++slot == 2) { slot = 0; sph ^= 1u; }
@@ -737,19 +749,18 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
             } else {
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                ptx::mma_f16_ss(acc, da + 2 * k, db + 2 * k, idesc, kk - k0 >= nacc || k > 0);
+                ptx::mma_f16_ss(acc, da + 2 * k, db + 2 * k, idesc, k > 0 ? 1u : more);
             }
             acc += n;
-            if (++turn == nacc) {
-              turn = 0;
+            if (acc == acc_end) {
               acc -= nacc * n;
+              more = 1;
             }
           }
           if (!ok) break;
-          ptx::mma_commit(&ss.a_empty[as]);
-          ptx::mma_commit(&ss.b_empty[bs]);
+          ptx::mma_commit(&ss.empty[as]);
           if (++as == kAStages) { as = 0; aph ^= 1u; }
-          if (++bs == kBStages) { bs = 0; bph ^= 1u; }
+          if (++bs == kBStages) bs = 0;
         }
         if (ok) ptx::mma_commit(&ss.acc_full[buf]);
       }
