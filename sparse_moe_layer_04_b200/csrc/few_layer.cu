@@ -201,14 +201,19 @@ __device__ __forceinline__ void router_logits_block(const FewRoute& p, float* s_
   }
 }
 
-// Selection for every token (a warp each), then the slots.  One block; s_ord
-// holds the keys' order [T][E].
-__device__ void select_and_list(const FewRoute& p, uint32_t* s_ord) {
-  __shared__ uint32_t s_mask[1024];
-  __shared__ int s_slot[1024];
+// Shared memory of the selection: the experts' token masks and slots (E
+// rounded up to 32 each), then the keys' order [T][E].
+__host__ __device__ constexpr int select_words(int T, int E) { return 2 * ((E + 31) / 32 * 32) + T * E; }
+
+// Selection for every token (a warp each), then the slots.  One block.
+__device__ void select_and_list(const FewRoute& p, uint32_t* smem) {
   __shared__ int s_cnt[32];
+  const int EP = (p.E + 31) / 32 * 32, groups = EP / 32;
+  uint32_t* s_mask = smem;
+  int* s_slot = reinterpret_cast<int*>(smem + EP);
+  uint32_t* s_ord = smem + 2 * EP;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int e = threadIdx.x; e < 1024; e += kRouterThreads) s_mask[e] = 0u;
+  for (int e = threadIdx.x; e < EP; e += kRouterThreads) s_mask[e] = 0u;
   bool bad = false;
   for (int i = threadIdx.x; i < p.T * p.E; i += kRouterThreads) {
     const float l = __ldcg(p.logits + i);
@@ -246,12 +251,12 @@ __device__ void select_and_list(const FewRoute& p, uint32_t* s_ord) {
     }
   }
   __syncthreads();
-  for (int g = warp; g < 32; g += kRouterWarps) {
+  for (int g = warp; g < groups; g += kRouterWarps) {
     const unsigned b = __ballot_sync(kAll, s_mask[g * 32 + lane] != 0u);
     if (lane == 0) s_cnt[g] = __popc(b);
   }
   __syncthreads();
-  for (int g = warp; g < 32; g += kRouterWarps) {
+  for (int g = warp; g < groups; g += kRouterWarps) {
     const int e = g * 32 + lane;
     const uint32_t m = s_mask[e];
     const unsigned b = __ballot_sync(kAll, m != 0u);
@@ -264,7 +269,7 @@ __device__ void select_and_list(const FewRoute& p, uint32_t* s_ord) {
       p.slot_mask[slot] = m;
     }
     if (e < p.E) p.counts[e] = __popc(m);
-    if (g == 31 && lane == 31) *p.nslots = slot + (m != 0u);
+    if (g == groups - 1 && lane == 31) *p.nslots = slot + (m != 0u);
   }
   __syncthreads();
   if (t < p.T && lane < p.k) p.slot_of[t * p.k + lane] = my_e != INT_MAX ? s_slot[my_e] : -1;
@@ -347,8 +352,12 @@ constexpr uint32_t kTmemCols = 512;
 // epilogue reads 16 columns from a piece's first one, at most 10 beyond the
 // set, which are still columns of this CTA.
 __host__ __device__ constexpr int acc_cols(bool fp8) { return fp8 ? 192 : 240; }
-// Accumulators of a set for a token operand of n rows.
-__device__ __forceinline__ int acc_count(bool fp8, int n) { return min(16, acc_cols(fp8) / n); }
+// Accumulators that a unit of kb K-blocks takes turns over, for a token operand
+// of n rows: chains of four K-blocks (16 steps) as far as the set reaches; each
+// one costs the epilogue a read.
+__device__ __forceinline__ int acc_count(bool fp8, int n, int kb) {
+  return min((kb + 3) / 4, acc_cols(fp8) / n);
+}
 constexpr int kQueue = 4;
 
 struct alignas(64) FewFfn {
@@ -390,6 +399,7 @@ struct Unit {
   int at;                // first feature, or output block
   int part;
   int expert;            // row of the weight arrays
+  uint32_t mask;         // tokens that chose it
 };
 
 struct FewShared {
@@ -416,7 +426,7 @@ struct QueueReader {
   __device__ __forceinline__ bool next(FewShared& ss, Unit& u, volatile int* abort, int lane) {
     if (__any_sync(kAll, !ptx::mbar_wait(&ss.q_full[slot], phase, abort))) return false;
     const volatile Unit& q = ss.q[slot];
-    u.down = q.down; u.slot = q.slot; u.at = q.at; u.part = q.part; u.expert = q.expert;
+    u.down = q.down; u.slot = q.slot; u.at = q.at; u.part = q.part; u.expert = q.expert; u.mask = q.mask;
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive_after_reads(&ss.q_empty[slot]);
     if (++slot == kQueue) { slot = 0; phase ^= 1u; }
@@ -471,8 +481,9 @@ __device__ __forceinline__ uint32_t scale_word(const int8_t* q, int n, bool chec
 
 // out for 128 columns, from the planes of every slot: shared experts, then the
 // token's choices in their order (moe_combine's).  Four groups of 32 threads
-// take every fourth token, a thread four columns; eight loads are in flight
-// before the first is added.
+// take every fourth token, a thread four columns; kMergeLoads loads are in
+// flight before the first is added.
+constexpr int kMergeLoads = 8;
 __device__ __forceinline__ void merge_block(const FewFfn& p, const FewShared& ss, int at, int tid) {
   const int d = at * 128 + (tid & 31) * 4;
   if (d >= p.D) return;
@@ -483,10 +494,10 @@ __device__ __forceinline__ void merge_block(const FewFfn& p, const FewShared& ss
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f), y = o;
     int j = 0, part = 0;                 // the term being added
     int lj = 0, lpart = 0;               // the term being loaded
-    for (int i0 = 0; i0 < n; i0 += 8) {
-      float4 r[8];
+    for (int i0 = 0; i0 < n; i0 += kMergeLoads) {
+      float4 r[kMergeLoads];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < kMergeLoads; ++i) {
         r[i] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (i0 + i < n) {
           const int s = lj < p.S ? lj : p.S + ss.tab_slot[t * p.k + lj - p.S];
@@ -496,7 +507,7 @@ __device__ __forceinline__ void merge_block(const FewFfn& p, const FewShared& ss
         }
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < kMergeLoads; ++i) {
         if (i0 + i < n) {
           y.x += r[i].x; y.y += r[i].y; y.z += r[i].z; y.w += r[i].w;
           if (++part == p.parts) {
@@ -568,7 +579,7 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
       uint32_t phase = 0, qphase = 0, issued = 0, parity = 0;
       int tile = atomicAdd(p.claim, 1);
       for (;;) {
-        Unit u{0, 0, 0, 0, 0};
+        Unit u{0, 0, 0, 0, 0, (1u << p.T) - 1u};
         if (tile < shared_tiles) {
           u.slot = tile / p.nts;
           u.at = (tile - u.slot * p.nts) * p.fpt_s;
@@ -592,8 +603,12 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
             u.part = r / p.nd;
             u.at = r - u.part * p.nd;
           }
-          if (u.down >= 0)
-            u.expert = u.slot < p.S ? u.slot : __ldcg(p.slot_expert + u.slot - p.S);
+          if (u.down >= 0 && u.slot >= p.S) {
+            u.expert = __ldcg(p.slot_expert + u.slot - p.S);
+            u.mask = __ldcg(p.slot_mask + u.slot - p.S);
+          } else {
+            u.expert = u.slot;
+          }
         }
         if (!ptx::mbar_wait(&ss.q_empty[qs], qphase ^ 1u, abort)) break;
         ss.q[qs] = u;
@@ -712,7 +727,7 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
       const bool sh = u.slot < p.S;
       const int sub = u.down ? 1 : sh ? p.sub_s : p.sub_r;
       const int n = u.down ? p.PA : p.NX;
-      const int nacc = acc_count(FP8, n);
+      const int nacc = acc_count(FP8, n, k1 - k0);
       const uint32_t idesc = FP8 ? ptx::idesc_mxf8(128, n) : ptx::idesc_bf16_f32(128, n);
       // sizes of a K-block within its stage, in the descriptors' units of 16 bytes
       const int a_step = (u.down ? kAStage : (sh ? p.fpt_s : p.fpt_r) * 2 * 128) >> 4;
@@ -782,17 +797,42 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
     bool waited = false;
     int buf = 0;
     uint32_t cph = 0;
+    // The ticket of a down unit is looked at with the next one, so that its round
+    // trip passes under that one's products: lane 0 of the first warp holds
+    // its number, and `last_at` is the output block it stands for (-1: none).
+    int ticket = 0, last_at = -1, planes = 0;
+    // All four warps; after this unit's planes are stored, or at the end: merges
+    // the block of the unit before if that was its last plane, then takes this
+    // unit's ticket.  The barrier orders the four warps' plane stores before
+    // lane 0's ticket, whose release makes them visible to the whole GPU.
+    auto settle = [&](int at) {
+      if (qt == 0 && lane == 0) {
+        ss.last = last_at >= 0 && ticket == planes - 1;
+        if (ss.last) *out_ticket(p, last_at) = 0;
+      }
+      if (!epi.sync(abort, lane)) return false;
+      const bool merge = *reinterpret_cast<volatile int*>(&ss.last);
+      if (at >= 0 && qt == 0 && lane == 0) ticket = ptx::atom_add_acq_rel_gpu(out_ticket(p, at), 1);
+      if (merge) {
+        __threadfence();
+        merge_block(p, ss, last_at, threadIdx.x - 128);
+      }
+      last_at = at;
+      // the flag is read before it is written again
+      return epi.sync(abort, lane);
+    };
     while (q.next(ss, u, abort, lane)) {
       const bool sh = u.slot < p.S;
       if (!waited && (u.down || !sh)) {
         ptx::pdl_wait();
         waited = true;
+        planes = (p.S + __ldcg(p.nslots)) * p.parts;
         for (int i = threadIdx.x - 128; i < p.T * p.k; i += 128) {
           ss.tab_slot[i] = __ldcg(p.slot_of + i);
           ss.tab_w[i] = __ldcg(p.w + i);
         }
       }
-      const uint32_t mask = sh ? (1u << p.T) - 1u : __ldcg(p.slot_mask + u.slot - p.S);
+      const uint32_t mask = u.mask;
       int k0, k1;
       unit_k<EB>(p, u, &k0, &k1);
       if (__any_sync(kAll, !ptx::mbar_wait(&ss.acc_full[buf], cph, abort))) break;
@@ -802,7 +842,7 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
       // weight row
       const int pieces = u.down ? (FP8 ? kPiecesA : kPiecesB) : (FP8 ? kPiecesH : 1);
       const int n = u.down ? p.PA : p.NX;
-      const int used = min(acc_count(FP8, n), k1 - k0);
+      const int nacc = acc_count(FP8, n, k1 - k0);
       const int fpt = sh ? p.fpt_s : p.fpt_r;
       const bool rows = u.down || qt * 16 < fpt;     // this warp's rows belong to the tile
       float v[16];
@@ -813,12 +853,18 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
           float s[16];
 #pragma unroll
           for (int t = 0; t < 16; ++t) s[t] = 0.f;
-          for (int a = 0; a < used; ++a) {
-            uint32_t r[16];
-            ptx::tmem_ld_x16(acc + a * n + c * p.T, r);
+          for (int a0 = 0; a0 < nacc; a0 += 4) {       // four reads in flight
+            uint32_t r[4][16];
+#pragma unroll
+            for (int a = 0; a < 4; ++a)
+              ptx::tmem_ld_x16(acc + min(a0 + a, nacc - 1) * n + c * p.T, r[a]);
             ptx::tmem_wait_ld();
 #pragma unroll
-            for (int t = 0; t < 16; ++t) s[t] += __uint_as_float(r[t]);
+            for (int a = 0; a < 4; ++a)
+              if (a0 + a < nacc) {
+#pragma unroll
+                for (int t = 0; t < 16; ++t) s[t] += __uint_as_float(r[a][t]);
+              }
           }
 #pragma unroll
           for (int t = 0; t < 16; ++t) v[t] += s[t];
@@ -896,21 +942,10 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
           for (int t = 0; t < 16; ++t)
             if ((mask >> t) & 1u) plane[(size_t)t * p.D] = v[t];
         }
-        __threadfence();
-        if (!epi.sync(abort, lane)) break;
-        if (qt == 0 && lane == 0) {
-          const int all = (p.S + __ldcg(p.nslots)) * p.parts;
-          const int got = ptx::atom_add_acq_rel_gpu(out_ticket(p, u.at), 1);
-          ss.last = got == all - 1;
-          if (ss.last) *out_ticket(p, u.at) = 0;
-        }
-        if (!epi.sync(abort, lane)) break;
-        if (*reinterpret_cast<volatile int*>(&ss.last)) {
-          __threadfence();
-          merge_block(p, ss, u.at, threadIdx.x - 128);
-        }
+        if (!settle(u.at)) break;
       }
     }
+    if (last_at >= 0 && !*abort) settle(-1);
   } else if (FP8 && warp >= 8) {
     // ---------------- scale writers ----------------
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -1008,9 +1043,9 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
 template <int TT>
 cudaError_t launch_few_router(const FewRoute& r, int blocks, cudaStream_t st) {
   const int part = kRouterWarps * kRouterExperts * TT * 4;
-  const int keys = r.T * r.E * 4;
+  const int keys = select_words(r.T, r.E) * 4;
   static std::atomic<uint64_t> smem_set{0};
-  const cudaError_t e = set_smem_once(few_router_kernel<TT>, std::max(part, kFewMaxT * 1024 * 4), smem_set);
+  const cudaError_t e = set_smem_once(few_router_kernel<TT>, std::max(part, select_words(kFewMaxT, 1024) * 4), smem_set);
   if (e != cudaSuccess) return e;
   return launch_pdl(few_router_kernel<TT>, dim3(blocks), dim3(kRouterThreads),
                     (size_t)std::max(part, keys), st, r);
@@ -1051,8 +1086,9 @@ FewPlan few_plan(const moe_dims_t& d, bool fp8) {
   const int eb = fp8 ? 128 : 64;
   const int kb = std::min((d.F + eb - 1) / eb, d.S > 0 ? (Fs + eb - 1) / eb : 1 << 30);
   // K parts of a down unit: until there are six units per SM, as long as a
-  // part has 16 K-blocks (shorter units end in less time than their
-  // epilogue takes); with fewer than two units per SM, down to four K-blocks
+  // part has 16 K-blocks (8 made one token through the large layer 124 instead
+  // of 115 us: a shorter unit streams in less time than its epilogue takes);
+  // with fewer than two units per SM, down to four K-blocks
   L.parts = 1;
   for (;;) {
     const long long n = (long long)L.nd * L.parts * L.max_slots;
