@@ -191,7 +191,7 @@ bool ws_layout(const moe_dims_t& d, WsLayout* L) {
   L->y = take((T * k + S * T) * D * 4);
   L->touched = take(4);
   L->gmask = take(T <= kPermBlockTokens ? E * (kPermBlockTokens / 32) * 4 : 0);
-  L->f_slots = L->f_mask = L->f_hq = L->f_hqe = L->f_act = L->f_exp = L->f_planes = 0;
+  L->f_route = L->f_slots = L->f_mask = L->f_hq = L->f_hqe = L->f_act = L->f_exp = L->f_planes = 0;
   if (T > 0 && T <= (size_t)kFewMaxT) {
     const FewPlan p16 = few_plan(d, false), p8 = few_plan(d, true);
     const size_t slots = p16.max_slots, most = slots - S;
@@ -204,6 +204,7 @@ bool ws_layout(const moe_dims_t& d, WsLayout* L) {
     // the bound grows with T, so that a workspace serves every smaller T
     const size_t planes =
         std::max(slots, std::min<size_t>(8 * slots, 12 * kSplitTargetBlocks / p16.nd));
+    L->f_route = take(2 * T * E * 4);
     L->f_slots = take((64 + T * k + slots) * 4);
     L->f_mask = take(slots * 4);
     L->f_hq = take(3 * T * D);
@@ -553,7 +554,8 @@ int forward_few_impl(const void* h, const float* Wr, const float* bias, const Ex
   a.out = out;
   a.idx = idx_out ? idx_out : w.at<int32_t>(w.L.idx);
   a.w = w_out ? w_out : w.at<float>(w.L.w);
-  a.logits = w.at<float>(w.L.partials);
+  a.scores = w.at<float>(w.L.f_route);
+  a.order = w.at<uint32_t>(w.L.f_route) + (size_t)dims->T * dims->E;
   int32_t* slots = w.at<int32_t>(w.L.f_slots);
   a.nslots = slots;
   a.slot_of = slots + 64;

@@ -56,7 +56,6 @@ namespace {
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kRouterThreads = 512;
 constexpr int kRouterWarps = kRouterThreads / 32;
-constexpr int kRouterExperts = 4;        // experts per router block
 constexpr int kPiecesH = 3, kPiecesA = 4;   // E4M3 pieces of a hidden value, an activation
 constexpr int kPiecesB = 3;                 // bf16 pieces of an activation
 constexpr int kPieceMinExp = -115;       // the last piece's exponent stays an E8M0 value
@@ -69,7 +68,8 @@ struct FewRoute {
   const float *Wr, *bias;
   int T, D, E, k;
   float scale;
-  float* logits;          // [T, E]
+  float* scores;          // [T, E]
+  uint32_t* order;        // [T, E] the keys' order
   int32_t* idx;           // [T, k]
   float* w;               // [T, k]
   int32_t* slot_of;       // [T, k] chosen-expert slot of each pair, -1 for none
@@ -144,17 +144,18 @@ __device__ __forceinline__ int block_exp(float top) {
   return max((int)((u + 0x1fffffu) >> 23) - 135, kPieceMinExp);
 }
 
-template <int TT>
-__device__ __forceinline__ void router_logits_block(const FewRoute& p, float* s_part) {
-  const int e0 = blockIdx.x * kRouterExperts;
+// Logits of EPB experts for every token, their scores and keys.
+template <int TT, int EPB>
+__device__ __forceinline__ void router_block(const FewRoute& p, float* s_part) {
+  const int e0 = blockIdx.x * EPB;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  float acc[kRouterExperts * TT];
+  float acc[EPB * TT];
 #pragma unroll
-  for (int i = 0; i < kRouterExperts * TT; ++i) acc[i] = 0.f;
+  for (int i = 0; i < EPB * TT; ++i) acc[i] = 0.f;
   for (int d = threadIdx.x * 4; d < p.D; d += kRouterThreads * 4) {
-    float4 wv[kRouterExperts];
+    float4 wv[EPB];
 #pragma unroll
-    for (int i = 0; i < kRouterExperts; ++i)
+    for (int i = 0; i < EPB; ++i)
       wv[i] = e0 + i < p.E ? *reinterpret_cast<const float4*>(p.Wr + (size_t)(e0 + i) * p.D + d)
                            : make_float4(0.f, 0.f, 0.f, 0.f);
     uint2 hv[TT];
@@ -167,8 +168,8 @@ __device__ __forceinline__ void router_logits_block(const FewRoute& p, float* s_
       const float a = __uint_as_float(hv[t].x << 16), b = __uint_as_float(hv[t].x & 0xffff0000u);
       const float c = __uint_as_float(hv[t].y << 16), e = __uint_as_float(hv[t].y & 0xffff0000u);
 #pragma unroll
-      for (int i = 0; i < kRouterExperts; ++i) {
-        float& s = acc[t * kRouterExperts + i];
+      for (int i = 0; i < EPB; ++i) {
+        float& s = acc[t * EPB + i];
         s = fmaf(a, wv[i].x, s);
         s = fmaf(b, wv[i].y, s);
         s = fmaf(c, wv[i].z, s);
@@ -176,7 +177,7 @@ __device__ __forceinline__ void router_logits_block(const FewRoute& p, float* s_
       }
     }
   }
-  constexpr int N = kRouterExperts * TT;
+  constexpr int N = EPB * TT;
   warp_sums<N>(acc, lane);
   // index of the sum a lane holds: its bits choose halves from the top down
   constexpr int PER = N > 32 ? N / 32 : 1;
@@ -193,12 +194,19 @@ __device__ __forceinline__ void router_logits_block(const FewRoute& p, float* s_
 #pragma unroll
   for (int i = 0; i < PER; ++i) s_part[warp * N + at + i] = acc[i];
   __syncthreads();
+  bool bad = false;
   for (int i = threadIdx.x; i < N; i += kRouterThreads) {
     double v = 0.0;
     for (int q = 0; q < kRouterWarps; ++q) v += (double)s_part[q * N + i];
-    const int t = i / kRouterExperts, e = e0 + i % kRouterExperts;
-    if (t < p.T && e < p.E) p.logits[(size_t)t * p.E + e] = (float)v;
+    const int t = i / EPB, e = e0 + i % EPB;
+    if (t < p.T && e < p.E) {
+      const float l = (float)v, sc = score(l), key = __fadd_rn(sc, p.bias[e]);
+      bad = !isfinite(l) || !isfinite(key);
+      p.scores[(size_t)t * p.E + e] = sc;
+      p.order[(size_t)t * p.E + e] = key_order(key);
+    }
   }
+  if (bad && p.status) atomicOr(p.status, kStNonFinite);
 }
 
 // Shared memory of the selection: the experts' token masks and slots (E
@@ -214,15 +222,8 @@ __device__ void select_and_list(const FewRoute& p, uint32_t* smem) {
   uint32_t* s_ord = smem + 2 * EP;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int e = threadIdx.x; e < EP; e += kRouterThreads) s_mask[e] = 0u;
-  bool bad = false;
-  for (int i = threadIdx.x; i < p.T * p.E; i += kRouterThreads) {
-    const float l = __ldcg(p.logits + i);
-    const float s = score(l);
-    const float key = __fadd_rn(s, p.bias[i % p.E]);
-    if (!isfinite(l) || !isfinite(key)) bad = true;
-    s_ord[i] = key_order(key);
-  }
-  if (__syncthreads_or(bad) && threadIdx.x == 0 && p.status) atomicOr(p.status, kStNonFinite);
+  for (int i = threadIdx.x; i < p.T * p.E; i += kRouterThreads) s_ord[i] = __ldcg(p.order + i);
+  __syncthreads();
   const int t = warp;
   int my_e = INT_MAX;
   if (t < p.T) {
@@ -241,7 +242,7 @@ __device__ void select_and_list(const FewRoute& p, uint32_t* smem) {
       if (bu && lane == j) my_e = be;
     }
     // the scores of the chosen, a lane each, and their sum in slot order
-    const float my_s = my_e != INT_MAX ? score(__ldcg(p.logits + (size_t)t * p.E + my_e)) : 0.f;
+    const float my_s = my_e != INT_MAX ? __ldcg(p.scores + (size_t)t * p.E + my_e) : 0.f;
     float sum = __shfl_sync(kAll, my_s, 0);
     for (int j = 1; j < p.k; ++j) sum = __fadd_rn(sum, __shfl_sync(kAll, my_s, j));
     if (lane < p.k) {
@@ -308,7 +309,7 @@ __device__ __forceinline__ void split_hidden(const FewRoute& p, int unit, int la
   }
 }
 
-template <int TT>
+template <int TT, int EPB>
 __global__ void __launch_bounds__(kRouterThreads) few_router_kernel(const FewRoute p) {
   extern __shared__ uint32_t s_dyn[];
   ptx::pdl_wait();
@@ -327,7 +328,7 @@ __global__ void __launch_bounds__(kRouterThreads) few_router_kernel(const FewRou
     if (threadIdx.x == 0) atomicAdd(p.hq_ready, 1);
     return;
   }
-  router_logits_block<TT>(p, reinterpret_cast<float*>(s_dyn));
+  router_block<TT, EPB>(p, reinterpret_cast<float*>(s_dyn));
   // the block that finishes last selects
   __shared__ int s_last;
   __syncthreads();
@@ -458,6 +459,12 @@ __device__ __forceinline__ int slot_target(const FewFfn& p, int slot) {
 
 // Waits, whole warp, until a slot's activations are stored; every lane acquires.
 __device__ __forceinline__ bool slot_wait(const FewFfn& p, int slot, volatile int* abort) {
+  // (most are ready; the others are looked at closely for a moment first)
+  for (int i = 0; i < 64; ++i) {
+    if (__all_sync(kAll, ptx::ld_acquire_gpu(slot_count(p, slot)) >= slot_target(p, slot)))
+      return true;
+    __nanosleep(20);
+  }
   return !__any_sync(kAll, !ptx::counter_wait(slot_count(p, slot), slot_target(p, slot), abort));
 }
 
@@ -467,17 +474,25 @@ __device__ __forceinline__ bool pieces_wait(const FewFfn& p, volatile int* abort
   return !__any_sync(kAll, !ptx::counter_wait(p.claim + 2, p.hq_blocks, abort));
 }
 
-// Four E8M0 bytes from exponents q[0 .. n-1] (n >= 1, the others count as 0);
-// outside [lo, hi] raises *bad.
-__device__ __forceinline__ uint32_t scale_word(const int8_t* q, int n, bool check, bool* bad) {
-  uint32_t w = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (i < n) w |= (uint32_t)(uint8_t)q[i] << (8 * i);
-  if (check)
-    *bad |= (__vcmpgts4(w, 0x07070707u) | __vcmplts4(w, 0x8b8b8b8bu)) != 0;
-  return __vadd4(w, 0x7f7f7f7fu);
-}
+// Up to four exponents q[0 .. n-1] (n >= 1): the aligned words that hold them,
+// so that the loads can be under way long before the bytes are put together.
+struct RawScales {
+  uint32_t a, b;
+  __device__ __forceinline__ void load(const int8_t* q, int n) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(q);
+    const uint32_t* base = reinterpret_cast<const uint32_t*>(at & ~(uintptr_t)3);
+    a = __ldcg(base);
+    b = 4 - (int)(at & 3) < n ? __ldcg(base + 1) : 0u;
+  }
+  // Four E8M0 bytes (exponents from n on count as 0); outside the weights' range
+  // of [-117, 7] raises *bad.
+  __device__ __forceinline__ uint32_t word(const int8_t* q, int n, bool check, bool* bad) const {
+    uint32_t w = __funnelshift_r(a, b, 8 * (int)(reinterpret_cast<uintptr_t>(q) & 3));
+    if (n < 4) w &= (1u << (8 * n)) - 1u;
+    if (check) *bad |= (__vcmpgts4(w, 0x07070707u) | __vcmplts4(w, 0x8b8b8b8bu)) != 0;
+    return __vadd4(w, 0x7f7f7f7fu);
+  }
+};
 
 // out for 128 columns, from the planes of every slot: shared experts, then the
 // token's choices in their order (moe_combine's).  Four groups of 32 threads
@@ -488,42 +503,50 @@ __device__ __forceinline__ void merge_block(const FewFfn& p, const FewShared& ss
   const int d = at * 128 + (tid & 31) * 4;
   if (d >= p.D) return;
   const size_t plane = (size_t)p.T * p.D;
+  // this thread's terms: its tokens one after the other, each token's slots,
+  // each slot's K parts
   const int n = (p.S + p.k) * p.parts;
-  for (int t = tid >> 5; t < p.T; t += 4) {
-    const float* src = p.planes + (size_t)t * p.D + d;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f), y = o;
-    int j = 0, part = 0;                 // the term being added
-    int lj = 0, lpart = 0;               // the term being loaded
-    for (int i0 = 0; i0 < n; i0 += kMergeLoads) {
-      float4 r[kMergeLoads];
+  const int total = (p.T - (tid >> 5) + 3) / 4 * n;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f), y = o;
+  int lt = tid >> 5, lj = 0, lpart = 0;  // the term being loaded
+  int t = lt, j = 0, part = 0;           // the term being added
+  for (int i0 = 0; i0 < total; i0 += kMergeLoads) {
+    float4 r[kMergeLoads];
 #pragma unroll
-      for (int i = 0; i < kMergeLoads; ++i) {
-        r[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (i0 + i < n) {
-          const int s = lj < p.S ? lj : p.S + ss.tab_slot[t * p.k + lj - p.S];
-          if (s >= (lj < p.S ? 0 : p.S))
-            r[i] = __ldcg(reinterpret_cast<const float4*>(src + ((size_t)s * p.parts + lpart) * plane));
-          if (++lpart == p.parts) { lpart = 0; ++lj; }
+    for (int i = 0; i < kMergeLoads; ++i) {
+      r[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i0 + i < total) {
+        const int s = lj < p.S ? lj : p.S + ss.tab_slot[lt * p.k + lj - p.S];
+        if (s >= (lj < p.S ? 0 : p.S))
+          r[i] = __ldcg(reinterpret_cast<const float4*>(
+              p.planes + ((size_t)s * p.parts + lpart) * plane + (size_t)lt * p.D + d));
+        if (++lpart == p.parts) {
+          lpart = 0;
+          if (++lj == p.S + p.k) { lj = 0; lt += 4; }
         }
       }
+    }
 #pragma unroll
-      for (int i = 0; i < kMergeLoads; ++i) {
-        if (i0 + i < n) {
-          y.x += r[i].x; y.y += r[i].y; y.z += r[i].z; y.w += r[i].w;
-          if (++part == p.parts) {
-            // an empty choice (NaN keys) adds nothing
-            const float c = j < p.S ? 1.f : ss.tab_slot[t * p.k + j - p.S] < 0 ? 0.f
-                                                                    : ss.tab_w[t * p.k + j - p.S];
-            o.x = fmaf(c, y.x, o.x); o.y = fmaf(c, y.y, o.y);
-            o.z = fmaf(c, y.z, o.z); o.w = fmaf(c, y.w, o.w);
-            y = make_float4(0.f, 0.f, 0.f, 0.f);
-            part = 0;
-            ++j;
+    for (int i = 0; i < kMergeLoads; ++i) {
+      if (i0 + i < total) {
+        y.x += r[i].x; y.y += r[i].y; y.z += r[i].z; y.w += r[i].w;
+        if (++part == p.parts) {
+          part = 0;
+          // an empty choice (NaN keys) adds nothing
+          const int at_j = t * p.k + j - p.S;
+          const float c = j < p.S ? 1.f : ss.tab_slot[at_j] < 0 ? 0.f : ss.tab_w[at_j];
+          o.x = fmaf(c, y.x, o.x); o.y = fmaf(c, y.y, o.y);
+          o.z = fmaf(c, y.z, o.z); o.w = fmaf(c, y.w, o.w);
+          y = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (++j == p.S + p.k) {
+            *reinterpret_cast<float4*>(p.out + (size_t)t * p.D + d) = o;
+            o = y;
+            j = 0;
+            t += 4;
           }
         }
       }
     }
-    *reinterpret_cast<float4*>(p.out + (size_t)t * p.D + d) = o;
   }
 }
 
@@ -585,13 +608,16 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
           u.at = (tile - u.slot * p.nts) * p.fpt_s;
           u.expert = u.slot;
         } else {
-          if (routed < 0) {
-            ptx::pdl_wait();             // the list of chosen experts
-            routed = __ldcg(p.nslots);
-          }
+          const bool fresh = routed < 0;
+          if (fresh) ptx::pdl_wait();    // the list of chosen experts
           int r = tile - shared_tiles;
+          // a gate/up tile's expert is read along with the list's length, which
+          // says whether there is such a tile
+          int s = min(r / p.ntr, p.max_slots - p.S - 1);
+          int expert = __ldcg(p.slot_expert + s);
+          uint32_t mask = __ldcg(p.slot_mask + s);
+          if (fresh) routed = __ldcg(p.nslots);
           if (r < routed * p.ntr) {
-            const int s = r / p.ntr;
             u.slot = p.S + s;
             u.at = (r - s * p.ntr) * p.fpt_r;
           } else {
@@ -602,10 +628,14 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
             r -= u.slot * per;
             u.part = r / p.nd;
             u.at = r - u.part * p.nd;
+            if (u.down >= 0 && u.slot >= p.S) {
+              expert = __ldcg(p.slot_expert + u.slot - p.S);
+              mask = __ldcg(p.slot_mask + u.slot - p.S);
+            }
           }
-          if (u.down >= 0 && u.slot >= p.S) {
-            u.expert = __ldcg(p.slot_expert + u.slot - p.S);
-            u.mask = __ldcg(p.slot_mask + u.slot - p.S);
+          if (u.slot >= p.S) {
+            u.expert = expert;
+            u.mask = mask;
           } else {
             u.expert = u.slot;
           }
@@ -950,6 +980,9 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
     // ---------------- scale writers ----------------
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const int KBD = (p.D + 127) / 128;
+    // the piece and token of this lane's two rows of the token operand
+    const int row_c[2] = {lane / p.T, (32 + lane) / p.T};
+    const int row_t[2] = {lane % p.T, (32 + lane) % p.T};
     QueueReader q;
     Unit u;
     bool pieces = false, bad = false;
@@ -975,30 +1008,58 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
       }
       const int8_t* ae = (sh ? p.ae_s : p.ae_r) +
                          (size_t)(sh ? u.slot : u.slot - p.S) * p.T * (KBF * 4);
-      bool ok = true;
-      for (int s = k0 / 4; s * 4 < k1; ++s) {
-        uint32_t wa[4], wx[4][2];
-        wa[0] = wa[1] = wa[2] = wa[3] = scale_word(we + 4 * s, KB - 4 * s, true, &bad);
-        // token words: gate/up, one per row (the bytes are K-blocks); down, one
-        // per row and K-block (the bytes are its steps of 32); N <= 64 rows
+      // Token words: gate/up, one per row (the bytes are K-blocks); down, one per
+      // row and K-block (the bytes are its steps of 32, and a row's exponents
+      // start on four bytes).  A set's words are loaded while the one before it
+      // is written.
+      const int8_t* xq[2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+      for (int j = 0; j < 2; ++j)
+        xq[j] = row_c[j] >= (u.down ? kPiecesA : kPiecesH) ? nullptr
+                : u.down ? ae + (size_t)row_t[j] * (KBF * 4)
+                         : p.hqe + (size_t)row_t[j] * KBD;
+      const int fe = (F + 31) / 32;      // exponents of an activation row
+      RawScales ra, rx[2];
+      uint32_t rd[4][2];
+      auto load = [&](int s) {
+        ra.load(we + 4 * s, KB - 4 * s);
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int row = j * 32 + lane, c = row / p.T, t = row - c * p.T;
-            wx[i][j] = 0x7f7f7f7fu;      // rows of no token: any valid scale
-            if (c >= (u.down ? kPiecesA : kPiecesH)) continue;
-            if (!u.down) {
-              if (i == 0) wx[i][j] = scale_word(p.hqe + t * KBD + 4 * s, KBD - 4 * s, false, &bad);
-            } else if (4 * s + i < KBF) {
-              // exponents past the last feature count as 0 (their codes are zero)
-              const int kb = 4 * s + i;
-              wx[i][j] = scale_word(ae + (size_t)t * (KBF * 4) + 4 * kb, (F + 31) / 32 - 4 * kb,
-                                    false, &bad);
-            }
-            wx[i][j] = __vsub4(wx[i][j], 0x04040404u * c);
+        for (int j = 0; j < 2; ++j) {
+          if (!xq[j]) continue;
+          if (!u.down) {
+            rx[j].load(xq[j] + 4 * s, KBD - 4 * s);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (4 * s + i < KBF)
+                rd[i][j] = __ldcg(reinterpret_cast<const uint32_t*>(xq[j]) + 4 * s + i);
           }
         }
+      };
+      bool ok = true;
+      load(k0 / 4);
+      for (int s = k0 / 4; s * 4 < k1; ++s) {
+        uint32_t wa[4], wx[4][2];
+        wa[0] = wa[1] = wa[2] = wa[3] = ra.word(we + 4 * s, KB - 4 * s, true, &bad);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint32_t lower = 0x04040404u * row_c[j];   // a piece's scale is 2^-4 of the one before
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            wx[i][j] = 0x7f7f7f7fu;      // rows of no token: any valid scale
+            if (!xq[j]) continue;
+            if (!u.down) {
+              if (i == 0) wx[i][j] = __vsub4(rx[j].word(xq[j] + 4 * s, KBD - 4 * s, false, &bad), lower);
+            } else if (4 * s + i < KBF) {
+              // exponents past the last feature count as 0 (their codes are zero)
+              const int n = fe - 4 * (4 * s + i);
+              uint32_t w = rd[i][j];
+              if (n < 4) w &= (1u << (8 * n)) - 1u;
+              wx[i][j] = __vsub4(__vadd4(w, 0x7f7f7f7fu), lower);
+            }
+          }
+        }
+        if ((s + 1) * 4 < k1) load(s + 1);
         if (__any_sync(kAll, !ptx::mbar_wait(&ss.sf_empty[slot], sph ^ 1u, abort))) { ok = false; break; }
         ptx::tc_fence_after();
         const uint32_t dst = tmem + 2 * acc_cols(FP8) + slot * kSfSlot + lanes;
@@ -1040,15 +1101,26 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
   }
 }
 
-template <int TT>
-cudaError_t launch_few_router(const FewRoute& r, int blocks, cudaStream_t st) {
-  const int part = kRouterWarps * kRouterExperts * TT * 4;
+template <int TT, int EPB>
+cudaError_t launch_router_as(const FewRoute& r, int blocks, cudaStream_t st) {
+  const int part = kRouterWarps * EPB * TT * 4;
   const int keys = select_words(r.T, r.E) * 4;
   static std::atomic<uint64_t> smem_set{0};
-  const cudaError_t e = set_smem_once(few_router_kernel<TT>, std::max(part, select_words(kFewMaxT, 1024) * 4), smem_set);
+  const cudaError_t e = set_smem_once(few_router_kernel<TT, EPB>,
+                                      std::max(part, select_words(kFewMaxT, 1024) * 4), smem_set);
   if (e != cudaSuccess) return e;
-  return launch_pdl(few_router_kernel<TT>, dim3(blocks), dim3(kRouterThreads),
+  return launch_pdl(few_router_kernel<TT, EPB>, dim3(blocks), dim3(kRouterThreads),
                     (size_t)std::max(part, keys), st, r);
+}
+
+// Experts per router block: one while that gives at most a block per SM (the
+// fewer, the shorter each block's chain of loads), else two.
+template <int TT>
+cudaError_t launch_few_router(FewRoute& r, int hq_blocks, cudaStream_t st) {
+  const int epb = r.E <= kSplitTargetBlocks ? 1 : 2;
+  r.router_blocks = (r.E + epb - 1) / epb;
+  const int blocks = r.router_blocks + hq_blocks;
+  return epb == 1 ? launch_router_as<TT, 1>(r, blocks, st) : launch_router_as<TT, 2>(r, blocks, st);
 }
 
 }  // namespace
@@ -1108,17 +1180,16 @@ cudaError_t launch_few(const FewArgs& a, cudaStream_t st, const char** why) {
   FewRoute r{};
   r.h = a.h; r.Wr = a.Wr; r.bias = a.bias;
   r.T = d.T; r.D = d.D; r.E = d.E; r.k = d.k; r.scale = d.scale;
-  r.logits = a.logits;
+  r.scores = a.scores;
+  r.order = a.order;
   r.idx = a.idx; r.w = a.w;
   r.slot_of = a.slot_of; r.slot_expert = a.slot_expert; r.slot_mask = a.slot_mask;
   r.nslots = a.nslots; r.counts = a.counts;
   r.ticket = a.ticket;
   r.status = a.status;
-  r.router_blocks = (d.E + kRouterExperts - 1) / kRouterExperts;
   r.hq = a.hq; r.hqe = a.hqe;
   const int units = fp8 ? d.T * ((d.D + 127) / 128) : 0;
   const int hq_blocks = (units + kRouterWarps - 1) / kRouterWarps;
-  const int blocks = r.router_blocks + hq_blocks;
   r.hq_ready = a.claim + 2;
 
   FewFfn f{};
@@ -1170,11 +1241,11 @@ cudaError_t launch_few(const FewArgs& a, cudaStream_t st, const char** why) {
   f.status = a.status;
 
   *why = "router launch";
-  cudaError_t e = d.T <= 1   ? launch_few_router<1>(r, blocks, st)
-                  : d.T <= 2 ? launch_few_router<2>(r, blocks, st)
-                  : d.T <= 4 ? launch_few_router<4>(r, blocks, st)
-                  : d.T <= 8 ? launch_few_router<8>(r, blocks, st)
-                             : launch_few_router<16>(r, blocks, st);
+  cudaError_t e = d.T <= 1   ? launch_few_router<1>(r, hq_blocks, st)
+                  : d.T <= 2 ? launch_few_router<2>(r, hq_blocks, st)
+                  : d.T <= 4 ? launch_few_router<4>(r, hq_blocks, st)
+                  : d.T <= 8 ? launch_few_router<8>(r, hq_blocks, st)
+                             : launch_few_router<16>(r, hq_blocks, st);
   if (e != cudaSuccess) return e;
   *why = "expert launch";
   static std::atomic<uint64_t> set16{0}, set8{0};

@@ -61,7 +61,7 @@ struct WsLayout {
       counters_s, xperm,
       act_r, act_s, y, touched, gmask, total;
   // the few-token layer: its counters, and for T <= kFewMaxT its scratch
-  size_t f_claim, f_slots, f_mask, f_hq, f_hqe, f_act, f_exp, f_planes;
+  size_t f_claim, f_route, f_slots, f_mask, f_hq, f_hqe, f_act, f_exp, f_planes;
 };
 bool ws_layout(const moe_dims_t& d, WsLayout* out);
 
@@ -251,7 +251,8 @@ struct FewArgs {
   int32_t* idx;
   float* w;
   // workspace
-  float* logits;           // [T, E]
+  float* scores;           // [T, E]
+  uint32_t* order;         // [T, E]
   int32_t *slot_of, *slot_expert, *nslots, *counts, *touched, *ticket, *claim;
   uint32_t* slot_mask;
   uint8_t *hq, *a_r, *a_s;
