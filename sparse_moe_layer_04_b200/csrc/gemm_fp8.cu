@@ -18,16 +18,17 @@
 // the epilogue holds one output column, and a warp stores 32 neighbouring
 // columns of a row at a time.
 //
-// CTA structure (352 threads, tiles taken round-robin):
+// CTA structure (480 threads, tiles taken round-robin):
 //   warp 0      weight producer: TMA of 128 x 128 codes a stage, 128-byte
 //               swizzled, into a deep ring (the weights come from HBM)
-//   warp 10     row producer: TMA of up to NT x 128 codes a stage into a ring
+//   warp 14     row producer: TMA of up to NT x 128 codes a stage into a ring
 //               of its own (the rows are read again for every column tile, so
 //               they come from L2)
 //   warp 1      TMEM allocator and MMA issuer (one elected thread)
-//   warps 2-5   epilogue: TMEM -> registers -> global; two accumulators, so
-//               a tile's epilogue overlaps the next tile's products
-//   warps 6-9   scale writers: the exponents of sixteen K-blocks at a time,
+//   warps 2-9   epilogue: TMEM -> registers -> global, two warps for each lane
+//               quarter, which take turns of 16 rows; two accumulators, so a
+//               tile's epilogue overlaps the next tile's products
+//   warps 10-13 scale writers: the exponents of sixteen K-blocks at a time,
 //               loaded a row per thread while the sixteen before them are in
 //               use, exchanged through shared memory, and written as 32-bit
 //               words of four E8M0 bytes into one of two TMEM slots; each of
@@ -53,7 +54,8 @@ namespace {
 
 constexpr int kBK = 128;                 // K elements of a stage = one exponent
 constexpr int kWTile = 128 * kBK;        // weight tile bytes
-constexpr int kThreads = 352;
+constexpr int kEpiWarps = 8, kSfWarp0 = 2 + kEpiWarps, kRowWarp = kSfWarp0 + 4;
+constexpr int kThreads = (kRowWarp + 1) * 32;
 constexpr int kMaxStages = 11;          // of either ring
 constexpr int kRingBytes = 208 * 1024;
 constexpr int kMaxG = 1024;
@@ -219,38 +221,58 @@ __device__ __forceinline__ uint32_t scale_bytes(uint32_t w, int i, int n, bool* 
   return __vadd4(w, 0x7f7f7f7fu);
 }
 
-// Sixteen accumulator columns (rows of the group) of one weight row per
-// lane -> outputs.
+// silu(g) * u, for a result that is rounded to bf16 (the division is good to 2
+// units of fp32).
+__device__ __forceinline__ float gate_times(float g, float u) {
+  return __fdividef(g, 1.0f + __expf(-g)) * u;
+}
+
+// Sixteen accumulator columns (rows of the group, from c0) of one weight row
+// per lane -> outputs.
 template <bool GATED>
 __device__ __forceinline__ void store16(const GemmParams8& p, const Tile8& ti, int q, int lane,
-                                        int c0, const float (&v)[16]) {
+                                        int c0, const uint32_t (&v)[16]) {
+  const int left = ti.rows - c0;         // rows to store, the same in every lane
   if (GATED) {
     // lanes 0-15 finish the even rows of each pair, lanes 16-31 the odd ones
     const bool up = lane >= 16;
     const int n = ti.n0 + q * 16 + (lane & 15);
-    __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y);
+    __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y) +
+                       (size_t)(ti.row0 + c0 + (up ? 1 : 0)) * p.N + n;
+    const size_t step = 2 * (size_t)p.N;
+    const int mine = n < p.N ? left - (up ? 1 : 0) : 0;
 #pragma unroll
     for (int j = 0; j < 16; j += 2) {
-      const float got = __shfl_xor_sync(kAll, up ? v[j] : v[j + 1], 16);
-      const float gate = up ? got : v[j];
-      const float mul = up ? v[j + 1] : got;
-      const int c = c0 + j + (up ? 1 : 0);
-      if (c < ti.rows && n < p.N)
-        y[(size_t)(ti.row0 + c) * p.N + n] = __float2bfloat16_rn(ffn::silu_times(gate, mul));
+      const float got = __uint_as_float(__shfl_xor_sync(kAll, up ? v[j] : v[j + 1], 16));
+      const float own = __uint_as_float(up ? v[j + 1] : v[j]);
+      const float a = gate_times(up ? got : own, up ? own : got);
+      if (j < mine) *y = __float2bfloat16_rn(a);
+      y += step;
     }
   } else {
     const int n = ti.n0 + q * 32 + lane;
     if (n >= p.N) return;
+    const size_t at = (size_t)(ti.row0 + c0) * p.N + n;
     if (p.y_bf16) {
-      __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y) + (size_t)(ti.row0 + c0) * p.N + n;
+      __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y) + at;
+      if (left >= 16) {
 #pragma unroll
-      for (int j = 0; j < 16; ++j)
-        if (c0 + j < ti.rows) y[(size_t)j * p.N] = __float2bfloat16_rn(v[j]);
+        for (int j = 0; j < 16; ++j, y += p.N) *y = __float2bfloat16_rn(__uint_as_float(v[j]));
+      } else {
+#pragma unroll
+        for (int j = 0; j < 16; ++j, y += p.N)
+          if (j < left) *y = __float2bfloat16_rn(__uint_as_float(v[j]));
+      }
     } else {
-      float* y = static_cast<float*>(p.y) + (size_t)(ti.row0 + c0) * p.N + n;
+      float* y = static_cast<float*>(p.y) + at;
+      if (left >= 16) {
 #pragma unroll
-      for (int j = 0; j < 16; ++j)
-        if (c0 + j < ti.rows) y[(size_t)j * p.N] = v[j];
+        for (int j = 0; j < 16; ++j, y += p.N) *y = __uint_as_float(v[j]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 16; ++j, y += p.N)
+          if (j < left) *y = __uint_as_float(v[j]);
+      }
     }
   }
 }
@@ -279,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
       ptx::mbar_init(&ss.sf_full[i], 4);
       ptx::mbar_init(&ss.sf_empty[i], 1);
       ptx::mbar_init(&ss.acc_full[i], 1);
-      ptx::mbar_init(&ss.acc_empty[i], 4);
+      ptx::mbar_init(&ss.acc_empty[i], kEpiWarps);
     }
     ptx::mbar_init(&ss.drain, 1);
     ptx::mbar_init(&ss.sf_bar, 4);
@@ -311,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
   // scale words cover K-blocks 4s .. 4s + 3
   const int s0 = kb0 / 4, s1 = kb1 > kb0 ? (kb1 + 3) / 4 : s0;
 
-  if (warp == 0 || warp == 10) {
+  if (warp == 0 || warp == kRowWarp) {
     const bool wside = warp == 0;
     if (ptx::elect_one()) {
       // Both producers walk the weights' stages.  The row producer's own stage
@@ -401,8 +423,9 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
       ptx::mma_commit(&ss.drain);
       ffn::wait_drain(&ss.drain, 0, abort);
     }
-  } else if (warp < 6) {
+  } else if (warp < kSfWarp0) {
     const int q = warp & 3;              // TMEM lane quarter of this warp
+    const int half = (warp - 2) >> 2;    // its turn among the quarter's two warps
     int buf = 0;
     uint32_t aphase = 0;
     for (; walk.more(); walk.next()) {
@@ -410,21 +433,29 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
       if (__any_sync(kAll, !ptx::mbar_wait(&ss.acc_full[buf], aphase, abort))) break;
       ptx::tc_fence_after();
       const uint32_t acc = tmem + buf * NT + ((uint32_t)(q * 32) << 16);
-      for (int c = 0; c < ti.rows; c += 16) {
-        uint32_t r[16];
-        ptx::tmem_ld_x16(acc + c, r);
-        ptx::tmem_wait_ld();
-        float v[16];
-#pragma unroll
-        for (int j = 0; j < 16; ++j) v[j] = kb1 > kb0 ? __uint_as_float(r[j]) : 0.f;
+      auto use = [&](int c, const uint32_t (&v)[16]) {
         if (p.split > 1) {
-          // this CTA's part of the tile, [row][weight row], in the ring (all
-          // its loads and products are done, and a cluster has one tile)
-          float* part = reinterpret_cast<float*>(ring);
+          // this CTA's part of the tile, [row][weight row], in the ring (all its
+          // loads and products are done, and a cluster has one tile)
+          float* part = reinterpret_cast<float*>(ring) + (size_t)c * 128 + q * 32 + lane;
 #pragma unroll
-          for (int j = 0; j < 16; ++j) part[(c + j) * 128 + q * 32 + lane] = v[j];
+          for (int j = 0; j < 16; ++j) part[j * 128] = __uint_as_float(v[j]);
         } else {
           store16<GATED>(p, ti, q, lane, c, v);
+        }
+      };
+      // sixteen columns are read while the sixteen before them are stored
+      uint32_t a[16], b[16];
+      int c = half * 16;
+      if (c < ti.rows) ptx::tmem_ld_x16(acc + c, a);
+      for (; c < ti.rows; c += 64) {
+        ptx::tmem_wait_ld();
+        if (c + 32 < ti.rows) ptx::tmem_ld_x16(acc + c + 32, b);
+        use(c, a);
+        if (c + 32 < ti.rows) {
+          ptx::tmem_wait_ld();
+          if (c + 64 < ti.rows) ptx::tmem_ld_x16(acc + c + 64, a);
+          use(c + 32, b);
         }
       }
       ptx::tc_fence_before();
@@ -432,10 +463,10 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
       if (lane == 0) ptx::mbar_arrive(&ss.acc_empty[buf]);
       if (++buf == 2) { buf = 0; aphase ^= 1u; }
     }
-  } else if (warp < 10) {
+  } else {
     constexpr int RPT = (NT + 127) / 128;      // rows per thread
     constexpr int XC = (NT + 31) / 32;         // scale columns of the rows
-    const int tid = threadIdx.x - 192;
+    const int tid = threadIdx.x - kSfWarp0 * 32;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     ptx::WarpBarrier team_bar{&ss.sf_bar};
     int slot = 0, sbuf = 0;
@@ -523,32 +554,38 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
     if (own.more() && !*abort) {
       const Tile8 ti = own.tile(ss.gm, p);
       const uint32_t part = ptx::smem_addr(ring);
-      if (GATED) {
-        for (int i = threadIdx.x; i < ti.rows * 64; i += kThreads) {
-          const int c = i >> 6, f = i & 63;
-          if (c % p.split != rank) continue;
-          const uint32_t at = part + (c * 128 + (f >> 4) * 32 + (f & 15)) * 4;
-          float g = 0.f, u = 0.f;
-          for (int r = 0; r < p.split; ++r) {
-            g += ptx::ld_cluster_f32(at, r);
-            u += ptx::ld_cluster_f32(at + 64, r);
+      // a thread finishes four neighbouring weight rows; the parts of all ranks
+      // are on their way before the first is added
+      constexpr int QUADS = GATED ? 16 : 32;     // of output columns in a row of the tile
+      for (int i = threadIdx.x; i < ti.rows * QUADS; i += kThreads) {
+        const int c = i / QUADS, f = (i % QUADS) * 4;
+        if (c % p.split != rank || ti.n0 + f >= p.N) continue;
+        const uint32_t at = part + (c * 128 + (GATED ? (f >> 4) * 32 + (f & 15) : f)) * 4;
+        float4 v[8], w[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+          if (r < p.split) {
+            v[r] = ptx::ld_cluster_f32x4(at, r);
+            if (GATED) w[r] = ptx::ld_cluster_f32x4(at + 64, r);
           }
-          if (ti.n0 + f < p.N)
-            static_cast<__nv_bfloat16*>(p.y)[(size_t)(ti.row0 + c) * p.N + ti.n0 + f] =
-                __float2bfloat16_rn(ffn::silu_times(g, u));
-        }
-      } else {
-        for (int i = threadIdx.x; i < ti.rows * 128; i += kThreads) {
-          const int c = i >> 7, f = i & 127;
-          if (c % p.split != rank) continue;
-          float v = 0.f;
-          for (int r = 0; r < p.split; ++r) v += ptx::ld_cluster_f32(part + i * 4, r);
-          const size_t at = (size_t)(ti.row0 + c) * p.N + ti.n0 + f;
-          if (ti.n0 + f < p.N) {
-            if (p.y_bf16) static_cast<__nv_bfloat16*>(p.y)[at] = __float2bfloat16_rn(v);
-            else static_cast<float*>(p.y)[at] = v;
+        float4 s = v[0], u = w[0];
+#pragma unroll
+        for (int r = 1; r < 8; ++r)
+          if (r < p.split) {
+            s.x += v[r].x; s.y += v[r].y; s.z += v[r].z; s.w += v[r].w;
+            if (GATED) { u.x += w[r].x; u.y += w[r].y; u.z += w[r].z; u.w += w[r].w; }
           }
+        if (GATED) {
+          s.x = gate_times(s.x, u.x); s.y = gate_times(s.y, u.y);
+          s.z = gate_times(s.z, u.z); s.w = gate_times(s.w, u.w);
         }
+        // (N is a multiple of 8: four columns are all there or not at all)
+        const size_t out = (size_t)(ti.row0 + c) * p.N + ti.n0 + f;
+        if (GATED || p.y_bf16)
+          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.y) + out) =
+              make_uint2(ffn::pack_bf16(s.x, s.y), ffn::pack_bf16(s.z, s.w));
+        else
+          *reinterpret_cast<float4*>(static_cast<float*>(p.y) + out) = s;
       }
     }
     ptx::cluster_sync();   // no CTA leaves while another reads its part
@@ -625,16 +662,24 @@ cudaError_t launch_gemm_fp8(const Gemm8Args& a, cudaStream_t st, const char** wh
   // Rows per tile.  240 (two accumulators of that width fill tensor memory) read
   // the weights for the most rows; narrower tiles leave shared memory to the
   // weights' ring.  So: the narrowest that cuts a group into no more blocks
-  // than 240 would, for groups two standard deviations above the average.
-  const int avg = (a.R + a.G - 1) / a.G;
+  // than 240 would, for groups two standard deviations above the average; and
+  // narrower still while that leaves SMs without a tile.
+  const int groups = std::min(a.G, a.R), avg = (a.R + groups - 1) / groups;
   const int top = a.G > 1 ? avg + (int)(2.f * sqrtf((float)avg)) : avg;
   const int nb = (top + 239) / 240, need = (top + nb - 1) / nb;
-  if (need <= 32) return launch_any<32>(p, gated, st, why, a);
-  if (need <= 64) return launch_any<64>(p, gated, st, why, a);
-  if (need <= 96) return launch_any<96>(p, gated, st, why, a);
-  if (need <= 144) return launch_any<144>(p, gated, st, why, a);
-  if (need <= 160) return launch_any<160>(p, gated, st, why, a);
-  return launch_any<240>(p, gated, st, why, a);
+  constexpr int widths[] = {32, 64, 96, 144, 160, 240};
+  int w = 0;
+  while (widths[w] < need) ++w;
+  const long long cols = gated ? (a.N + 63) / 64 : (a.N + 127) / 128;
+  while (w > 0 && (long long)groups * ((avg + widths[w] - 1) / widths[w]) * cols < num_sms()) --w;
+  switch (widths[w]) {
+    case 32: return launch_any<32>(p, gated, st, why, a);
+    case 64: return launch_any<64>(p, gated, st, why, a);
+    case 96: return launch_any<96>(p, gated, st, why, a);
+    case 144: return launch_any<144>(p, gated, st, why, a);
+    case 160: return launch_any<160>(p, gated, st, why, a);
+    default: return launch_any<240>(p, gated, st, why, a);
+  }
 }
 
 }  // namespace moe

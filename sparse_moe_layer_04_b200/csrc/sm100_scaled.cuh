@@ -102,14 +102,15 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// The float at this CTA's shared address `addr` in CTA `rank` of the cluster.
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr, uint32_t rank) {
-  float v;
+// The four floats at this CTA's shared address `addr` in CTA `rank` of the
+// cluster.
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr, uint32_t rank) {
+  float4 v;
   asm volatile(
       "{\n\t.reg .u32 a;\n\t"
-      "mapa.shared::cluster.u32 a, %1, %2;\n\t"
-      "ld.shared::cluster.f32 %0, [a];\n\t}"
-      : "=f"(v)
+      "mapa.shared::cluster.u32 a, %4, %5;\n\t"
+      "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n\t}"
+      : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
       : "r"(addr), "r"(rank)
       : "memory");
   return v;
