@@ -599,7 +599,7 @@ int check_gemm_fp8(const void* x, const int8_t* xe, const int32_t* offsets, cons
   if (K < 16 || K % 16) return fail(MOE_ERR_INVALID_ARG, "K = %d not a positive multiple of 16", K);
   if ((long long)G * N >= (1ll << 31)) return fail(MOE_ERR_UNSUPPORTED, "G*N >= 2^31");
   // tiles are numbered with 32 bits: R / 32 + G row blocks times N / 64 columns
-  if (((long long)R / 32 + G + 1) * (N / 64 + 1) >= (1ll << 31))
+  if (((long long)R / 32 + G + 1) * (N / 64 + 1) >= (1ll << 30))
     return fail(MOE_ERR_UNSUPPORTED, "R x N is too large for one call");
   if (G > 1 && !offsets) return fail(MOE_ERR_INVALID_ARG, "offsets is NULL with G > 1");
   if (R == 0) return MOE_OK;

@@ -367,7 +367,7 @@ struct alignas(64) FewFfn {
   CUtensorMap w1_r, w3_r, w1_s, w3_s;    // [E * F, D], box 16 rows
   CUtensorMap w2_r, w2_s;                // [E * D, F], box 128 rows
   const int8_t *e1_r, *e3_r, *e2_r, *e1_s, *e3_s, *e2_s;
-  int T, D, F, k, S, Fs;
+  int T, D, E, F, k, S, Fs;
   int NX, PA;            // token operand rows: gate/up, down
   // features per gate/up tile (64, 32 or 16) and K-blocks per stage of one,
   // of a chosen and of a shared expert
@@ -474,15 +474,16 @@ __device__ __forceinline__ bool pieces_wait(const FewFfn& p, volatile int* abort
   return !__any_sync(kAll, !ptx::counter_wait(p.claim + 2, p.hq_blocks, abort));
 }
 
-// Up to four exponents q[0 .. n-1] (n >= 1): the aligned words that hold them,
-// so that the loads can be under way long before the bytes are put together.
+// Up to four exponents q[0 .. n-1] (n >= 1) of an array [lo, hi): the aligned
+// words that hold them, so that the loads can be under way long before the
+// bytes are put together.
 struct RawScales {
   uint32_t a, b;
-  __device__ __forceinline__ void load(const int8_t* q, int n) {
+  __device__ __forceinline__ void load(const int8_t* q, int n, const int8_t* lo, const int8_t* hi) {
     const uintptr_t at = reinterpret_cast<uintptr_t>(q);
     const uint32_t* base = reinterpret_cast<const uint32_t*>(at & ~(uintptr_t)3);
-    a = __ldcg(base);
-    b = 4 - (int)(at & 3) < n ? __ldcg(base + 1) : 0u;
+    a = ptx::exp_word(base, lo, hi);
+    b = 4 - (int)(at & 3) < n ? ptx::exp_word(base + 1, lo, hi) : 0u;
   }
   // Four E8M0 bytes (exponents from n on count as 0); outside the weights' range
   // of [-117, 7] raises *bad.
@@ -998,14 +999,15 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
       if (u.down && !slot_wait(p, u.slot, abort)) break;
       int k0, k1;
       unit_k<EB>(p, u, &k0, &k1);
-      const int8_t* we;
+      // the weights' exponents: the array, and this unit's row of blocks in it
+      const int8_t* we0 = u.down          ? (sh ? p.e2_s : p.e2_r)
+                          : (lane & 16) ? (sh ? p.e3_s : p.e3_r)
+                                        : (sh ? p.e1_s : p.e1_r);
+      const int8_t* we_end = we0 + (size_t)(sh ? p.S : p.E) * KBF * KBD;
       const int KB = u.down ? KBF : KBD;
-      if (u.down) {
-        we = (sh ? p.e2_s : p.e2_r) + ((size_t)u.expert * KBD + u.at) * KB;
-      } else {
-        we = (lane & 16 ? (sh ? p.e3_s : p.e3_r) : (sh ? p.e1_s : p.e1_r)) +
-             ((size_t)u.expert * KBF + u.at / 128) * KB;
-      }
+      const int8_t* we = we0 + (u.down ? (size_t)u.expert * KBD + u.at
+                                       : (size_t)u.expert * KBF + u.at / 128) * KB;
+      const int8_t* hqe_end = p.hqe + (size_t)p.T * KBD;
       const int8_t* ae = (sh ? p.ae_s : p.ae_r) +
                          (size_t)(sh ? u.slot : u.slot - p.S) * p.T * (KBF * 4);
       // Token words: gate/up, one per row (the bytes are K-blocks); down, one per
@@ -1022,12 +1024,12 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
       RawScales ra, rx[2];
       uint32_t rd[4][2];
       auto load = [&](int s) {
-        ra.load(we + 4 * s, KB - 4 * s);
+        ra.load(we + 4 * s, KB - 4 * s, we0, we_end);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           if (!xq[j]) continue;
           if (!u.down) {
-            rx[j].load(xq[j] + 4 * s, KBD - 4 * s);
+            rx[j].load(xq[j] + 4 * s, KBD - 4 * s, p.hqe, hqe_end);
           } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -1221,7 +1223,7 @@ cudaError_t launch_few(const FewArgs& a, cudaStream_t st, const char** why) {
     f.e1_r = a.w8->W1e; f.e3_r = a.w8->W3e; f.e2_r = a.w8->W2e;
     f.e1_s = a.w8->Ws1e; f.e3_s = a.w8->Ws3e; f.e2_s = a.w8->Ws2e;
   }
-  f.T = d.T; f.D = d.D; f.F = d.F; f.k = d.k; f.S = d.S; f.Fs = Fs;
+  f.T = d.T; f.D = d.D; f.E = d.E; f.F = d.F; f.k = d.k; f.S = d.S; f.Fs = Fs;
   f.NX = L.NX; f.PA = L.PA;
   f.fpt_r = L.fpt_r; f.fpt_s = L.fpt_s; f.sub_r = L.sub_r; f.sub_s = L.sub_s;
   f.parts = L.parts; f.nd = L.nd;

@@ -199,15 +199,17 @@ struct Walk {
   }
 };
 
-// Exponents q[0 .. n-1] (n <= 16) as they stand in memory, in words of four.
-// Any alignment: the aligned words that hold them are loaded and shifted.
-__device__ __forceinline__ void load_exps(const int8_t* q, int n, uint32_t (&w)[4]) {
+// Exponents q[0 .. n-1] (n <= 16) of an array [lo, hi) as they stand in memory,
+// in words of four.  Any alignment: the aligned words that hold them are
+// loaded and shifted.
+__device__ __forceinline__ void load_exps(const int8_t* q, int n, const int8_t* lo,
+                                          const int8_t* hi, uint32_t (&w)[4]) {
   const uintptr_t at = reinterpret_cast<uintptr_t>(q);
   const uint32_t* base = reinterpret_cast<const uint32_t*>(at & ~(uintptr_t)3);
   const int off = (int)(at & 3);
   uint32_t v[5];
 #pragma unroll
-  for (int i = 0; i < 5; ++i) v[i] = 4 * i - off < n ? __ldg(base + i) : 0u;
+  for (int i = 0; i < 5; ++i) v[i] = 4 * i - off < n ? ptx::exp_word(base + i, lo, hi) : 0u;
 #pragma unroll
   for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(v[i], v[i + 1], 8 * off);
 }
@@ -480,11 +482,13 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
 #pragma unroll
       for (int i = 0; i < RPT; ++i) {
         const int r = tid + 128 * i;
-        if (r < ti.rows) load_exps(p.xe + (size_t)(ti.row0 + r) * p.KB + 16 * c, n, xw[i]);
+        if (r < ti.rows)
+          load_exps(p.xe + (size_t)(ti.row0 + r) * p.KB + 16 * c, n, p.xe,
+                    p.xe + (size_t)p.R * p.KB, xw[i]);
       }
-      load_exps((GATED && (lane & 16) ? p.w3e : p.w1e) +
-                    ((size_t)ti.g * p.NB + ti.n0 / 128) * p.KB + 16 * c,
-                n, ww);
+      const int8_t* we = GATED && (lane & 16) ? p.w3e : p.w1e;
+      load_exps(we + ((size_t)ti.g * p.NB + ti.n0 / 128) * p.KB + 16 * c, n, we,
+                we + (size_t)p.G * p.NB * p.KB, ww);
     };
     int c = c0;
     Tile8 ti{};

@@ -72,6 +72,19 @@ __device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const uint32_t* r) {
       : "memory");
 }
 
+// The aligned word of exponents at `w`, of an array [lo, hi) of bytes: as one load
+// where the word lies inside, byte by byte at the array's two ends (bytes outside
+// count as 0).
+__device__ __forceinline__ uint32_t exp_word(const uint32_t* w, const int8_t* lo, const int8_t* hi) {
+  const int8_t* b = reinterpret_cast<const int8_t*>(w);
+  if (b >= lo && b + 4 <= hi) return __ldcg(w);
+  uint32_t v = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (b + i >= lo && b + i < hi) v |= (uint32_t)(uint8_t)__ldcg(b + i) << (8 * i);
+  return v;
+}
+
 // A barrier of a few warps whose wait is bounded: an mbarrier that one lane of
 // each warp arrives on.  False when the wait gave up (as mbar_wait).
 struct WarpBarrier {

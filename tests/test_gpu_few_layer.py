@@ -37,7 +37,7 @@ class Layer:
     def __init__(self, moe, T, D, E, F, k, S, Fs, fp8, scale=2.5, seed=0):
         g = torch.Generator(device="cuda").manual_seed(seed + 7 * D + E)
         self.moe, self.fp8, self.T, self.D, self.E, self.k, self.S = moe, fp8, T, D, E, k, S
-        Fs = max(Fs, 16)
+        Fs = Fs or 16
         self.F, self.Fs = F, Fs
         self.d = moe.dims(T=T, D=D, E=E, F=F, k=k, S=S, Fs=Fs, scale=scale)
 
@@ -129,7 +129,8 @@ class Layer:
 
 
 CASES = [  # T, D, E, F, k, S, Fs
-    (1, 16, 1, 16, 1, 0, 0),            # the smallest layer
+    (1, 16, 1, 16, 1, 0, 0),            # the smallest layer, FP8 weights
+    (2, 8, 3, 8, 2, 1, 8),              # the smallest sizes, bf16 weights
     (1, 128, 8, 64, 2, 1, 64),
     (5, 128, 8, 64, 2, 1, 64),          # the tiny layer
     (16, 256, 16, 192, 8, 1, 320),

@@ -299,3 +299,120 @@ def test_on_another_stream_and_in_a_graph(moe, status):
         moe.moe_quantize_fp8(h, x, xe)
         moe.moe_grouped_gemm_fp8(x, xe, W, We, want, offsets=off)
         assert torch.equal(y, want) and torch.equal(c, x)
+
+
+@pytest.mark.parametrize("shift", [1, 2, 3])
+def test_exponents_at_any_address(moe, status, shift):
+    """Exponent arrays that start and end off every alignment, with the bytes
+    around them holding what would be refused."""
+    def moved(t):
+        raw = torch.full((t.numel() + 8,), -128, dtype=torch.int8, device="cuda")
+        view = raw[shift:shift + t.numel()].view(t.shape)
+        view.copy_(t)
+        return view
+
+    for G, R, N, K in ((3, 50, 136, 1424), (1, 300, 72, 272), (1, 1, 256, 2048)):
+        x, xe, [(W, We), (W3, We3)] = operands(shift + R, G, R, N, K, 2)
+        off = torch.tensor(spread(G, R, 0, 0, 1), dtype=torch.int32, device="cuda")
+        a, b = torch.empty((R, N), device="cuda"), torch.empty((R, N), device="cuda")
+        moe.moe_grouped_gemm_fp8(x, xe, W, We, a, offsets=off, ws=status)
+        moe.moe_grouped_gemm_fp8(x, moved(xe), W, moved(We), b, offsets=off, ws=status)
+        assert torch.equal(a, b)
+        a, b = a.bfloat16(), b.bfloat16()
+        moe.moe_gated_gemm_fp8(x, xe - 9, W, We, W3, We3, a, offsets=off, ws=status)
+        moe.moe_gated_gemm_fp8(x, moved(xe - 9), W, moved(We), W3, moved(We3), b, offsets=off, ws=status)
+        assert torch.equal(a, b)
+
+
+def test_wide_rows_and_every_row_tile(moe, status):
+    """Average group sizes on both sides of every row-tile width, with columns
+    enough that the widths are chosen by the rows."""
+    for avg in (31, 33, 60, 70, 92, 100, 120, 142, 150, 170, 239, 250):
+        G, N, K = 12, 1664, 144
+        x, xe, [(W, We)] = operands(avg, G, avg * G, N, K)
+        bounds = spread(G, avg * G, 0, 0, avg)
+        off = torch.tensor(bounds, dtype=torch.int32, device="cuda")
+        y = torch.empty((avg * G, N), device="cuda")
+        moe.moe_grouped_gemm_fp8(x, xe, W, We, y, offsets=off, ws=status)
+        ref, mag = product64(x, xe, W, We, bounds)
+        assert bool(((y.double() - ref).abs() <= (K / 32 + 1) * 2.0 ** -22 * mag).all()), avg
+
+
+@pytest.mark.parametrize("T,D,E,F,k", [(37, 256, 12, 144, 3), (300, 384, 8, 256, 2)])
+def test_expert_ffn_from_8bit_products(moe, T, D, E, F, k):
+    """Routing, grouping, the two products with their quantisations, and the
+    merge, one after the other on one stream, as a layer with 8-bit activations
+    runs; every step against its definition on the step before, and the whole
+    against the layer with bf16 activations within what the roundings to E4M3
+    (half a step, 2^-4, or half the subnormal step, 2^-10 of the block's scale)
+    can make of it."""
+    gen = torch.Generator().manual_seed(T)
+    import moe_inputs as mi
+    d = moe.dims(T=T, D=D, E=E, F=F, k=k, S=0, Fs=16, scale=2.5)
+    ws = moe.alloc_workspace(d)
+    h = torch.randn(T, D, generator=gen).to(torch.bfloat16).cuda()
+    Wr, bias = (torch.randn(E, D, generator=gen) / D ** 0.5).cuda(), torch.zeros(E, device="cuda")
+    W = {n: mi.quantize_fp8_blocks((torch.randn(E, r, c, generator=gen) / c ** 0.5).bfloat16().cuda())
+         for n, (r, c) in dict(W1=(F, D), W3=(F, D), W2=(D, F)).items()}
+    i32 = dict(dtype=torch.int32, device="cuda")
+    idx, inv, rw = torch.empty((T, k), **i32), torch.empty((T, k), **i32), torch.empty((T, k), device="cuda")
+    counts, off, perm = torch.empty(E, **i32), torch.empty(E + 1, **i32), torch.empty(T * k, **i32)
+    logits, R = torch.empty((T, E), device="cuda"), T * k
+    xq, aq = (torch.empty((R, n), dtype=torch.uint8, device="cuda") for n in (D, F))
+    xe, ae = (torch.empty((R, blocks(n)), dtype=torch.int8, device="cuda") for n in (D, F))
+    act = torch.empty((R, F), dtype=torch.bfloat16, device="cuda")
+    y, out = torch.empty((R, D), device="cuda"), torch.empty((T, D), device="cuda")
+
+    def layer():
+        moe.moe_router_logits(h, Wr, d, logits, ws)
+        moe.moe_route(logits, bias, d, idx, rw, ws)
+        moe.moe_permute(idx, d, counts, off, perm, inv, ws)
+        moe.moe_quantize_fp8(h, xq, xe, idx=perm, ws=ws)
+        moe.moe_gated_gemm_fp8(xq, xe, *W["W1"], *W["W3"], act, offsets=off, ws=ws)
+        moe.moe_quantize_fp8(act, aq, ae, ws=ws)
+        moe.moe_grouped_gemm_fp8(aq, ae, *W["W2"], y, offsets=off, ws=ws)
+        moe.moe_combine(y, rw, inv, d, out, ws)
+
+    layer()
+    assert moe.moe_get_device_status(ws) == 0
+    bounds = off.tolist()
+    vals, e = quantize64(h[perm.long()])
+    assert torch.equal(TABLE[xq.cpu().long()], vals) and torch.equal(xe.cpu().int(), e.int())
+    g, gm = product64(xq, xe, *W["W1"], bounds)
+    u, um = product64(xq, xe, *W["W3"], bounds)
+    unit = (D / 32 + 1) * 2.0 ** -22
+    silu = g * torch.sigmoid(g)
+    tol = (2.0 ** -8 + 2.0 ** -16) * (silu * u).abs() + 1.1 * unit * gm * (u.abs() + unit * um) + \
+        silu.abs() * unit * um + 2.0 ** -133
+    assert bool(((act.double() - silu * u).abs() <= tol).all())
+    vals, e = quantize64(act)
+    assert torch.equal(TABLE[aq.cpu().long()], vals) and torch.equal(ae.cpu().int(), e.int())
+    ref, mag = product64(aq, ae, *W["W2"], bounds)
+    assert bool(((y.double() - ref).abs() <= (F / 32 + 1) * 2.0 ** -22 * mag).all())
+
+    # the whole, with activations that are not rounded to 8 bits
+    x = h.double()[perm.long()]
+    eh = 2.0 ** -4 * x.abs() + 2.0 ** -10 * torch.pow(2.0, xe.double().cpu()).cuda().repeat_interleave(128, 1)[:, :D]
+    whole, err = torch.zeros_like(out, dtype=torch.float64), torch.zeros_like(out, dtype=torch.float64)
+    for b in range(E):
+        r = slice(bounds[b], bounds[b + 1])
+        m1, m3, m2 = (matrix64(W[n][0][b], W[n][1][b]) for n in ("W1", "W3", "W2"))
+        gg, uu = x[r] @ m1.t(), x[r] @ m3.t()
+        eg, eu = eh[r] @ m1.abs().t(), eh[r] @ m3.abs().t()
+        s = gg * torch.sigmoid(gg)
+        ea = 1.1 * eg * (uu.abs() + eu) + s.abs() * eu
+        step = torch.pow(2.0, ae[r].double().cpu()).cuda().repeat_interleave(128, 1)[:, :F]
+        ea = ea + (2.0 ** -4 + 2.0 ** -7) * ((s * uu).abs() + ea) + 2.0 ** -10 * step
+        c = rw.double().flatten()[torch.argsort(inv.flatten())][r, None]
+        whole.index_add_(0, perm[r].long(), c * ((s * uu) @ m2.t()))
+        err.index_add_(0, perm[r].long(), c * (ea @ m2.abs().t()))
+    assert bool(((out.double() - whole).abs() <= 1.001 * err + 1e-5 * whole.abs()).all())
+    rel = float((out.double() - whole).norm() / whole.norm())
+    assert rel < 2.0 ** -4, rel            # no worse than one rounding of everything
+
+    graph, want = torch.cuda.CUDAGraph(), out.clone()
+    with torch.cuda.graph(graph):
+        layer()
+    out.zero_()
+    graph.replay()
+    assert torch.equal(out, want) and moe.moe_get_device_status(ws) == 0
