@@ -38,8 +38,8 @@
 //
 // The tensor core's bf16 form cuts off its running sum at each step of 16,
 // which over K = 6144 adds up to 1.5e-5 of the result (measured).  K-blocks
-// therefore take turns over as many accumulators as fit in tensor memory, and
-// the epilogue adds those in fp32.
+// therefore take turns over as many accumulators as fit in tensor memory, 48
+// K-blocks at a time, and the epilogue adds those in fp32.
 #include <algorithm>
 #include <climits>
 
@@ -359,6 +359,9 @@ __host__ __device__ constexpr int acc_cols(bool fp8) { return fp8 ? 192 : 240; }
 __device__ __forceinline__ int acc_count(bool fp8, int n, int kb) {
   return min((kb + 3) / 4, acc_cols(fp8) / n);
 }
+// K-blocks that go into one set before the epilogue takes it (a multiple of the
+// K-blocks of a stage and of a scale word).
+constexpr int kSegment = 48;
 constexpr int kQueue = 4;
 
 struct alignas(64) FewFfn {
@@ -758,60 +761,64 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
       const bool sh = u.slot < p.S;
       const int sub = u.down ? 1 : sh ? p.sub_s : p.sub_r;
       const int n = u.down ? p.PA : p.NX;
-      const int nacc = acc_count(FP8, n, k1 - k0);
       const uint32_t idesc = FP8 ? ptx::idesc_mxf8(128, n) : ptx::idesc_bf16_f32(128, n);
       // sizes of a K-block within its stage, in the descriptors' units of 16 bytes
       const int a_step = (u.down ? kAStage : (sh ? p.fpt_s : p.fpt_r) * 2 * 128) >> 4;
       const int b_step = n * 128 >> 4;
       bool ok = true;
-      if (ptx::elect_one()) {
-        ok = ptx::mbar_wait(&ss.acc_empty[buf], cph ^ 1u, abort);
-        uint32_t acc = tmem + buf * acc_cols(FP8);
-        const uint32_t acc_end = acc + nacc * n;
-        uint32_t more = 0;               // 0 in the first turn over the accumulators
-        int kk = k0;
-        while (ok && kk < k1) {
-          if (!ptx::mbar_wait(&ss.full[as], aph, abort)) { ok = false; break; }
-          uint64_t da = desc_a + as * (kAStage >> 4), db = desc_b + bs * (kBStage >> 4);
-          const int end = min(kk + sub, k1);
-          for (; kk < end; ++kk, da += a_step, db += b_step) {
-            if (FP8 && (kk == k0 || (kk & 3) == 0) &&
-                !ptx::mbar_wait(&ss.sf_full[slot], sph, abort)) { ok = false; break; }
-            ptx::tc_fence_after();
-            if (FP8) {
-              const uint32_t sfa = tmem + 2 * acc_cols(FP8) + slot * kSfSlot;
-              // gate/up: one word per row covers four K-blocks; down: one word per
-              // row and K-block covers its four steps of 32
-              const uint32_t sfb = sfa + 4 + (u.down ? (kk & 3) * 4 : 0);
+      for (int seg = k0; seg < k1 && ok; seg += kSegment) {
+        const int seg_end = min(seg + kSegment, k1);
+        if (ptx::elect_one()) {
+          ok = ptx::mbar_wait(&ss.acc_empty[buf], cph ^ 1u, abort);
+          const int nacc = acc_count(FP8, n, seg_end - seg);
+          uint32_t acc = tmem + buf * acc_cols(FP8);
+          const uint32_t acc_end = acc + nacc * n;
+          uint32_t more = 0;             // 0 in the first turn over the accumulators
+          int kk = seg;
+          while (ok && kk < seg_end) {
+            if (!ptx::mbar_wait(&ss.full[as], aph, abort)) { ok = false; break; }
+            uint64_t da = desc_a + as * (kAStage >> 4), db = desc_b + bs * (kBStage >> 4);
+            const int end = min(kk + sub, seg_end);
+            for (; kk < end; ++kk, da += a_step, db += b_step) {
+              if (FP8 && (kk == k0 || (kk & 3) == 0) &&
+                  !ptx::mbar_wait(&ss.sf_full[slot], sph, abort)) { ok = false; break; }
+              ptx::tc_fence_after();
+              if (FP8) {
+                const uint32_t sfa = tmem + 2 * acc_cols(FP8) + slot * kSfSlot;
+                // gate/up: one word per row covers four K-blocks; down: one word
+                // per row and K-block covers its four steps of 32
+                const uint32_t sfb = sfa + 4 + (u.down ? (kk & 3) * 4 : 0);
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                ptx::mma_mxf8_ss(acc, da + 2 * k, db + 2 * k,
-                                 idesc | ptx::idesc_sf_byte(kk & 3, u.down ? k : kk & 3), sfa, sfb,
-                                 k > 0 ? 1u : more);
-              if ((kk & 3) == 3 || kk == k1 - 1) {
-                ptx::mma_commit(&ss.sf_empty[slot]);
-                if (++slot == 2) { slot = 0; sph ^= 1u; }
+                for (int k = 0; k < 4; ++k)
+                  ptx::mma_mxf8_ss(acc, da + 2 * k, db + 2 * k,
+                                   idesc | ptx::idesc_sf_byte(kk & 3, u.down ? k : kk & 3), sfa,
+                                   sfb, k > 0 ? 1u : more);
+                if ((kk & 3) == 3 || kk == k1 - 1) {
+                  ptx::mma_commit(&ss.sf_empty[slot]);
+                  if (++slot == 2) { slot = 0; sph ^= 1u; }
+                }
+              } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  ptx::mma_f16_ss(acc, da + 2 * k, db + 2 * k, idesc, k > 0 ? 1u : more);
               }
-            } else {
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                ptx::mma_f16_ss(acc, da + 2 * k, db + 2 * k, idesc, k > 0 ? 1u : more);
+              acc += n;
+              if (acc == acc_end) {
+                acc -= nacc * n;
+                more = 1;
+              }
             }
-            acc += n;
-            if (acc == acc_end) {
-              acc -= nacc * n;
-              more = 1;
-            }
+            if (!ok) break;
+            ptx::mma_commit(&ss.empty[as]);
+            if (++as == kAStages) { as = 0; aph ^= 1u; }
+            if (++bs == kBStages) bs = 0;
           }
-          if (!ok) break;
-          ptx::mma_commit(&ss.empty[as]);
-          if (++as == kAStages) { as = 0; aph ^= 1u; }
-          if (++bs == kBStages) bs = 0;
+          if (ok) ptx::mma_commit(&ss.acc_full[buf]);
         }
-        if (ok) ptx::mma_commit(&ss.acc_full[buf]);
+        if (++buf == 2) { buf = 0; cph ^= 1u; }
+        ok = !__any_sync(kAll, !ok);
       }
-      if (++buf == 2) { buf = 0; cph ^= 1u; }
-      if (__any_sync(kAll, !ok)) break;
+      if (!ok) break;
     }
     // nothing of this CTA is in flight when its tensor memory is freed
     if (ptx::elect_one()) {
@@ -866,21 +873,22 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
       const uint32_t mask = u.mask;
       int k0, k1;
       unit_k<EB>(p, u, &k0, &k1);
-      if (__any_sync(kAll, !ptx::mbar_wait(&ss.acc_full[buf], cph, abort))) break;
-      ptx::tc_fence_after();
-      const uint32_t acc = tmem + buf * acc_cols(FP8) + lanes;
       // the token columns, pieces and accumulators added: v[t] is this lane's
       // weight row
       const int pieces = u.down ? (FP8 ? kPiecesA : kPiecesB) : (FP8 ? kPiecesH : 1);
       const int n = u.down ? p.PA : p.NX;
-      const int nacc = acc_count(FP8, n, k1 - k0);
       const int fpt = sh ? p.fpt_s : p.fpt_r;
       const bool rows = u.down || qt * 16 < fpt;     // this warp's rows belong to the tile
       float v[16];
 #pragma unroll
       for (int t = 0; t < 16; ++t) v[t] = 0.f;
-      if (rows) {
-        for (int c = pieces - 1; c >= 0; --c) {        // smallest piece first
+      bool ok = true;
+      for (int seg = k0; seg < k1; seg += kSegment) {
+        if (__any_sync(kAll, !ptx::mbar_wait(&ss.acc_full[buf], cph, abort))) { ok = false; break; }
+        ptx::tc_fence_after();
+        const uint32_t acc = tmem + buf * acc_cols(FP8) + lanes;
+        const int nacc = acc_count(FP8, n, min(kSegment, k1 - seg));
+        for (int c = rows ? pieces - 1 : -1; c >= 0; --c) {   // smallest piece first
           float s[16];
 #pragma unroll
           for (int t = 0; t < 16; ++t) s[t] = 0.f;
@@ -900,11 +908,12 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
 #pragma unroll
           for (int t = 0; t < 16; ++t) v[t] += s[t];
         }
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&ss.acc_empty[buf]);
+        if (++buf == 2) { buf = 0; cph ^= 1u; }
       }
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(&ss.acc_empty[buf]);
-      if (++buf == 2) { buf = 0; cph ^= 1u; }
+      if (!ok) break;
 
       if (!u.down) {
         const int F = sh ? p.Fs : p.F;
