@@ -477,21 +477,29 @@ __device__ __forceinline__ bool pieces_wait(const FewFfn& p, volatile int* abort
   return !__any_sync(kAll, !ptx::counter_wait(p.claim + 2, p.hq_blocks, abort));
 }
 
-// Up to four exponents q[0 .. n-1] (n >= 1) of an array [lo, hi): the aligned
-// words that hold them, so that the loads can be under way long before the
-// bytes are put together.
+// Up to four exponents q[0 .. n-1] (n >= 1): the aligned words that hold them
+// (`inside`: these lie within the array; else the bytes), so that the loads can
+// be under way long before the bytes are put together.
 struct RawScales {
   uint32_t a, b;
-  __device__ __forceinline__ void load(const int8_t* q, int n, const int8_t* lo, const int8_t* hi) {
-    const uintptr_t at = reinterpret_cast<uintptr_t>(q);
-    const uint32_t* base = reinterpret_cast<const uint32_t*>(at & ~(uintptr_t)3);
-    a = ptx::exp_word(base, lo, hi);
-    b = 4 - (int)(at & 3) < n ? ptx::exp_word(base + 1, lo, hi) : 0u;
+  int shift;
+  __device__ __forceinline__ void load(const int8_t* q, int n, bool inside) {
+    if (inside) {
+      const uintptr_t at = reinterpret_cast<uintptr_t>(q);
+      const uint32_t* base = reinterpret_cast<const uint32_t*>(at & ~(uintptr_t)3);
+      shift = 8 * (int)(at & 3);
+      a = __ldcg(base);
+      b = 4 - (int)(at & 3) < n ? __ldcg(base + 1) : 0u;
+    } else {
+      shift = 0;
+      a = ptx::bytes_word(q, n);
+      b = 0;
+    }
   }
   // Four E8M0 bytes (exponents from n on count as 0); outside the weights' range
   // of [-117, 7] raises *bad.
-  __device__ __forceinline__ uint32_t word(const int8_t* q, int n, bool check, bool* bad) const {
-    uint32_t w = __funnelshift_r(a, b, 8 * (int)(reinterpret_cast<uintptr_t>(q) & 3));
+  __device__ __forceinline__ uint32_t word(int n, bool check, bool* bad) const {
+    uint32_t w = __funnelshift_r(a, b, shift);
     if (n < 4) w &= (1u << (8 * n)) - 1u;
     if (check) *bad |= (__vcmpgts4(w, 0x07070707u) | __vcmplts4(w, 0x8b8b8b8bu)) != 0;
     return __vadd4(w, 0x7f7f7f7fu);
@@ -1016,7 +1024,7 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
       const int KB = u.down ? KBF : KBD;
       const int8_t* we = we0 + (u.down ? (size_t)u.expert * KBD + u.at
                                        : (size_t)u.expert * KBF + u.at / 128) * KB;
-      const int8_t* hqe_end = p.hqe + (size_t)p.T * KBD;
+      const bool inside = ptx::words_inside(we, KB, we0, we_end);
       const int8_t* ae = (sh ? p.ae_s : p.ae_r) +
                          (size_t)(sh ? u.slot : u.slot - p.S) * p.T * (KBF * 4);
       // Token words: gate/up, one per row (the bytes are K-blocks); down, one per
@@ -1033,12 +1041,13 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
       RawScales ra, rx[2];
       uint32_t rd[4][2];
       auto load = [&](int s) {
-        ra.load(we + 4 * s, KB - 4 * s, we0, we_end);
+        ra.load(we + 4 * s, KB - 4 * s, inside);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           if (!xq[j]) continue;
           if (!u.down) {
-            rx[j].load(xq[j] + 4 * s, KBD - 4 * s, p.hqe, hqe_end);
+            // (in the workspace, with room behind them)
+            rx[j].load(xq[j] + 4 * s, KBD - 4 * s, true);
           } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -1051,7 +1060,7 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
       load(k0 / 4);
       for (int s = k0 / 4; s * 4 < k1; ++s) {
         uint32_t wa[4], wx[4][2];
-        wa[0] = wa[1] = wa[2] = wa[3] = ra.word(we + 4 * s, KB - 4 * s, true, &bad);
+        wa[0] = wa[1] = wa[2] = wa[3] = ra.word(KB - 4 * s, true, &bad);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const uint32_t lower = 0x04040404u * row_c[j];   // a piece's scale is 2^-4 of the one before
@@ -1060,7 +1069,7 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
             wx[i][j] = 0x7f7f7f7fu;      // rows of no token: any valid scale
             if (!xq[j]) continue;
             if (!u.down) {
-              if (i == 0) wx[i][j] = __vsub4(rx[j].word(xq[j] + 4 * s, KBD - 4 * s, false, &bad), lower);
+              if (i == 0) wx[i][j] = __vsub4(rx[j].word(KBD - 4 * s, false, &bad), lower);
             } else if (4 * s + i < KBF) {
               // exponents past the last feature count as 0 (their codes are zero)
               const int n = fe - 4 * (4 * s + i);

@@ -201,15 +201,20 @@ struct Walk {
 
 // Exponents q[0 .. n-1] (n <= 16) of an array [lo, hi) as they stand in memory,
 // in words of four.  Any alignment: the aligned words that hold them are
-// loaded and shifted.
+// loaded and shifted, but for those that reach beyond the array's ends.
 __device__ __forceinline__ void load_exps(const int8_t* q, int n, const int8_t* lo,
                                           const int8_t* hi, uint32_t (&w)[4]) {
+  if (!ptx::words_inside(q, n, lo, hi)) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = ptx::bytes_word(q + 4 * i, n - 4 * i);
+    return;
+  }
   const uintptr_t at = reinterpret_cast<uintptr_t>(q);
   const uint32_t* base = reinterpret_cast<const uint32_t*>(at & ~(uintptr_t)3);
   const int off = (int)(at & 3);
   uint32_t v[5];
 #pragma unroll
-  for (int i = 0; i < 5; ++i) v[i] = 4 * i - off < n ? ptx::exp_word(base + i, lo, hi) : 0u;
+  for (int i = 0; i < 5; ++i) v[i] = 4 * i - off < n ? __ldcg(base + i) : 0u;
 #pragma unroll
   for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(v[i], v[i + 1], 8 * off);
 }

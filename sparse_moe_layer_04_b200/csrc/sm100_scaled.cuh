@@ -72,16 +72,20 @@ __device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const uint32_t* r) {
       : "memory");
 }
 
-// The aligned word of exponents at `w`, of an array [lo, hi) of bytes: as one load
-// where the word lies inside, byte by byte at the array's two ends (bytes outside
-// count as 0).
-__device__ __forceinline__ uint32_t exp_word(const uint32_t* w, const int8_t* lo, const int8_t* hi) {
-  const int8_t* b = reinterpret_cast<const int8_t*>(w);
-  if (b >= lo && b + 4 <= hi) return __ldcg(w);
+// Whether the aligned words that hold q[0 .. n-1] lie inside the array [lo, hi)
+// of bytes, as they do everywhere but at an unaligned array's two ends.
+__device__ __forceinline__ bool words_inside(const int8_t* q, int n, const int8_t* lo,
+                                             const int8_t* hi) {
+  const uintptr_t first = reinterpret_cast<uintptr_t>(q) & ~(uintptr_t)3;
+  const uintptr_t end = (reinterpret_cast<uintptr_t>(q + n) + 3) & ~(uintptr_t)3;
+  return first >= reinterpret_cast<uintptr_t>(lo) && end <= reinterpret_cast<uintptr_t>(hi);
+}
+// Bytes q[0 .. n-1] (at most four) as a word, byte by byte.
+__device__ __forceinline__ uint32_t bytes_word(const int8_t* q, int n) {
   uint32_t v = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    if (b + i >= lo && b + i < hi) v |= (uint32_t)(uint8_t)__ldcg(b + i) << (8 * i);
+    if (i < n) v |= (uint32_t)(uint8_t)__ldcg(q + i) << (8 * i);
   return v;
 }
 
