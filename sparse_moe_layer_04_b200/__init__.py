@@ -128,10 +128,10 @@ def _device() -> int:
         return -2
 
 
-def _stream(stream) -> int:
+def _stream(stream, dev: Optional[int] = None) -> int:
     if stream is None:
         # the current stream's handle without building a torch.cuda.Stream (3 us a call)
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if dev is None else dev)
     return getattr(stream, "cuda_stream", stream)
 
 
@@ -279,7 +279,7 @@ def moe_forward_few(h, Wr, bias, W1, W3, W2, Ws1, Ws3, Ws2, d, out, ws, idx_out=
     _check(_lib.moe_forward_few(*_few_routing(h, Wr, bias, d, dev), _arg(W1, bf, (E, F, D), dev, "W1"),
                                 _arg(W3, bf, (E, F, D), dev, "W3"), _arg(W2, bf, (E, D, F), dev, "W2"),
                                 *shared, ctypes.byref(d),
-                                *_few_outputs(d, out, idx_out, w_out, ws, dev), _stream(stream)))
+                                *_few_outputs(d, out, idx_out, w_out, ws, dev), _stream(stream, dev)))
 
 
 def moe_forward_few_fp8(h, Wr, bias, w8: moe_fp8_weights_t, d, out, ws, idx_out=None, w_out=None,
@@ -288,7 +288,7 @@ def moe_forward_few_fp8(h, Wr, bias, w8: moe_fp8_weights_t, d, out, ws, idx_out=
     dev = _device()
     _check(_lib.moe_forward_few_fp8(*_few_routing(h, Wr, bias, d, dev), ctypes.byref(w8),
                                     ctypes.byref(d), *_few_outputs(d, out, idx_out, w_out, ws, dev),
-                                    _stream(stream)))
+                                    _stream(stream, dev)))
 
 
 def moe_fp8_dequantize(codes, exps, out, ws=None, stream=None) -> None:
@@ -352,7 +352,7 @@ def moe_quantize_fp8(x, codes, exps, idx=None, ws=None, stream=None) -> None:
         None if idx is None else _arg(idx, torch.int32, (R,), dev, "idx"), R, K,
         _codes(codes, (R, K), dev, "codes"),
         _arg(exps, torch.int8, (R, (K + 127) // 128), dev, "exps"), _ws_arg(ws, dev)[0],
-        _stream(stream)))
+        _stream(stream, dev)))
 
 
 def _product_sizes(x, W):
@@ -379,7 +379,7 @@ def moe_grouped_gemm_fp8(x, xe, W, We, y, offsets=None, ws=None, stream=None) ->
         None if offsets is None else _arg(offsets, torch.int32, (G + 1,), dev, "offsets"),
         _codes(W, (*lead, N, K), dev, "W"), _arg(We, torch.int8, eshape, dev, "We"), G, R, N, K,
         _arg(y, y.dtype, (R, N), dev, "y"), int(y.dtype is torch.bfloat16), _ws_arg(ws, dev)[0],
-        _stream(stream)))
+        _stream(stream, dev)))
 
 
 def moe_gated_gemm_fp8(x, xe, W1, W1e, W3, W3e, act, offsets=None, ws=None, stream=None) -> None:
@@ -392,7 +392,7 @@ def moe_gated_gemm_fp8(x, xe, W1, W1e, W3, W3e, act, offsets=None, ws=None, stre
         None if offsets is None else _arg(offsets, torch.int32, (G + 1,), dev, "offsets"),
         _codes(W1, (*lead, N, K), dev, "W1"), _arg(W1e, torch.int8, eshape, dev, "W1e"),
         _codes(W3, (*lead, N, K), dev, "W3"), _arg(W3e, torch.int8, eshape, dev, "W3e"), G, R, N, K,
-        _arg(act, torch.bfloat16, (R, N), dev, "act"), _ws_arg(ws, dev)[0], _stream(stream)))
+        _arg(act, torch.bfloat16, (R, N), dev, "act"), _ws_arg(ws, dev)[0], _stream(stream, dev)))
 
 
 def moe_gather_rows(src, idx, dst, ws=None, stream=None) -> None:
