@@ -199,11 +199,10 @@ bool ws_layout(const moe_dims_t& d, WsLayout* L) {
     const size_t act = std::max((most * F + S * Fs) * p16.PA * 2 + 16,
                                 (most * F + S * Fs) * p8.PA + 16) + 256;
     const size_t ex = (most * ((F + 127) / 128) + S * ((Fs + 127) / 128)) * 4 * T + 256;
-    // planes of the down products: few_plan splits K only while there are
-    // fewer than 6 * 148 units, so at most twice that many units are split;
-    // the bound grows with T, so that a workspace serves every smaller T
-    const size_t planes =
-        std::max(slots, std::min<size_t>(8 * slots, 12 * kSplitTargetBlocks / p16.nd));
+    // planes of the down products: few_plan splits K only while all the parts
+    // of all units are at most kSplitTargetBlocks, so the bound grows with T and
+    // a workspace serves every smaller T
+    const size_t planes = std::max(slots, (size_t)kSplitTargetBlocks / p16.nd);
     L->f_route = take(2 * T * E * 4);
     L->f_slots = take((64 + T * k + slots) * 4);
     L->f_mask = take(slots * 4);

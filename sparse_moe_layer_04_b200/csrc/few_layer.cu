@@ -46,7 +46,6 @@
 #include <cuda_bf16.h>
 
 #include "ffn_common.cuh"
-#include "fp8_convert.cuh"
 #include "route_order.cuh"
 #include "sm100_scaled.cuh"
 
@@ -56,6 +55,7 @@ namespace {
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kRouterThreads = 512;
 constexpr int kRouterWarps = kRouterThreads / 32;
+constexpr int EPB = 2;                   // experts per router block
 constexpr int kPiecesH = 3, kPiecesA = 4;   // E4M3 pieces of a hidden value, an activation
 constexpr int kPiecesB = 3;                 // bf16 pieces of an activation
 constexpr int kPieceMinExp = -115;       // the last piece's exponent stays an E8M0 value
@@ -145,7 +145,7 @@ __device__ __forceinline__ int block_exp(float top) {
 }
 
 // Logits of EPB experts for every token, their scores and keys.
-template <int TT, int EPB>
+template <int TT>
 __device__ __forceinline__ void router_block(const FewRoute& p, float* s_part) {
   const int e0 = blockIdx.x * EPB;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -309,7 +309,7 @@ __device__ __forceinline__ void split_hidden(const FewRoute& p, int unit, int la
   }
 }
 
-template <int TT, int EPB>
+template <int TT>
 __global__ void __launch_bounds__(kRouterThreads) few_router_kernel(const FewRoute p) {
   extern __shared__ uint32_t s_dyn[];
   ptx::pdl_wait();
@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(kRouterThreads) few_router_kernel(const FewRou
     if (threadIdx.x == 0) atomicAdd(p.hq_ready, 1);
     return;
   }
-  router_block<TT, EPB>(p, reinterpret_cast<float*>(s_dyn));
+  router_block<TT>(p, reinterpret_cast<float*>(s_dyn));
   // the block that finishes last selects
   __shared__ int s_last;
   __syncthreads();
@@ -1121,26 +1121,17 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
   }
 }
 
-template <int TT, int EPB>
-cudaError_t launch_router_as(const FewRoute& r, int blocks, cudaStream_t st) {
+template <int TT>
+cudaError_t launch_few_router(FewRoute& r, int hq_blocks, cudaStream_t st) {
+  r.router_blocks = (r.E + EPB - 1) / EPB;
   const int part = kRouterWarps * EPB * TT * 4;
   const int keys = select_words(r.T, r.E) * 4;
   static std::atomic<uint64_t> smem_set{0};
-  const cudaError_t e = set_smem_once(few_router_kernel<TT, EPB>,
+  const cudaError_t e = set_smem_once(few_router_kernel<TT>,
                                       std::max(part, select_words(kFewMaxT, 1024) * 4), smem_set);
   if (e != cudaSuccess) return e;
-  return launch_pdl(few_router_kernel<TT, EPB>, dim3(blocks), dim3(kRouterThreads),
+  return launch_pdl(few_router_kernel<TT>, dim3(r.router_blocks + hq_blocks), dim3(kRouterThreads),
                     (size_t)std::max(part, keys), st, r);
-}
-
-// Experts per router block: one while that gives at most a block per SM (the
-// fewer, the shorter each block's chain of loads), else two.
-template <int TT>
-cudaError_t launch_few_router(FewRoute& r, int hq_blocks, cudaStream_t st) {
-  const int epb = r.E <= kSplitTargetBlocks ? 1 : 2;
-  r.router_blocks = (r.E + epb - 1) / epb;
-  const int blocks = r.router_blocks + hq_blocks;
-  return epb == 1 ? launch_router_as<TT, 1>(r, blocks, st) : launch_router_as<TT, 2>(r, blocks, st);
 }
 
 }  // namespace
@@ -1155,17 +1146,21 @@ FewPlan few_plan(const moe_dims_t& d, bool fp8) {
   L.max_slots = d.S + most;
   const int Fs = d.S > 0 ? d.Fs : 0;
   // Features per gate/up tile: 64 fill the 128 weight rows of a product.  When
-  // that leaves fewer than two tiles per SM, 32 (and with bf16 weights 16)
-  // spread the weight stream over more SMs; the rows they leave unused cost
-  // tensor time that the stream does not need.  The shared experts' tiles run
-  // while the routing is still being made, so they are to keep every SM busy
-  // by themselves: about a tile per SM.
+  // that gives tiles to fewer than three quarters of the SMs, 32 (and with bf16
+  // weights 16) spread the weight stream over more of them; the rows they leave
+  // unused cost tensor time, which is why tiles are not cut any further.  (One
+  // chosen expert of 2048 x 6144: 36 us with 16 features a tile, 55 with 64; 14
+  // tokens, 55 experts of 192 x 104, up to 126 tiles of 64: 21 us as they are,
+  // 25 in narrower ones.)  The shared experts' tiles run while the routing is
+  // still being made and are to keep every SM busy by themselves, unless they
+  // are small (one token, 1.6 MB tiles: 114 us cut into quarters, 116 whole).
   const int least = fp8 ? 32 : 16;
   auto tiles = [](int experts, int F, int fpt) { return (long long)experts * ((F + fpt - 1) / fpt); };
   L.fpt_s = L.fpt_r = 64;
-  while (L.fpt_s > least && tiles(d.S, Fs, L.fpt_s) < kSplitTargetBlocks * 3 / 4) L.fpt_s /= 2;
-  while (L.fpt_r > least && tiles(d.S, Fs, L.fpt_s) + tiles(most, d.F, L.fpt_r) < 2 * kSplitTargetBlocks)
-    L.fpt_r /= 2;
+  const int few = kSplitTargetBlocks * 3 / 4;
+  auto bytes = [&](int fpt) { return (long long)fpt * 2 * d.D * (fp8 ? 1 : 2); };
+  while (L.fpt_s > least && tiles(d.S, Fs, L.fpt_s) < few && bytes(L.fpt_s) > 400 << 10) L.fpt_s /= 2;
+  while (L.fpt_r > least && tiles(d.S, Fs, L.fpt_s) + tiles(most, d.F, L.fpt_r) < few) L.fpt_r /= 2;
   // K-blocks per stage: the stage stays 16 KB of weights, within the token stage
   auto sub = [&](int fpt) {
     int n = 64 / fpt;
@@ -1177,17 +1172,14 @@ FewPlan few_plan(const moe_dims_t& d, bool fp8) {
   L.nd = (d.D + 127) / 128;
   const int eb = fp8 ? 128 : 64;
   const int kb = std::min((d.F + eb - 1) / eb, d.S > 0 ? (Fs + eb - 1) / eb : 1 << 30);
-  // K parts of a down unit: until there are six units per SM, as long as a
-  // part has 16 K-blocks (8 made one token through the large layer 124 instead
-  // of 115 us: a shorter unit streams in less time than its epilogue takes);
-  // with fewer than two units per SM, down to four K-blocks
+  // K parts of a down unit, each with a plane to write and to add: only while
+  // all of them have an SM and at least eight K-blocks.  (One chosen expert, 48
+  // output blocks: 36 us in two parts, 39 in one, 43 in four; one token through
+  // nine experts, 432 units: 114 us in one, two or four parts.)
   L.parts = 1;
-  for (;;) {
-    const long long n = (long long)L.nd * L.parts * L.max_slots;
-    if (L.parts == 8 || n >= 6 * kSplitTargetBlocks) break;
-    if (kb < (n < 2 * kSplitTargetBlocks ? 8 : 32) * L.parts) break;
+  while (L.parts < 8 && (long long)L.nd * L.parts * L.max_slots * 2 <= kSplitTargetBlocks &&
+         kb >= 16 * L.parts)
     L.parts *= 2;
-  }
   return L;
 }
 

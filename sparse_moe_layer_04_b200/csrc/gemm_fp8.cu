@@ -646,9 +646,14 @@ cudaError_t launch_any(GemmParams8& p, bool gated, cudaStream_t st, const char**
   const long long blocks = std::min<long long>(a.R, (long long)a.R / NT + std::min(a.G, a.R));
   const long long tiles = blocks * p.nt;
   // Few tiles: split K over a cluster while that leaves every CTA an SM of its
-  // own and at least two K-blocks.
+  // own and two K-blocks, and takes at least nine K-blocks off each: joining
+  // the parts costs about 2 us.  (Graph times: 20 groups of 58 rows, N = 32, K =
+  // 4688 12.0 us split against 13.7; 13 groups of 6 rows, N = 8, K = 4192 gated
+  // 8.4 against 11.7; one row, N = 6144, K = 2048 8.3 against 7.5, which is why
+  // eight K-blocks are not enough.)
   p.split = 1;
-  while (p.split < 8 && tiles * p.split * 2 <= num_sms() && p.KB >= p.split * 4) p.split *= 2;
+  for (int s = 2; s <= 8; s *= 2)
+    if (tiles * s <= num_sms() && p.KB >= s * 2 && p.KB - p.KB / s >= 9) p.split = s;
   return gated ? launch_nt<NT, true>(p, tiles, st) : launch_nt<NT, false>(p, tiles, st);
 }
 
@@ -672,7 +677,10 @@ cudaError_t launch_gemm_fp8(const Gemm8Args& a, cudaStream_t st, const char** wh
   // the weights for the most rows; narrower tiles leave shared memory to the
   // weights' ring.  So: the narrowest that cuts a group into no more blocks
   // than 240 would, for groups two standard deviations above the average; and
-  // narrower still while that leaves SMs without a tile.
+  // narrower still while a quarter of the SMs have no tile.  (17 groups of 632
+  // rows, N = 40, K = 528 gated: 10.0 us narrowed against 13.3; 73 groups of
+  // 297, N = 24, K = 144, with a tile for 146 of 148 SMs: 12.7 narrowed against
+  // 9.6.)
   const int groups = std::min(a.G, a.R), avg = (a.R + groups - 1) / groups;
   const int top = a.G > 1 ? avg + (int)(2.f * sqrtf((float)avg)) : avg;
   const int nb = (top + 239) / 240, need = (top + nb - 1) / nb;
@@ -680,7 +688,7 @@ cudaError_t launch_gemm_fp8(const Gemm8Args& a, cudaStream_t st, const char** wh
   int w = 0;
   while (widths[w] < need) ++w;
   const long long cols = gated ? (a.N + 63) / 64 : (a.N + 127) / 128;
-  while (w > 0 && (long long)groups * ((avg + widths[w] - 1) / widths[w]) * cols < num_sms()) --w;
+  while (w > 0 && (long long)groups * ((avg + widths[w] - 1) / widths[w]) * cols < num_sms() * 3 / 4) --w;
   switch (widths[w]) {
     case 32: return launch_any<32>(p, gated, st, why, a);
     case 64: return launch_any<64>(p, gated, st, why, a);

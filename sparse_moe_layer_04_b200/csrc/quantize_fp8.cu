@@ -9,6 +9,12 @@
 // one rounding.  448 = 0.875 * 2^9: with max = 1.m * 2^p (bf16, 7 fraction
 // bits), e = p - 8, or p - 7 when the fraction is above that of 448 = 1.75 *
 // 2^8, which the integer sum below decides without branches.
+//
+// 32768 x 6144 rows gathered from 4096: 65 to 73 us, 600 MB through L2 (each
+// row is read eight times, 50 MB of HBM reads and 203 MB of writes).  Without
+// the loads it takes 43 us, without the arithmetic 57: what the SMs get out of
+// L2 bounds it.  Resident warps that walk rows with the next one on its way took
+// 68.
 #include <cuda_bf16.h>
 
 #include "moe_internal.cuh"
@@ -30,8 +36,6 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
 
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
-
-__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
 
 // 32 bytes in one load (16-byte aligned addresses that are not 32-byte aligned
 // take two).
@@ -83,7 +87,7 @@ __global__ void __launch_bounds__(kThreads) quantize_fp8_kernel(
     // the largest magnitude of the block, as bf16 bits (they order like the values)
     uint32_t t2 = 0;
 #pragma unroll
-    for (int q = 0; q < 8; ++q) t2 = max_u16x2(t2, w[i][q] & 0x7fff7fffu);
+    for (int q = 0; q < 8; ++q) t2 = __vmaxu2(t2, w[i][q] & 0x7fff7fffu);
     uint32_t top = max(t2 & 0xffffu, t2 >> 16);
 #pragma unroll
     for (int off = 4; off; off >>= 1) top = max(top, __shfl_xor_sync(kAll, top, off));
@@ -136,8 +140,9 @@ cudaError_t launch_quantize_fp8(const uint16_t* x, int src_rows, const int32_t* 
   // rows start on 32 bytes when the matrix does (K is a multiple of 16)
   const bool wide = (reinterpret_cast<uintptr_t>(x) & 31u) == 0;
   const int KB = (K + 127) / 128;
-  // A chunk per warp while that fits on the SMs at once (latency counts); else
-  // four, whose loads a warp has in flight together.
+  // A chunk per warp while that fits on the SMs at once (104 rows of 6144: 1.9
+  // us against 2.8); else four, whose loads a warp has in flight together
+  // (32768 rows: 70 us against 75; 17380 rows of 4544: 33 against 30).
   if ((long long)gx * chunks <= 4ll * num_sms())
     return launch_pdl(quantize_fp8_kernel<1>, dim3(gx, chunks), dim3(kThreads), 0, st, x, src_rows,
                       idx, R, K, KB, wide, codes, exps, status);
