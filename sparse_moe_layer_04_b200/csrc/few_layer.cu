@@ -416,7 +416,8 @@ struct FewShared {
   Unit q[kQueue];
   uint32_t tmem_base;
   int abort, bad, last, exit_last;
-  float act[64 * 17];    // FP8: activations of a tile [feature][token]
+  int act_count;         // epilogue warps that have stored their part of a gate/up tile
+  float act[2][64 * 17]; // FP8: activations of a tile [feature][token], by turns
   int tab_slot[kFewMaxT * 32];   // the tokens' choices: slot and weight
   float tab_w[kFewMaxT * 32];
 };
@@ -591,12 +592,13 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
     }
     for (int i = 0; i < kQueue; ++i) {
       ptx::mbar_init(&ss.q_full[i], 1);
-      ptx::mbar_init(&ss.q_empty[i], 1 + 1 + 4 + (FP8 ? 4 : 0));
+      ptx::mbar_init(&ss.q_empty[i], 1 + 1 + 1 + 4 + (FP8 ? 4 : 0));
     }
     ptx::mbar_init(&ss.drain, 1);
     ptx::mbar_init(&ss.epi, 4);
     ss.abort = 0;
     ss.bad = 0;
+    ss.act_count = 0;
     ptx::fence_barrier_init();
   }
   ptx::tc_fence_before();
@@ -833,6 +835,36 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
       ptx::mma_commit(&ss.drain);
       ffn::wait_drain(&ss.drain, 0, abort);
     }
+  } else if (warp == 3) {
+    // ---------------- hand-over of activations ----------------
+    // Counts a slot's finished tiles for the whole GPU, so that the epilogue
+    // does not wait for its stores to get there.
+    QueueReader q;
+    Unit u;
+    int want = 0;
+    while (q.next(ss, u, abort, lane)) {
+      if (u.down) continue;
+      want += 4;
+      const long long t0 = clock64();
+      bool ok = true;
+      while (*reinterpret_cast<volatile int*>(&ss.act_count) < want) {
+        __nanosleep(20);
+        if (*abort) { ok = false; break; }
+        if (clock64() - t0 > ptx::kWaitBudgetCycles) {
+          *abort = 1;
+          ok = false;
+          break;
+        }
+      }
+      if (__any_sync(kAll, !ok)) break;
+      if (lane == 0) {
+        // what the four warps stored before they were counted is ordered before
+        // this, for TMA too
+        __threadfence();
+        ptx::fence_proxy_async_global();
+        atomicAdd(slot_count(p, u.slot), 4);
+      }
+    }
   } else if (warp >= 4 && warp < 8) {
     // ---------------- epilogue ----------------
     const int qt = warp & 3;
@@ -841,7 +873,7 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
     Unit u;
     ptx::WarpBarrier epi{&ss.epi};
     bool waited = false;
-    int buf = 0;
+    int buf = 0, turn = 0;
     uint32_t cph = 0;
     // The ticket of a down unit is looked at with the next one, so that its round
     // trip passes under that one's products: lane 0 of the first warp holds
@@ -933,10 +965,11 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
         for (int t = 0; t < 16; t += 2) {
           const float got = __shfl_xor_sync(kAll, up ? v[t] : v[t + 1], 16);
           const float gate = up ? got : v[t], mul = up ? v[t + 1] : got;
-          const float a = f < F ? gate / (1.0f + expf(-gate)) * mul : 0.f;
+          // (the division is good to 2 units)
+          const float a = f < F ? __fdividef(gate, 1.0f + expf(-gate)) * mul : 0.f;
           const int tt = t + (up ? 1 : 0);
           if (FP8) {
-            ss.act[(qt * 16 + (lane & 15)) * 17 + tt] = a;
+            ss.act[turn][(qt * 16 + (lane & 15)) * 17 + tt] = a;
           } else if (rows && f < F && ((mask >> tt) & 1u)) {
             __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(sh ? p.a_s : p.a_r) +
                                  (row0 + tt) * F + f;
@@ -958,7 +991,7 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
           for (int i = qt; i < p.T * (fpt / 32); i += 4) {
             const int t = i % p.T, b = i / p.T;
             if (!((mask >> t) & 1u)) continue;
-            float a = ss.act[(b * 32 + lane) * 17 + t];
+            float a = ss.act[turn][(b * 32 + lane) * 17 + t];
             const bool odd = !isfinite(a);
             if (odd) a = 0.f;
             const float top = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(fabsf(a))));
@@ -974,14 +1007,16 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
               if (fb + lane < F) dst[(size_t)c * p.T * F] = (uint8_t)(odd ? 0x7fu : code);
             }
           }
-          // the tile's activations are read: the next may be written
-          if (!epi.sync(abort, lane)) break;
+          // the next tile writes the other half; a warp that comes back to this
+          // one has met all four at that tile's barrier
+          turn ^= 1;
         }
-        // the stores become visible to the whole GPU and to TMA, then the count
-        ptx::fence_proxy_async_global();
-        __threadfence();
+        // this warp's part is stored, as far as this CTA can see
         __syncwarp();
-        if (lane == 0) atomicAdd(slot_count(p, u.slot), 1);
+        if (lane == 0) {
+          __threadfence_block();
+          atomicAdd(&ss.act_count, 1);
+        }
       } else {
         const int d = u.at * 128 + qt * 32 + lane;
         float* plane = p.planes + (size_t)(u.slot * p.parts + u.part) * p.T * p.D + d;
