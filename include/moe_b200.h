@@ -278,9 +278,9 @@ int moe_forward_fp8(const void* h, const float* Wr, const float* bias, const moe
  * nothing) in two kernels on `stream`: routing, then both expert products and
  * the merge in one persistent kernel that reads each chosen expert's weights
  * once.  The same layer, arguments, limits, workspace and errors as
- * moe_forward; two differences in precision: the logits' sums run in another
- * (fixed) order, and the gated activation enters the w2 product with its 24
- * significant bits instead of 8.  Capturable in a CUDA graph; no internal
+ * moe_forward; differences in precision: the logits' sums and the merge's run
+ * in other (fixed) orders, and the gated activation enters the w2 product
+ * with its 24 significant bits instead of 8.  Capturable in a CUDA graph; no internal
  * stream.  moe_ws_expert_counts and moe_ws_touched_experts hold for it too.
  * Repeated calls give identical bits.  Calls that share a workspace must not
  * overlap on the GPU; one workspace sized for the largest T may serve calls of
@@ -292,8 +292,8 @@ int moe_forward_few(const void* h, const float* Wr, const float* bias, const voi
 
 /* moe_forward_few with FP8 expert weights (rules as moe_forward_fp8).  The
  * codes enter the tensor core as they are; hidden rows and activations enter
- * as sums of three and four E4M3 pieces, which hold a hidden value to within
- * 2^-25 of the largest of its 128 neighbours (exactly, when it is not much
+ * as sums of two and four E4M3 pieces, which hold a hidden value to within
+ * 2^-21 of the largest of its 128 neighbours (exactly, when it is not much
  * smaller than that), and an activation to within 2^-16 of itself plus 2^-29
  * of the largest of its 32 neighbours.  A non-finite activation gives NaN.
  * An exponent outside [-117, 7] raises MOE_ERR_BOUNDS. */

@@ -191,7 +191,7 @@ bool ws_layout(const moe_dims_t& d, WsLayout* L) {
   L->y = take((T * k + S * T) * D * 4);
   L->touched = take(4);
   L->gmask = take(T <= kPermBlockTokens ? E * (kPermBlockTokens / 32) * 4 : 0);
-  L->f_route = L->f_slots = L->f_mask = L->f_hq = L->f_hqe = L->f_act = L->f_exp = L->f_planes = 0;
+  L->f_route = L->f_slots = L->f_w = L->f_mask = L->f_hq = L->f_hqe = L->f_act = L->f_exp = L->f_planes = 0;
   if (T > 0 && T <= (size_t)kFewMaxT) {
     const FewPlan p16 = few_plan(d, false), p8 = few_plan(d, true);
     const size_t slots = p16.max_slots, most = slots - S;
@@ -205,6 +205,7 @@ bool ws_layout(const moe_dims_t& d, WsLayout* L) {
     const size_t planes = std::max(slots, (size_t)kSplitTargetBlocks / p16.nd);
     L->f_route = take(2 * T * E * 4);
     L->f_slots = take((64 + T * k + slots) * 4);
+    L->f_w = take(slots * kFewMaxT * 4);
     L->f_mask = take(slots * 4);
     L->f_hq = take(3 * T * D);
     L->f_hqe = take(T * ((D + 127) / 128));
@@ -560,6 +561,7 @@ int forward_few_impl(const void* h, const float* Wr, const float* bias, const Ex
   a.slot_of = slots + 64;
   a.slot_expert = a.slot_of + dims->T * dims->k;
   a.slot_mask = w.at<uint32_t>(w.L.f_mask);
+  a.slot_w = w.at<float>(w.L.f_w);
   a.counts = w.at<int32_t>(w.L.counts);
   a.touched = w.at<int32_t>(w.L.touched);
   a.ticket = w.at<int32_t>(w.L.f_claim);

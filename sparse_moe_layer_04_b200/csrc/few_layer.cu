@@ -9,13 +9,15 @@
 //                       last the selection, the weights and the list of
 //                       "slots": the shared experts, then the chosen experts
 //                       in increasing order.  FP8: the hidden rows are also
-//                       split into three E4M3 pieces here.
+//                       split into two E4M3 pieces here.
 //   few_ffn_kernel      tiles claimed in order from a counter:
 //     gate/up  (slot, up to 64 features): act = silu(W1 h) * (W3 h) for every
 //              token, kept for the tokens that chose the expert
-//     down     (slot, 128 output rows, part of K): y = W2 act, written to a
-//              plane of its own; whoever completes the last plane of 128
-//              output rows adds the planes in the order of moe_combine
+//     down     (slots, 128 output rows, part of K): y = W2 act of one slot, or
+//              of a few when the experts are narrow, weighted and added, written
+//              to a plane of its own; whoever completes the last plane of 128
+//              output rows adds the planes, shared experts first, then in the
+//              order of the token's choices
 // The shared experts' gate/up tiles need no routing, so this kernel starts on
 // them while the first one runs (programmatic dependent launch).
 //
@@ -31,9 +33,9 @@
 // the codes enter as they are, with their block exponents as the tensor
 // core's scales, and the other operand is a sum of E4M3 pieces, each holding 4
 // bits of what the ones before it leave, with a scale 2^4 lower.  A bf16 value
-// has 8 bits, so two pieces hold it and a third reaches values far below their
-// block's largest (E4M3's subnormal step is 2^-17.8 of it: three pieces leave
-// 2^-25.8); four hold an activation to 2^-16 of itself.  The pieces cost
+// has 8 bits, so two pieces hold it, down to the second one's subnormal step:
+// 2^-13 of the block's scale, which leaves at most 2^-21.8 of the block's
+// largest value; four hold an activation to 2^-16 of itself.  The pieces cost
 // columns, not weight bytes.
 //
 // The tensor core's bf16 form cuts off its running sum at each step of 16,
@@ -56,7 +58,7 @@ constexpr unsigned kAll = 0xffffffffu;
 constexpr int kRouterThreads = 512;
 constexpr int kRouterWarps = kRouterThreads / 32;
 constexpr int EPB = 2;                   // experts per router block
-constexpr int kPiecesH = 3, kPiecesA = 4;   // E4M3 pieces of a hidden value, an activation
+constexpr int kPiecesH = 2, kPiecesA = 4;   // E4M3 pieces of a hidden value, an activation
 constexpr int kPiecesB = 3;                 // bf16 pieces of an activation
 constexpr int kPieceMinExp = -115;       // the last piece's exponent stays an E8M0 value
 
@@ -73,6 +75,7 @@ struct FewRoute {
   int32_t* idx;           // [T, k]
   float* w;               // [T, k]
   int32_t* slot_of;       // [T, k] chosen-expert slot of each pair, -1 for none
+  float* slot_w;          // [slots][kFewMaxT] weight of a slot for each token that chose it
   int32_t* slot_expert;   // [slots]
   uint32_t* slot_mask;    // [slots] bit t: token t chose it
   int32_t* nslots;        // chosen experts
@@ -226,6 +229,7 @@ __device__ void select_and_list(const FewRoute& p, uint32_t* smem) {
   __syncthreads();
   const int t = warp;
   int my_e = INT_MAX;
+  float my_w = 0.f;
   if (t < p.T) {
     uint32_t* ord = s_ord + t * p.E;
     for (int j = 0; j < p.k; ++j) {
@@ -247,7 +251,8 @@ __device__ void select_and_list(const FewRoute& p, uint32_t* smem) {
     for (int j = 1; j < p.k; ++j) sum = __fadd_rn(sum, __shfl_sync(kAll, my_s, j));
     if (lane < p.k) {
       p.idx[t * p.k + lane] = my_e;
-      p.w[t * p.k + lane] = __fmul_rn(__fdiv_rn(my_s, sum), p.scale);
+      my_w = __fmul_rn(__fdiv_rn(my_s, sum), p.scale);
+      p.w[t * p.k + lane] = my_w;
       if (my_e != INT_MAX) atomicOr(&s_mask[my_e], 1u << t);
     }
   }
@@ -273,10 +278,14 @@ __device__ void select_and_list(const FewRoute& p, uint32_t* smem) {
     if (g == groups - 1 && lane == 31) *p.nslots = slot + (m != 0u);
   }
   __syncthreads();
-  if (t < p.T && lane < p.k) p.slot_of[t * p.k + lane] = my_e != INT_MAX ? s_slot[my_e] : -1;
+  if (t < p.T && lane < p.k) {
+    const int slot = my_e != INT_MAX ? s_slot[my_e] : -1;
+    p.slot_of[t * p.k + lane] = slot;
+    if (slot >= 0) p.slot_w[slot * kFewMaxT + t] = my_w;
+  }
 }
 
-// One warp: the three pieces of 128 columns of a hidden row.
+// One warp: the pieces of 128 columns of a hidden row.
 __device__ __forceinline__ void split_hidden(const FewRoute& p, int unit, int lane) {
   const int KB = (p.D + 127) / 128;
   const int t = unit / KB, kb = unit - t * KB;
@@ -379,15 +388,17 @@ struct alignas(64) FewFfn {
   int nd;                // blocks of 128 output rows
   int ntr, nts;          // gate/up tiles per chosen / shared slot
   int max_slots;         // S + the most experts the call can choose
+  int spu_r, spu_s;      // slots of a down unit: chosen, shared
+  int ngs;               // shared groups of slots (units per output block and part)
   // routing (written by the first kernel)
-  const int32_t *idx, *slot_of, *slot_expert, *nslots;
+  const int32_t *slot_of, *slot_expert, *nslots;
   const uint32_t* slot_mask;
-  const float* w;
+  const float* slot_w;
   const int8_t* hqe;     // FP8: exponents of the hidden rows [T, KB]
   // activations, their exponents (FP8: one per 32 features, [slots, T, 4 * KB])
   uint8_t *a_r, *a_s;
   int8_t *ae_r, *ae_s;
-  float* planes;         // [slot * parts + part][T][D]
+  float* planes;         // [group * parts + part][T][D]
   float* out;
   int32_t* claim;        // claim counter, exit ticket, blocks of pieces written, then
                          // per-slot counts, then per-output-block tickets; zero
@@ -404,6 +415,9 @@ struct Unit {
   int part;
   int expert;            // row of the weight arrays
   uint32_t mask;         // tokens that chose it
+  // down units of several slots come one slot at a time: 1 the first, 2 the last
+  int ends;
+  int plane;
 };
 
 struct FewShared {
@@ -418,8 +432,8 @@ struct FewShared {
   int abort, bad, last, exit_last;
   int act_count;         // epilogue warps that have stored their part of a gate/up tile
   float act[2][64 * 17]; // FP8: activations of a tile [feature][token], by turns
-  int tab_slot[kFewMaxT * 32];   // the tokens' choices: slot and weight
-  float tab_w[kFewMaxT * 32];
+  int tab[kFewMaxT * 32];        // the tokens' choices: their group of slots, -1 where an
+                                 // earlier choice has it too (or there is none)
 };
 
 constexpr int few_smem() { return 1024 + kRing + (int)sizeof(FewShared); }
@@ -431,7 +445,7 @@ struct QueueReader {
   __device__ __forceinline__ bool next(FewShared& ss, Unit& u, volatile int* abort, int lane) {
     if (__any_sync(kAll, !ptx::mbar_wait(&ss.q_full[slot], phase, abort))) return false;
     const volatile Unit& q = ss.q[slot];
-    u.down = q.down; u.slot = q.slot; u.at = q.at; u.part = q.part; u.expert = q.expert; u.mask = q.mask;
+    u.down = q.down; u.slot = q.slot; u.at = q.at; u.part = q.part; u.expert = q.expert; u.mask = q.mask; u.ends = q.ends; u.plane = q.plane;
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive_after_reads(&ss.q_empty[slot]);
     if (++slot == kQueue) { slot = 0; phase ^= 1u; }
@@ -507,56 +521,47 @@ struct RawScales {
   }
 };
 
-// out for 128 columns, from the planes of every slot: shared experts, then the
-// token's choices in their order (moe_combine's).  Four groups of 32 threads
-// take every fourth token, a thread four columns; kMergeLoads loads are in
-// flight before the first is added.
+// out for 128 columns, from the planes: shared groups, then the groups of the
+// token's choices in their order.  Four groups of 32 threads take every fourth
+// token, a thread four columns; kMergeLoads loads are in flight before the
+// first is added.
 constexpr int kMergeLoads = 8;
 __device__ __forceinline__ void merge_block(const FewFfn& p, const FewShared& ss, int at, int tid) {
   const int d = at * 128 + (tid & 31) * 4;
   if (d >= p.D) return;
   const size_t plane = (size_t)p.T * p.D;
-  // this thread's terms: its tokens one after the other, each token's slots,
-  // each slot's K parts
-  const int n = (p.S + p.k) * p.parts;
+  // this thread's terms: its tokens one after the other, each token's groups,
+  // each group's K parts
+  const int n = (p.ngs + p.k) * p.parts;
   const int total = (p.T - (tid >> 5) + 3) / 4 * n;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f), y = o;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   int lt = tid >> 5, lj = 0, lpart = 0;  // the term being loaded
-  int t = lt, j = 0, part = 0;           // the term being added
+  int t = lt, done = 0;                  // the token being added, its terms so far
   for (int i0 = 0; i0 < total; i0 += kMergeLoads) {
     float4 r[kMergeLoads];
 #pragma unroll
     for (int i = 0; i < kMergeLoads; ++i) {
       r[i] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (i0 + i < total) {
-        const int s = lj < p.S ? lj : p.S + ss.tab_slot[lt * p.k + lj - p.S];
-        if (s >= (lj < p.S ? 0 : p.S))
+        const int g = lj < p.ngs ? lj : ss.tab[lt * p.k + lj - p.ngs];
+        if (g >= 0)
           r[i] = __ldcg(reinterpret_cast<const float4*>(
-              p.planes + ((size_t)s * p.parts + lpart) * plane + (size_t)lt * p.D + d));
+              p.planes + ((size_t)g * p.parts + lpart) * plane + (size_t)lt * p.D + d));
         if (++lpart == p.parts) {
           lpart = 0;
-          if (++lj == p.S + p.k) { lj = 0; lt += 4; }
+          if (++lj == p.ngs + p.k) { lj = 0; lt += 4; }
         }
       }
     }
 #pragma unroll
     for (int i = 0; i < kMergeLoads; ++i) {
       if (i0 + i < total) {
-        y.x += r[i].x; y.y += r[i].y; y.z += r[i].z; y.w += r[i].w;
-        if (++part == p.parts) {
-          part = 0;
-          // an empty choice (NaN keys) adds nothing
-          const int at_j = t * p.k + j - p.S;
-          const float c = j < p.S ? 1.f : ss.tab_slot[at_j] < 0 ? 0.f : ss.tab_w[at_j];
-          o.x = fmaf(c, y.x, o.x); o.y = fmaf(c, y.y, o.y);
-          o.z = fmaf(c, y.z, o.z); o.w = fmaf(c, y.w, o.w);
-          y = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (++j == p.S + p.k) {
-            *reinterpret_cast<float4*>(p.out + (size_t)t * p.D + d) = o;
-            o = y;
-            j = 0;
-            t += 4;
-          }
+        o.x += r[i].x; o.y += r[i].y; o.z += r[i].z; o.w += r[i].w;
+        if (++done == n) {
+          *reinterpret_cast<float4*>(p.out + (size_t)t * p.D + d) = o;
+          o = make_float4(0.f, 0.f, 0.f, 0.f);
+          done = 0;
+          t += 4;
         }
       }
     }
@@ -616,7 +621,8 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
       uint32_t phase = 0, qphase = 0, issued = 0, parity = 0;
       int tile = atomicAdd(p.claim, 1);
       for (;;) {
-        Unit u{0, 0, 0, 0, 0, (1u << p.T) - 1u};
+        Unit u{0, 0, 0, 0, 0, (1u << p.T) - 1u, 3, 0};
+        int slots = 1;                   // of a down unit
         if (tile < shared_tiles) {
           u.slot = tile / p.nts;
           u.at = (tile - u.slot * p.nts) * p.fpt_s;
@@ -636,16 +642,26 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
             u.at = (r - s * p.ntr) * p.fpt_r;
           } else {
             r -= routed * p.ntr;
-            const int per = p.nd * p.parts;
-            u.slot = r / per;
-            u.down = u.slot < p.S + routed ? 1 : -1;
-            r -= u.slot * per;
+            const int per = p.nd * p.parts, g = r / per;
+            const int groups = p.ngs + (routed + p.spu_r - 1) / p.spu_r;
+            r -= g * per;
+            u.down = g < groups ? 1 : -1;
             u.part = r / p.nd;
             u.at = r - u.part * p.nd;
-            if (u.down >= 0 && u.slot >= p.S) {
-              expert = __ldcg(p.slot_expert + u.slot - p.S);
-              mask = __ldcg(p.slot_mask + u.slot - p.S);
+            u.plane = g * p.parts + u.part;
+            if (g < p.ngs) {
+              u.slot = g * p.spu_s;
+              slots = min(p.spu_s, p.S - u.slot);
+            } else {
+              const int first = (g - p.ngs) * p.spu_r;
+              u.slot = p.S + first;
+              slots = min(p.spu_r, routed - first);
+              if (u.down >= 0) {
+                expert = __ldcg(p.slot_expert + first);
+                mask = __ldcg(p.slot_mask + first);
+              }
             }
+            u.ends = slots > 1 ? 1 : 3;
           }
           if (u.slot >= p.S) {
             u.expert = expert;
@@ -666,14 +682,34 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
         bool ok = true;
         if (u.down) {
           const CUtensorMap* m = sh ? &p.w2_s : &p.w2_r;
-          const int row = u.expert * p.D + u.at * 128;
-          for (int kb = k0; kb < k1; ++kb) {
-            if (!ptx::mbar_wait(&ss.empty[stage], phase ^ 1u, abort)) { ok = false; break; }
-            ptx::mbar_arrive_expect_tx(&ss.full[stage], kAStage);
-            ptx::tma_load_2d_hint(ring_a + stage * kAStage, m, &ss.full[stage], kb * EB, row, policy);
-            issued |= 1u << stage;
-            parity = (parity & ~(1u << stage)) | (phase << stage);
-            if (++stage == kAStages) { stage = 0; phase ^= 1u; }
+          for (;;) {
+            // the unit's next slot, if it has one
+            Unit v = u;
+            if (--slots > 0) {
+              ++v.slot;
+              v.ends = slots > 1 ? 0 : 2;
+              if (sh) {
+                v.expert = v.slot;
+              } else {
+                v.expert = __ldcg(p.slot_expert + v.slot - p.S);
+                v.mask = __ldcg(p.slot_mask + v.slot - p.S);
+              }
+            }
+            const int row = u.expert * p.D + u.at * 128;
+            for (int kb = k0; kb < k1; ++kb) {
+              if (!ptx::mbar_wait(&ss.empty[stage], phase ^ 1u, abort)) { ok = false; break; }
+              ptx::mbar_arrive_expect_tx(&ss.full[stage], kAStage);
+              ptx::tma_load_2d_hint(ring_a + stage * kAStage, m, &ss.full[stage], kb * EB, row, policy);
+              issued |= 1u << stage;
+              parity = (parity & ~(1u << stage)) | (phase << stage);
+              if (++stage == kAStages) { stage = 0; phase ^= 1u; }
+            }
+            if (!ok || slots <= 0) break;
+            u = v;
+            if (!ptx::mbar_wait(&ss.q_empty[qs], qphase ^ 1u, abort)) { ok = false; break; }
+            ss.q[qs] = u;
+            ptx::mbar_arrive(&ss.q_full[qs]);
+            if (++qs == kQueue) { qs = 0; qphase ^= 1u; }
           }
         } else {
           const CUtensorMap* m1 = sh ? &p.w1_s : &p.w1_r;
@@ -874,7 +910,10 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
     ptx::WarpBarrier epi{&ss.epi};
     bool waited = false;
     int buf = 0, turn = 0;
-    uint32_t cph = 0;
+    uint32_t cph = 0, omask = 0;
+    float o[16];                         // a down unit's sum over its slots, per token
+#pragma unroll
+    for (int t = 0; t < 16; ++t) o[t] = 0.f;
     // The ticket of a down unit is looked at with the next one, so that its round
     // trip passes under that one's products: lane 0 of the first warp holds
     // its number, and `last_at` is the output block it stands for (-1: none).
@@ -904,13 +943,23 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
       if (!waited && (u.down || !sh)) {
         ptx::pdl_wait();
         waited = true;
-        planes = (p.S + __ldcg(p.nslots)) * p.parts;
+        planes = (p.ngs + (__ldcg(p.nslots) + p.spu_r - 1) / p.spu_r) * p.parts;
+        // (read after a barrier of all four warps, in settle)
         for (int i = threadIdx.x - 128; i < p.T * p.k; i += 128) {
-          ss.tab_slot[i] = __ldcg(p.slot_of + i);
-          ss.tab_w[i] = __ldcg(p.w + i);
+          const int s = __ldcg(p.slot_of + i), g = s / p.spu_r, first = i / p.k * p.k;
+          bool have = s >= 0;
+          if (p.spu_r > 1)
+            for (int j = first; j < i; ++j) {
+              const int o = __ldcg(p.slot_of + j);
+              if (o >= 0 && o / p.spu_r == g) have = false;
+            }
+          ss.tab[i] = have ? p.ngs + g : -1;
         }
       }
       const uint32_t mask = u.mask;
+      // a down unit's weights: lane t has token t's
+      float wl = 1.f;
+      if (u.down && !sh && lane < kFewMaxT) wl = __ldcg(p.slot_w + (u.slot - p.S) * kFewMaxT + lane);
       int k0, k1;
       unit_k<EB>(p, u, &k0, &k1);
       // the token columns, pieces and accumulators added: v[t] is this lane's
@@ -1019,11 +1068,24 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
         }
       } else {
         const int d = u.at * 128 + qt * 32 + lane;
-        float* plane = p.planes + (size_t)(u.slot * p.parts + u.part) * p.T * p.D + d;
+        if (u.ends & 1) {
+#pragma unroll
+          for (int t = 0; t < 16; ++t) o[t] = 0.f;
+          omask = 0;
+        }
+        omask |= mask;
+#pragma unroll
+        for (int t = 0; t < 16; ++t) {
+          const float c = __shfl_sync(kAll, wl, t);
+          // (what the slot made of other tokens is left out, whatever it is)
+          if ((mask >> t) & 1u) o[t] = fmaf(c, v[t], o[t]);
+        }
+        if (!(u.ends & 2)) continue;
+        float* plane = p.planes + (size_t)u.plane * p.T * p.D + d;
         if (d < p.D) {
 #pragma unroll
           for (int t = 0; t < 16; ++t)
-            if ((mask >> t) & 1u) plane[(size_t)t * p.D] = v[t];
+            if ((omask >> t) & 1u) plane[(size_t)t * p.D] = o[t];
         }
         if (!settle(u.at)) break;
       }
@@ -1215,6 +1277,18 @@ FewPlan few_plan(const moe_dims_t& d, bool fp8) {
   while (L.parts < 8 && (long long)L.nd * L.parts * L.max_slots * 2 <= kSplitTargetBlocks &&
          kb >= 16 * L.parts)
     L.parts *= 2;
+  // Slots of a down unit: narrow experts are taken together until a unit has 16
+  // K-blocks, as long as there are two units per SM (a unit's plane and ticket
+  // cost its epilogue 1 us).
+  auto together = [&](int slots, int kbs) {
+    int n = 1;
+    while (L.parts == 1 && n * kbs < 16 &&
+           (long long)L.nd * ((slots + 2 * n - 1) / (2 * n)) >= 2 * kSplitTargetBlocks)
+      n *= 2;
+    return n;
+  };
+  L.spu_r = together(most, (d.F + eb - 1) / eb);
+  L.spu_s = together(d.S, (Fs + eb - 1) / eb);
   return L;
 }
 
@@ -1230,7 +1304,7 @@ cudaError_t launch_few(const FewArgs& a, cudaStream_t st, const char** why) {
   r.scores = a.scores;
   r.order = a.order;
   r.idx = a.idx; r.w = a.w;
-  r.slot_of = a.slot_of; r.slot_expert = a.slot_expert; r.slot_mask = a.slot_mask;
+  r.slot_of = a.slot_of; r.slot_w = a.slot_w; r.slot_expert = a.slot_expert; r.slot_mask = a.slot_mask;
   r.nslots = a.nslots; r.counts = a.counts;
   r.ticket = a.ticket;
   r.status = a.status;
@@ -1275,9 +1349,11 @@ cudaError_t launch_few(const FewArgs& a, cudaStream_t st, const char** why) {
   f.ntr = (d.F + L.fpt_r - 1) / L.fpt_r;
   f.nts = (Fs + L.fpt_s - 1) / L.fpt_s;
   f.max_slots = L.max_slots;
-  f.idx = a.idx; f.slot_of = a.slot_of; f.slot_expert = a.slot_expert; f.nslots = a.nslots;
+  f.spu_r = L.spu_r; f.spu_s = L.spu_s;
+  f.ngs = (d.S + L.spu_s - 1) / L.spu_s;
+  f.slot_of = a.slot_of; f.slot_expert = a.slot_expert; f.nslots = a.nslots;
   f.slot_mask = a.slot_mask;
-  f.w = a.w;
+  f.slot_w = a.slot_w;
   f.hqe = a.hqe;
   f.a_r = a.a_r; f.a_s = a.a_s; f.ae_r = a.ae_r; f.ae_s = a.ae_s;
   f.planes = a.planes;

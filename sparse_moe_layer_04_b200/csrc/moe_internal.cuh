@@ -61,7 +61,7 @@ struct WsLayout {
       counters_s, xperm,
       act_r, act_s, y, touched, gmask, total;
   // the few-token layer: its counters, and for T <= kFewMaxT its scratch
-  size_t f_claim, f_route, f_slots, f_mask, f_hq, f_hqe, f_act, f_exp, f_planes;
+  size_t f_claim, f_route, f_slots, f_w, f_mask, f_hq, f_hqe, f_act, f_exp, f_planes;
 };
 bool ws_layout(const moe_dims_t& d, WsLayout* out);
 
@@ -239,6 +239,7 @@ struct FewPlan {
   // of a shared expert
   int fpt_r, fpt_s, sub_r, sub_s;
   int nd, parts;   // output blocks of 128 rows; K parts of a down unit
+  int spu_r, spu_s;  // slots of a down unit: chosen, shared experts
 };
 FewPlan few_plan(const moe_dims_t& d, bool fp8);
 struct FewArgs {
@@ -255,6 +256,7 @@ struct FewArgs {
   uint32_t* order;         // [T, E]
   int32_t *slot_of, *slot_expert, *nslots, *counts, *touched, *ticket, *claim;
   uint32_t* slot_mask;
+  float* slot_w;           // [slots, kFewMaxT]
   uint8_t *hq, *a_r, *a_s;
   int8_t *hqe, *ae_r, *ae_s;
   float* planes;

@@ -8,7 +8,9 @@ element by element: each step of the tensor core (16 or 32 products and the
 running sum) is off by at most 2^-22 of the sum of magnitudes; an activation
 enters the second product within 2^-16 of itself (two bf16 pieces: 2^-18, four
 E4M3 pieces: 2^-16) plus, for E4M3, 2^-29 of its largest neighbour; a hidden
-value enters exactly (bf16) or within 2^-25 of its largest neighbour (E4M3);
+value enters exactly (bf16) or within 2^-21 of its largest neighbour (E4M3: two
+pieces end at half of 2^-13 of the block's scale, whose largest value is above
+224 of it);
 |silu'| <= 1.1; the merge adds at most T k + S terms in fp32.
 """
 import numpy as np
@@ -81,7 +83,7 @@ class Layer:
         D, F = h.shape[1], w1.shape[0]
         x = h.double()
         step = (D / 16 + 2) * 2.0 ** -22
-        eh = 2.0 ** -25 * x.abs().amax(1, keepdim=True).expand_as(x) if self.fp8 else 0 * x
+        eh = 2.0 ** -21 * x.abs().amax(1, keepdim=True).expand_as(x) if self.fp8 else 0 * x
         gate, up = x @ w1.t(), x @ w3.t()
         eg = step * (x.abs() @ w1.abs().t()) + eh @ w1.abs().t()
         eu = step * (x.abs() @ w3.abs().t()) + eh @ w3.abs().t()
@@ -143,6 +145,9 @@ CASES = [  # T, D, E, F, k, S, Fs
     (16, 144, 5, 976, 1, 16, 32),       # sixteen of them
     (4, 6144, 16, 2048, 8, 1, 2048),    # full-size experts, K split over units
     (12, 4096, 12, 1408, 8, 1, 1408),
+    (10, 5040, 98, 128, 3, 0, 0),       # narrow experts: several to a unit of the second product
+    (7, 6144, 24, 64, 4, 16, 32),       # and shared ones
+    (16, 5008, 200, 80, 13, 1, 4096),   # several choices of a token in one unit
 ]
 
 
