@@ -21,6 +21,8 @@
  *  - Every pointer argument is a DEVICE pointer unless stated otherwise; the
  *    caller allocates and owns every buffer and the stream.  The library never
  *    allocates device memory: all scratch lives in the caller's workspace.
+ *  - Calls run on the current device, which must hold every buffer and the
+ *    stream.
  *  - Arrays are dense and row-major.  Device pointers must be 16-byte aligned.
  *  - bf16 means IEEE bfloat16 stored as uint16_t bit patterns.
  *  - Calls only enqueue work on `stream` and return at once; results are

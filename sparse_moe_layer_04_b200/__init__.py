@@ -310,10 +310,11 @@ def _arg(t: torch.Tensor, dtype, shape, dev: int, name: str) -> int:
     current one, which the kernels run on), or the error it deserves.  One test
     per property on the way that every call takes: checks are most of a small
     call's host time."""
-    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
-        return t.data_ptr()
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name}: expected a tensor, got {type(t).__name__}")
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        raise TypeError(f"{name}: expected a tensor, got {type(t).__name__}") from None
     if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.dtype is not dtype:
@@ -327,9 +328,10 @@ def _arg(t: torch.Tensor, dtype, shape, dev: int, name: str) -> int:
 
 def _codes(t: torch.Tensor, shape, dev: int, name: str) -> int:
     """_arg of E4M3 codes, as either of their types."""
-    if t.dtype in _CODE_DTYPES:
-        return _arg(t, t.dtype, shape, dev, name)
-    raise TypeError(f"{name}: expected uint8 or float8_e4m3fn codes, got {t.dtype}")
+    dtype = getattr(t, "dtype", None)
+    if dtype in _CODE_DTYPES:
+        return _arg(t, dtype, shape, dev, name)
+    raise TypeError(f"{name}: expected uint8 or float8_e4m3fn codes, got {dtype or type(t).__name__}")
 
 
 def _ws_arg(ws: Optional[torch.Tensor], dev: int):

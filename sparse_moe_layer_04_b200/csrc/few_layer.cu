@@ -977,25 +977,24 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
         ptx::tc_fence_after();
         const uint32_t acc = tmem + buf * acc_cols(FP8) + lanes;
         const int nacc = acc_count(FP8, n, min(kSegment, k1 - seg));
-        for (int c = rows ? pieces - 1 : -1; c >= 0; --c) {   // smallest piece first
-          float s[16];
+        // smallest piece first, a piece's accumulators one after the other, four
+        // reads in flight
+        const int reads = rows ? pieces * nacc : 0;
+        int c = pieces - 1, a = 0;
+        for (int i0 = 0; i0 < reads; i0 += 4) {
+          uint32_t r[4][16];
 #pragma unroll
-          for (int t = 0; t < 16; ++t) s[t] = 0.f;
-          for (int a0 = 0; a0 < nacc; a0 += 4) {       // four reads in flight
-            uint32_t r[4][16];
-#pragma unroll
-            for (int a = 0; a < 4; ++a)
-              ptx::tmem_ld_x16(acc + min(a0 + a, nacc - 1) * n + c * p.T, r[a]);
-            ptx::tmem_wait_ld();
-#pragma unroll
-            for (int a = 0; a < 4; ++a)
-              if (a0 + a < nacc) {
-#pragma unroll
-                for (int t = 0; t < 16; ++t) s[t] += __uint_as_float(r[a][t]);
-              }
+          for (int i = 0; i < 4; ++i) {
+            if (i0 + i < reads) ptx::tmem_ld_x16(acc + a * n + c * p.T, r[i]);
+            if (++a == nacc) { a = 0; --c; }
           }
+          ptx::tmem_wait_ld();
 #pragma unroll
-          for (int t = 0; t < 16; ++t) v[t] += s[t];
+          for (int i = 0; i < 4; ++i)
+            if (i0 + i < reads) {
+#pragma unroll
+              for (int t = 0; t < 16; ++t) v[t] += __uint_as_float(r[i][t]);
+            }
         }
         ptx::tc_fence_before();
         __syncwarp();

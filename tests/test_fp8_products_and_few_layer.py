@@ -142,7 +142,8 @@ def test_binding_refusals_quantize(on_cpu):
                              ((x, c, e, z(3, dtype=torch.int32)), ValueError, "codes"),
                              ((x, c, e, z(4, dtype=torch.int64)), TypeError, "idx"),
                              ((x, c, e, None, z(8)), TypeError, "ws"),
-                             ((x, c, None), AttributeError, "dtype")):
+                             ((x, c, None), TypeError, "exps: expected a tensor"),
+                             ((x, None, e), TypeError, "codes")):
         with pytest.raises(kind, match=text):
             f(*args)
 
@@ -184,6 +185,7 @@ def test_binding_refusals_few_layer(on_cpu):
                                (dict(out=out.to(bf)), TypeError, "out"),
                                (dict(idx_out=z(4, 3, dtype=torch.int32)), ValueError, "idx_out"),
                                (dict(w_out=z(4, 2, dtype=bf)), TypeError, "w_out"),
+                               (dict(W1=None), TypeError, "W1: expected a tensor"),
                                (dict(ws=z(16)), TypeError, "ws")):
         with pytest.raises(kind, match=text):
             on_cpu.moe_forward_few(**{**good, **change})

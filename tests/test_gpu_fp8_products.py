@@ -416,3 +416,51 @@ def test_expert_ffn_from_8bit_products(moe, T, D, E, F, k):
     out.zero_()
     graph.replay()
     assert torch.equal(out, want) and moe.moe_get_device_status(ws) == 0
+
+
+def test_the_most_groups(moe, status):
+    """1024 groups: most of them empty, one row in many, many rows in a few."""
+    G, R, N, K = 1024, 900, 72, 272
+    x, xe, [(W, We)] = operands(11, G, R, N, K)
+    gen = torch.Generator().manual_seed(4)
+    cut = torch.cat([torch.randint(0, R + 1, (500,), generator=gen),
+                     torch.randint(0, 40, (523,), generator=gen)]).sort().values.tolist()
+    bounds = [0, *cut, R]
+    off = torch.tensor(bounds, dtype=torch.int32, device="cuda")
+    y = torch.empty((R, N), device="cuda")
+    moe.moe_grouped_gemm_fp8(x, xe, W, We, y, offsets=off, ws=status)
+    ref, mag = product64(x, xe, W, We, bounds)
+    assert bool(((y.double() - ref).abs() <= (K / 32 + 1) * 2.0 ** -22 * mag).all())
+
+
+def test_more_than_2_to_the_31_elements(moe, status):
+    """Codes, exponents and outputs whose offsets pass 32 bits."""
+    R, K = 360_000, 6144                        # 2.2e9 codes from five rows
+    gen = torch.Generator().manual_seed(12)
+    x = torch.randn(5, K, generator=gen).to(torch.bfloat16).cuda()
+    idx = torch.randint(0, 5, (R,), generator=gen, dtype=torch.int32).cuda()
+    codes = torch.empty((R, K), dtype=torch.uint8, device="cuda")
+    exps = torch.empty((R, K // 128), dtype=torch.int8, device="cuda")
+    moe.moe_quantize_fp8(x, codes, exps, idx=idx, ws=status)
+    vals, e = quantize64(x)
+    for r in (0, 1, 349_524, 349_526, R - 1):   # around 2^31 / 6144 too
+        assert torch.equal(TABLE[codes[r].cpu().long()], vals[idx[r].item()])
+        assert torch.equal(exps[r].cpu().int(), e[idx[r].item()].int())
+    W, We = rand_codes(gen, (1, 8, K)), rand_exps(gen, (1, 1, K // 128))
+    y = torch.empty((R, 8), device="cuda")
+    moe.moe_grouped_gemm_fp8(codes, exps, W, We, y, ws=status)
+    base, base_e = torch.empty((5, K), dtype=torch.uint8, device="cuda"), torch.empty((5, K // 128), dtype=torch.int8, device="cuda")
+    moe.moe_quantize_fp8(x, base, base_e)
+    ref, mag = product64(base, base_e, W, We, [0, 5])
+    assert bool(((y.double() - ref[idx.long()]).abs() <= (K / 32 + 1) * 2.0 ** -22 * mag[idx.long()]).all())
+    del codes, exps, y
+    R, N, K = 270_000, 8192, 16                 # 2.2e9 outputs
+    x, xe, [(W, We)] = operands(13, 1, 64, N, K)
+    xs, es = x.repeat(R // 64 + 1, 1)[:R].contiguous(), xe.repeat(R // 64 + 1, 1)[:R].contiguous()
+    y = torch.empty((R, N), dtype=torch.bfloat16, device="cuda")
+    moe.moe_grouped_gemm_fp8(xs, es, W, We, y, ws=status)
+    small = torch.empty((64, N), dtype=torch.bfloat16, device="cuda")
+    moe.moe_grouped_gemm_fp8(x, xe, W, We, small)
+    for r in (0, 131_072, 262_143, 262_144, R - 64):
+        at = torch.arange(r, r + 64, device="cuda")
+        assert torch.equal(y[r:r + 64], small[at % 64])
