@@ -799,8 +799,8 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
     Unit u;
     int as = 0, bs = 0, buf = 0, slot = 0;
     uint32_t aph = 0, cph = 0, sph = 0;
-    const uint64_t desc_a = ptx::smem_desc_sw128(ptx::smem_addr(ring_a));
-    const uint64_t desc_b = ptx::smem_desc_sw128(ptx::smem_addr(ring_b));
+    const uint32_t desc_a = ptx::desc_sw128_lo(ptx::smem_addr(ring_a));
+    const uint32_t desc_b = ptx::desc_sw128_lo(ptx::smem_addr(ring_b));
     while (q.next(ss, u, abort, lane)) {
       int k0, k1;
       unit_k<EB>(p, u, &k0, &k1);
@@ -811,6 +811,8 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
       // sizes of a K-block within its stage, in the descriptors' units of 16 bytes
       const int a_step = (u.down ? kAStage : (sh ? p.fpt_s : p.fpt_r) * 2 * 128) >> 4;
       const int b_step = n * 128 >> 4;
+      // down: the four steps of a K-block name the token word's bytes in turn
+      const uint32_t id_step = u.down ? ptx::idesc_sf_byte(0, 1) : 0u;
       bool ok = true;
       for (int seg = k0; seg < k1 && ok; seg += kSegment) {
         const int seg_end = min(seg + kSegment, k1);
@@ -823,7 +825,7 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
           int kk = seg;
           while (ok && kk < seg_end) {
             if (!ptx::mbar_wait(&ss.full[as], aph, abort)) { ok = false; break; }
-            uint64_t da = desc_a + as * (kAStage >> 4), db = desc_b + bs * (kBStage >> 4);
+            uint32_t da = desc_a + as * (kAStage >> 4), db = desc_b + bs * (kBStage >> 4);
             const int end = min(kk + sub, seg_end);
             for (; kk < end; ++kk, da += a_step, db += b_step) {
               if (FP8 && (kk == k0 || (kk & 3) == 0) &&
@@ -834,11 +836,11 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
                 // gate/up: one word per row covers four K-blocks; down: one word
                 // per row and K-block covers its four steps of 32
                 const uint32_t sfb = sfa + 4 + (u.down ? (kk & 3) * 4 : 0);
+                const uint32_t id = idesc | ptx::idesc_sf_byte(kk & 3, u.down ? 0 : kk & 3);
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                  ptx::mma_mxf8_ss(acc, da + 2 * k, db + 2 * k,
-                                   idesc | ptx::idesc_sf_byte(kk & 3, u.down ? k : kk & 3), sfa,
-                                   sfb, k > 0 ? 1u : more);
+                  ptx::mma_mxf8_ss(acc, ptx::desc_sw128(da + 2 * k), ptx::desc_sw128(db + 2 * k),
+                                   id + k * id_step, sfa, sfb, k > 0 ? 1u : more);
                 if ((kk & 3) == 3 || kk == k1 - 1) {
                   ptx::mma_commit(&ss.sf_empty[slot]);
                   if (++slot == 2) { slot = 0; sph ^= 1u; }
@@ -846,7 +848,8 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
               } else {
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                  ptx::mma_f16_ss(acc, da + 2 * k, db + 2 * k, idesc, k > 0 ? 1u : more);
+                  ptx::mma_f16_ss(acc, ptx::desc_sw128(da + 2 * k), ptx::desc_sw128(db + 2 * k), idesc,
+                                  k > 0 ? 1u : more);
               }
               acc += n;
               if (acc == acc_end) {

@@ -393,6 +393,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
     }
   } else if (warp == 1) {
     if (ptx::elect_one()) {
+      const uint32_t desc_w = ptx::desc_sw128_lo(ptx::smem_addr(ring));
+      const uint32_t desc_x = ptx::desc_sw128_lo(ptx::smem_addr(ring_x));
       int ws = 0, xs = 0, buf = 0, slot = 0;
       uint32_t phase = 0, aphase = 0, sphase = 0;
       bool ok = true;
@@ -407,13 +409,13 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
           }
           if (!ptx::mbar_wait(&ss.full[ws], phase, abort)) { ok = false; break; }
           ptx::tc_fence_after();
-          const uint64_t da = ptx::smem_desc_sw128(ptx::smem_addr(ring + ws * kWTile));
-          const uint64_t db = ptx::smem_desc_sw128(ptx::smem_addr(ring_x + xs * C::X_BYTES));
+          const uint32_t da = desc_w + ws * (kWTile >> 4), db = desc_x + xs * (C::X_BYTES >> 4);
           const uint32_t id = idesc | ptx::idesc_sf_byte(kb & 3, kb & 3);
           const uint32_t sfa = sf_base + slot * kSfSlotCols, sfb = sfa + 4;
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            ptx::mma_mxf8_ss(acc, da + 2 * k, db + 2 * k, id, sfa, sfb, kb > kb0 || k > 0);
+            ptx::mma_mxf8_ss(acc, ptx::desc_sw128(da + 2 * k), ptx::desc_sw128(db + 2 * k), id, sfa, sfb,
+                             k > 0 ? 1u : kb > kb0);
           ptx::mma_commit(&ss.empty[ws]);
           if (++ws == C::WST) { ws = 0; phase ^= 1u; }
           if (++xs == C::XST) xs = 0;

@@ -21,6 +21,17 @@ __device__ __forceinline__ bool elect_one() {
   return ok != 0;
 }
 
+// The descriptor of ptx::smem_desc_sw128 from its low word (address >> 4 and the
+// leading offset): only that word changes from tile to tile and step to step,
+// and adding to it alone saves the issuing thread the carries.
+__device__ __forceinline__ uint32_t desc_sw128_lo(uint32_t saddr) {
+  return ((saddr & 0x3FFFFu) >> 4) | (1u << 16);
+}
+__device__ __forceinline__ uint64_t desc_sw128(uint32_t lo) {
+  constexpr uint32_t hi = (1024u >> 4) | (1u << 14) | (2u << 29);
+  return (uint64_t)hi << 32 | lo;
+}
+
 // Instruction descriptor of tcgen05.mma kind::mxf8f6f4 with block scales:
 // A and B E4M3 (format 0), both K-major, fp32 accumulator, scales E8M0 (bit
 // 23), N >> 3 in bits 17-22, M >> 4 in bits 24-28.  The byte of each 32-bit
