@@ -27,7 +27,8 @@
 //   warp 1      TMEM allocator and MMA issuer (one elected thread)
 //   warps 2-9   epilogue: TMEM -> registers -> global, two warps for each lane
 //               quarter, which take turns of 16 rows; two accumulators, so a
-//               tile's epilogue overlaps the next tile's products
+//               tile's epilogue overlaps the next tile's products (three
+//               where a CTA takes two weight tiles at a time and they fit)
 //   warps 10-13 scale writers: the exponents of sixteen K-blocks at a time,
 //               loaded a row per thread while the sixteen before them are in
 //               use, exchanged through shared memory, and written as 32-bit
@@ -59,7 +60,6 @@ constexpr int kThreads = (kRowWarp + 1) * 32;
 constexpr int kMaxStages = 11;          // of either ring
 constexpr int kRingBytes = 208 * 1024;
 constexpr int kMaxG = 1024;
-constexpr int kSfSlotCols = 12;          // 4 columns for the weights, 8 for the rows
 constexpr unsigned kAll = 0xffffffffu;
 
 struct alignas(64) GemmParams8 {
@@ -89,26 +89,34 @@ struct Tile8 {
   int g, n0, row0, rows;     // group, first output column, first row, rows
 };
 
-template <int NT>
+// NT: rows of a tile.  NW: weight tiles of 128 that share the rows of a stage (2:
+// the rows are staged once for twice the products, which halves what a product
+// draws from L2).
+template <int NT, int NW>
 struct Cfg {
   // rows of one TMA box of the row operand: a tile loads only as many boxes as
   // its rows need
   static constexpr int XBOX = NT % 48 == 0 ? 48 : 32;
   static constexpr int X_BYTES = NT * kBK;
+  static constexpr int W_BYTES = NW * kWTile;
   // The rows come from L2, whose latency under this load takes five or six
-  // K-blocks to cover; six stages of weights keep HBM busy (5 + 6 instead of 4
-  // + 8 at NT = 160: see the figures below).
-  static constexpr int XST = NT > 160 ? 4 : NT > 144 ? 5 : 6;
-  static constexpr int WST = (kRingBytes - XST * X_BYTES) / kWTile < kMaxStages
-                                 ? (kRingBytes - XST * X_BYTES) / kWTile
+  // K-blocks of one weight tile to cover; six stages of weights keep HBM busy.
+  // (64 experts, 8192 rows, N = 2048, K = 6144 gated: 290 us with 5 + 6 stages of
+  // rows and weights, 318 with 4 + 8.)
+  static constexpr int XST = NW == 2 ? kRingBytes / (W_BYTES + X_BYTES) : NT > 160 ? 4 : NT > 144 ? 5 : 6;
+  static constexpr int WST = NW == 2 ? XST
+                             : (kRingBytes - XST * X_BYTES) / W_BYTES < kMaxStages
+                                 ? (kRingBytes - XST * X_BYTES) / W_BYTES
                                  : kMaxStages;
-  static constexpr int RING = WST * kWTile + XST * X_BYTES;
+  static constexpr int RING = WST * W_BYTES + XST * X_BYTES;
   static_assert(XST <= WST, "the weights' stages release the rows'");
-  static constexpr int SF_COLS = 2 * kSfSlotCols;
-  static constexpr uint32_t TMEM_COLS = 2 * NT + SF_COLS <= 128   ? 128
-                                        : 2 * NT + SF_COLS <= 256 ? 256
-                                                                  : 512;
-  static_assert(2 * NT + SF_COLS <= 512 && NT % 16 == 0 && NT <= 240, "tensor memory columns");
+  // scale columns of a slot: 4 for each weight tile, 8 for the rows
+  static constexpr int SF_SLOT = 4 * NW + 8;
+  // accumulators, used in turn: two, or the three that fit
+  static constexpr int ACC = NW == 2 && 3 * NT + 2 * SF_SLOT <= 512 ? 3 : 2;
+  static constexpr int COLS = ACC * NT + 2 * SF_SLOT;
+  static constexpr uint32_t TMEM_COLS = COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
+  static_assert(COLS <= 512 && NT % 16 == 0 && NT <= 240, "tensor memory columns");
   static_assert(NT % XBOX == 0 && XBOX % 8 == 0 && X_BYTES % 1024 == 0, "row boxes");
 };
 
@@ -116,7 +124,7 @@ struct Shared8 {
   // of the weights' stages; a K-block's rows arrive on the same barrier
   uint64_t full[kMaxStages], empty[kMaxStages];
   uint64_t sf_full[2], sf_empty[2];
-  uint64_t acc_full[2], acc_empty[2];
+  uint64_t acc_full[3], acc_empty[3];
   uint64_t drain;
   uint64_t sf_bar;             // barrier of the four scale warps
   uint32_t tmem_base;
@@ -126,9 +134,9 @@ struct Shared8 {
   GroupMap gm;
 };
 
-template <int NT>
+template <int NT, int NW>
 constexpr int smem_bytes8() {
-  return 1024 + Cfg<NT>::RING + (int)sizeof(Shared8);
+  return 1024 + Cfg<NT, NW>::RING + (int)sizeof(Shared8);
 }
 
 __device__ __forceinline__ int blocks_of(int rows, int nt) { return (rows + nt - 1) / nt; }
@@ -171,7 +179,7 @@ __device__ void build_groups(GroupMap& gm, const GemmParams8& p, int lane) {
 // The tiles of one CTA (or team of CTAs): t, t + step, ...  Tiles are numbered
 // by group, then output column tile, row blocks fastest (the CTAs that run
 // together share weight tiles through L2).
-template <bool GATED>
+template <bool GATED, int NW>
 struct Walk {
   int t, step, total;
   int g = 0;
@@ -192,7 +200,7 @@ struct Walk {
     }
     Tile8 ti;
     ti.g = g;
-    ti.n0 = local * (GATED ? 64 : 128);
+    ti.n0 = local * (GATED ? 64 : 128) * NW;
     ti.row0 = gm.off[g] + b * per;
     ti.rows = min(per, rows - b * per);
     return ti;
@@ -284,13 +292,14 @@ __device__ __forceinline__ void store16(const GemmParams8& p, const Tile8& ti, i
   }
 }
 
-template <int NT, bool GATED>
+template <int NT, bool GATED, int NW>
 __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_constant__ GemmParams8 p) {
-  using C = Cfg<NT>;
+  using C = Cfg<NT, NW>;
+  constexpr int COLS_W = GATED ? 64 : 128;   // output columns of a weight tile
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = ptx::smem_addr(smem_raw);
   uint8_t* ring = smem_raw + (((raw + 1023u) & ~1023u) - raw);
-  uint8_t* ring_x = ring + C::WST * kWTile;
+  uint8_t* ring_x = ring + C::WST * C::W_BYTES;
   Shared8& ss = *reinterpret_cast<Shared8*>(ring + C::RING);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -307,6 +316,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(&ss.sf_full[i], 4);
       ptx::mbar_init(&ss.sf_empty[i], 1);
+    }
+    for (int i = 0; i < C::ACC; ++i) {
       ptx::mbar_init(&ss.acc_full[i], 1);
       ptx::mbar_init(&ss.acc_empty[i], kEpiWarps);
     }
@@ -329,12 +340,12 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
   ptx::tc_fence_after();
 
   const uint32_t tmem = ss.tmem_base;
-  const uint32_t sf_base = tmem + 2 * NT;
+  const uint32_t sf_base = tmem + C::ACC * NT;
   volatile int* abort = &ss.abort;
   // a cluster of `split` CTAs works on the same tile, each on its K-blocks
   const int rank = p.split > 1 ? (int)ptx::cluster_rank() : 0;
   const int first = blockIdx.x / p.split, step = gridDim.x / p.split;
-  Walk<GATED> walk(ss.gm, p, first, step);
+  Walk<GATED, NW> walk(ss.gm, p, first, step);
   const int kb0 = (int)((long long)p.KB * rank / p.split);
   const int kb1 = (int)((long long)p.KB * (rank + 1) / p.split);
   // scale words cover K-blocks 4s .. 4s + 3
@@ -354,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
         const Tile8 ti = walk.tile(ss.gm, p);
         const int wrow = ti.g * p.N + ti.n0;
         const int boxes = (mma_rows(ti.rows) + C::XBOX - 1) / C::XBOX;
-        const int bytes = wside ? kWTile : boxes * C::XBOX * kBK;
+        const int bytes = wside ? C::W_BYTES : boxes * C::XBOX * kBK;
         for (int kb = kb0; kb < kb1; ++kb) {
           if (lag > 0) {
             --lag;
@@ -373,14 +384,16 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
             for (int j = 0; j < boxes; ++j)
               load(dst + j * C::XBOX * kBK, &p.x, ti.row0 + j * C::XBOX);
           } else if (GATED) {
-            uint8_t* dst = ring + stage * kWTile;
+            uint8_t* dst = ring + stage * C::W_BYTES;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < 4 * NW; ++j) {
               load(dst + j * 4096, &p.w1, wrow + j * 16);
               load(dst + j * 4096 + 2048, &p.w3, wrow + j * 16);
             }
           } else {
-            load(ring + stage * kWTile, &p.w1, wrow);
+#pragma unroll
+            for (int w = 0; w < NW; ++w)
+              load(ring + stage * C::W_BYTES + w * kWTile, &p.w1, wrow + w * 128);
           }
           issued |= 1u << stage;
           parity = (parity & ~(1u << stage)) | (phase << stage);
@@ -401,21 +414,50 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
       for (; ok && walk.more(); walk.next()) {
         const Tile8 ti = walk.tile(ss.gm, p);
         const uint32_t idesc = ptx::idesc_mxf8(128, mma_rows(ti.rows));
+        // the products of K-block kb with weight tile w, from a stage
+        auto products = [&](int w, int acc, int kb, int wstage, int xstage) {
+          const uint32_t da = desc_w + wstage * (C::W_BYTES >> 4) + w * (kWTile >> 4);
+          const uint32_t db = desc_x + xstage * (C::X_BYTES >> 4);
+          const uint32_t id = idesc | ptx::idesc_sf_byte(kb & 3, kb & 3);
+          const uint32_t sf = sf_base + slot * C::SF_SLOT;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            ptx::mma_mxf8_ss(tmem + acc * NT, ptx::desc_sw128(da + 2 * k), ptx::desc_sw128(db + 2 * k),
+                             id, sf + 4 * w, sf + 4 * NW, k > 0 ? 1u : kb > kb0);
+        };
+        auto next_acc = [&] {
+          if (++buf == C::ACC) { buf = 0; aphase ^= 1u; }
+        };
         if (!ptx::mbar_wait(&ss.acc_empty[buf], aphase ^ 1u, abort)) break;
-        const uint32_t acc = tmem + buf * NT;
+        const int acc0 = buf;
+        int lead = kb0;                  // K-blocks that the first weight tile is done with
+        if (NW == 2) {
+          // while the second accumulator is still being stored, the first weight
+          // tile goes ahead: by the K-blocks that the ring and a scale slot hold
+          next_acc();
+          if (!ptx::mbar_wait(&ss.sf_full[slot], sphase, abort)) break;
+          int ls = ws;
+          uint32_t lphase = phase;
+          const int most = min(kb1, C::WST < 4 ? C::WST : 4);
+          while (ok && lead < most && !ptx::mbar_test(&ss.acc_empty[buf], aphase ^ 1u)) {
+            ok = ptx::mbar_wait(&ss.full[ls], lphase, abort);
+            ptx::tc_fence_after();
+            if (ok) products(0, acc0, lead++, ls, ls);
+            if (++ls == C::WST) { ls = 0; lphase ^= 1u; }
+          }
+          if (!ok || !ptx::mbar_wait(&ss.acc_empty[buf], aphase ^ 1u, abort)) break;
+        }
         for (int kb = kb0; kb < kb1; ++kb) {
           if (kb == kb0 || (kb & 3) == 0) {
             if (!ptx::mbar_wait(&ss.sf_full[slot], sphase, abort)) { ok = false; break; }
           }
           if (!ptx::mbar_wait(&ss.full[ws], phase, abort)) { ok = false; break; }
           ptx::tc_fence_after();
-          const uint32_t da = desc_w + ws * (kWTile >> 4), db = desc_x + xs * (C::X_BYTES >> 4);
-          const uint32_t id = idesc | ptx::idesc_sf_byte(kb & 3, kb & 3);
-          const uint32_t sfa = sf_base + slot * kSfSlotCols, sfb = sfa + 4;
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            ptx::mma_mxf8_ss(acc, ptx::desc_sw128(da + 2 * k), ptx::desc_sw128(db + 2 * k), id, sfa, sfb,
-                             k > 0 ? 1u : kb > kb0);
+          if (NW == 1 || kb >= lead) products(0, acc0, kb, ws, xs);
+          if (NW == 2) {
+            if (kb == kb1 - 1) ptx::mma_commit(&ss.acc_full[acc0]);
+            products(1, buf, kb, ws, xs);
+          }
           ptx::mma_commit(&ss.empty[ws]);
           if (++ws == C::WST) { ws = 0; phase ^= 1u; }
           if (++xs == C::XST) xs = 0;
@@ -426,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
         }
         if (!ok) break;
         ptx::mma_commit(&ss.acc_full[buf]);
-        if (++buf == 2) { buf = 0; aphase ^= 1u; }
+        next_acc();
       }
       // nothing is in flight when tensor memory is freed
       ptx::mma_commit(&ss.drain);
@@ -434,16 +476,17 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
     }
   } else if (warp < kSfWarp0) {
     const int q = warp & 3;              // TMEM lane quarter of this warp
-    const int half = (warp - 2) >> 2;    // its turn among the quarter's two warps
-    int buf = 0;
+    const int half = (warp - 2) >> 2;    // its turn of 16 rows among the quarter's two warps
+    int buf = 0, w = 0;
     uint32_t aphase = 0;
-    for (; walk.more(); walk.next()) {
-      const Tile8 ti = walk.tile(ss.gm, p);
+    while (walk.more()) {
+      Tile8 ti = walk.tile(ss.gm, p);
+      ti.n0 += w * COLS_W;
       if (__any_sync(kAll, !ptx::mbar_wait(&ss.acc_full[buf], aphase, abort))) break;
       ptx::tc_fence_after();
       const uint32_t acc = tmem + buf * NT + ((uint32_t)(q * 32) << 16);
       auto use = [&](int c, const uint32_t (&v)[16]) {
-        if (p.split > 1) {
+        if (NW == 1 && p.split > 1) {
           // this CTA's part of the tile, [row][weight row], in the ring (all its
           // loads and products are done, and a cluster has one tile)
           float* part = reinterpret_cast<float*>(ring) + (size_t)c * 128 + q * 32 + lane;
@@ -470,7 +513,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
       ptx::tc_fence_before();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&ss.acc_empty[buf]);
-      if (++buf == 2) { buf = 0; aphase ^= 1u; }
+      if (++buf == C::ACC) { buf = 0; aphase ^= 1u; }
+      if (++w == NW) { w = 0; walk.next(); }
     }
   } else {
     constexpr int RPT = (NT + 127) / 128;      // rows per thread
@@ -483,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
     bool bad = false, ok = true;
     // chunk c: K-blocks 16 c .. 16 c + 15, scale sets 4 c .. 4 c + 3
     const int c0 = s0 / 4, c1 = (s1 + 3) / 4;
-    uint32_t xw[RPT][4], ww[4];
+    uint32_t xw[RPT][4], ww[NW][4];
     auto load = [&](const Tile8& ti, int c) {
       const int n = min(16, p.KB - 16 * c);
 #pragma unroll
@@ -494,8 +538,13 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
                     p.xe + (size_t)p.R * p.KB, xw[i]);
       }
       const int8_t* we = GATED && (lane & 16) ? p.w3e : p.w1e;
-      load_exps(we + ((size_t)ti.g * p.NB + ti.n0 / 128) * p.KB + 16 * c, n, we,
-                we + (size_t)p.G * p.NB * p.KB, ww);
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        // (a second weight tile may lie behind the last column: any scale will do)
+        const int nb = min((ti.n0 + w * COLS_W) / 128, p.NB - 1);
+        load_exps(we + ((size_t)ti.g * p.NB + nb) * p.KB + 16 * c, n, we,
+                  we + (size_t)p.G * p.NB * p.KB, ww[w]);
+      }
     };
     int c = c0;
     Tile8 ti{};
@@ -505,9 +554,11 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
     }
     while (ok && walk.more()) {
       const int n = min(16, p.KB - 16 * c);
-      uint32_t wa[4];
+      uint32_t wa[NW][4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) wa[i] = scale_bytes(ww[i], i, n, &bad);
+      for (int w = 0; w < NW; ++w)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) wa[w][i] = scale_bytes(ww[w][i], i, n, &bad);
 #pragma unroll
       for (int i = 0; i < RPT; ++i) {
         const int r = tid + 128 * i;
@@ -539,13 +590,16 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
           break;
         }
         ptx::tc_fence_after();
-        const uint32_t dst = sf_base + slot * kSfSlotCols + lanes;
-        const uint32_t w4[4] = {wa[j], wa[j], wa[j], wa[j]};
-        ptx::tmem_st_x4(dst, w4);
+        const uint32_t dst = sf_base + slot * C::SF_SLOT + lanes, dx = dst + 4 * NW;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+          const uint32_t w4[4] = {wa[w][j], wa[w][j], wa[w][j], wa[w][j]};
+          ptx::tmem_st_x4(dst + 4 * w, w4);
+        }
         // (words of rows behind the tile's last are whatever stood there)
-        if (XC > 4 && rows > 128) ptx::tmem_st_x8(dst + 4, wx);
-        else if (XC > 1) ptx::tmem_st_x4(dst + 4, wx);
-        else ptx::tmem_st_x1(dst + 4, wx[0]);
+        if (XC > 4 && rows > 128) ptx::tmem_st_x8(dx, wx);
+        else if (XC > 1) ptx::tmem_st_x4(dx, wx);
+        else ptx::tmem_st_x1(dx, wx[0]);
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
         __syncwarp();
@@ -558,10 +612,10 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
   }
 
   __syncthreads();
-  if (p.split > 1) {
+  if (NW == 1 && p.split > 1) {
     // partial tiles -> outputs: rank r finishes the rows r, r + split, ...
     ptx::cluster_sync();
-    Walk<GATED> own(ss.gm, p, first, step);
+    Walk<GATED, NW> own(ss.gm, p, first, step);
     if (own.more() && !*abort) {
       const Tile8 ti = own.tile(ss.gm, p);
       const uint32_t part = ptx::smem_addr(ring);
@@ -608,11 +662,11 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
   }
 }
 
-template <int NT, bool GATED>
+template <int NT, bool GATED, int NW>
 cudaError_t launch_nt(const GemmParams8& p, long long tiles, cudaStream_t st) {
-  constexpr int smem = smem_bytes8<NT>();
+  constexpr int smem = smem_bytes8<NT, NW>();
   static std::atomic<uint64_t> smem_set{0};
-  cudaError_t e = set_smem_once(gemm_fp8_kernel<NT, GATED>, smem, smem_set);
+  cudaError_t e = set_smem_once(gemm_fp8_kernel<NT, GATED, NW>, smem, smem_set);
   if (e != cudaSuccess) return e;
   const long long want = tiles * p.split, sms = num_sms();
   cudaLaunchConfig_t cfg = {};
@@ -628,22 +682,22 @@ cudaError_t launch_nt(const GemmParams8& p, long long tiles, cudaStream_t st) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, gemm_fp8_kernel<NT, GATED>, p);
+  return cudaLaunchKernelEx(&cfg, gemm_fp8_kernel<NT, GATED, NW>, p);
 }
 
-template <int NT>
-cudaError_t launch_any(GemmParams8& p, bool gated, cudaStream_t st, const char** why,
-                       const Gemm8Args& a) {
-  const uint32_t box = gated ? 16 : 128;
-  bool ok = make_tensor_map(&p.x, a.x, a.R, a.K, Cfg<NT>::XBOX, kBK, 1, 128) &&
+template <int NT, int NW, bool GATED>
+cudaError_t launch_any(GemmParams8& p, cudaStream_t st, const char** why, const Gemm8Args& a) {
+  const uint32_t box = GATED ? 16 : 128;
+  bool ok = make_tensor_map(&p.x, a.x, a.R, a.K, Cfg<NT, NW>::XBOX, kBK, 1, 128) &&
             make_tensor_map(&p.w1, a.W1, (uint64_t)a.G * a.N, a.K, box, kBK, 1, 128);
   p.w3 = p.w1;
-  if (ok && gated) ok = make_tensor_map(&p.w3, a.W3, (uint64_t)a.G * a.N, a.K, box, kBK, 1, 128);
+  if (ok && GATED) ok = make_tensor_map(&p.w3, a.W3, (uint64_t)a.G * a.N, a.K, box, kBK, 1, 128);
   if (!ok) {
     *why = "cuTensorMapEncodeTiled failed for a product operand";
     return cudaErrorInvalidValue;
   }
-  p.nt = gated ? (a.N + 63) / 64 : (a.N + 127) / 128;
+  constexpr int COLS = (GATED ? 64 : 128) * NW;
+  p.nt = (a.N + COLS - 1) / COLS;
   // row blocks: at most one per group with rows, and one per NT rows
   const long long blocks = std::min<long long>(a.R, (long long)a.R / NT + std::min(a.G, a.R));
   const long long tiles = blocks * p.nt;
@@ -654,15 +708,59 @@ cudaError_t launch_any(GemmParams8& p, bool gated, cudaStream_t st, const char**
   // 8.4 against 11.7; one row, N = 6144, K = 2048 8.3 against 7.5, which is why
   // eight K-blocks are not enough.)
   p.split = 1;
-  for (int s = 2; s <= 8; s *= 2)
+  for (int s = 2; NW == 1 && s <= 8; s *= 2)
     if (tiles * s <= num_sms() && p.KB >= s * 2 && p.KB - p.KB / s >= 9) p.split = s;
-  return gated ? launch_nt<NT, true>(p, tiles, st) : launch_nt<NT, false>(p, tiles, st);
+  return launch_nt<NT, GATED, NW>(p, tiles, st);
+}
+
+// Rows per tile.  240 (two accumulators of that width fill tensor memory) read
+// the weights for the most rows; narrower tiles leave shared memory to the
+// weights' ring.  So: the narrowest that cuts a group into no more blocks than
+// 240 would, for groups two standard deviations above the average; and narrower
+// still while a quarter of the SMs have no tile.  (17 groups of 632 rows, N = 40,
+// K = 528 gated: 10.0 us narrowed against 13.3; 73 groups of 297, N = 24, K =
+// 144, with a tile for 146 of 148 SMs: 12.7 narrowed against 9.6.)
+//
+// Two weight tiles for the rows of a stage, where the tiles are many: halving
+// their number must not leave SMs idle at the end, and the epilogue, which the
+// next tile covers only in part, must be small beside the products.  At 160 rows
+// three accumulators fit, so from 8 tiles an SM on (128 groups of 256 rows, N =
+// 4096: 117 us against 136 at K = 512, 252 against 286 at K = 1408; gated 576
+// against 675; 5 tiles an SM, 128 groups of 125 rows, N = 768, K = 1024: 37.1
+// against 35.3).  At 240 rows only two fit, which 32 K-blocks make up for (one
+// group of 8192 rows, N = 8192: 372 us against 400 at K = 6144, 133 against 125 at
+// K = 2048); the gated epilogue is longer, and there 160 rows are faster (K = 6144:
+// 724 against 766, and 765 with one weight tile).
+template <bool GATED>
+cudaError_t launch_rows(GemmParams8& p, cudaStream_t st, const char** why, const Gemm8Args& a) {
+  const int groups = std::min(a.G, a.R), avg = (a.R + groups - 1) / groups;
+  const int top = a.G > 1 ? avg + (int)(2.f * sqrtf((float)avg)) : avg;
+  const int nb = (top + 239) / 240, need = (top + nb - 1) / nb;
+  constexpr int widths[] = {32, 64, 96, 144, 160, 240};
+  int w = 0;
+  while (widths[w] < need) ++w;
+  const long long cols = GATED ? (a.N + 63) / 64 : (a.N + 127) / 128;
+  auto tiles = [&] { return (long long)groups * ((avg + widths[w] - 1) / widths[w]) * cols; };
+  while (w > 0 && tiles() < num_sms() * 3 / 4) --w;
+  const bool long_k = p.KB >= 32;
+  if (widths[w] > 96 && (widths[w] < 240 || long_k) && tiles() >= (long_k ? 4 : 8) * num_sms()) {
+    if constexpr (!GATED)
+      if (widths[w] == 240) return launch_any<240, 2, GATED>(p, st, why, a);
+    return launch_any<160, 2, GATED>(p, st, why, a);
+  }
+  switch (widths[w]) {
+    case 32: return launch_any<32, 1, GATED>(p, st, why, a);
+    case 64: return launch_any<64, 1, GATED>(p, st, why, a);
+    case 96: return launch_any<96, 1, GATED>(p, st, why, a);
+    case 144: return launch_any<144, 1, GATED>(p, st, why, a);
+    case 160: return launch_any<160, 1, GATED>(p, st, why, a);
+    default: return launch_any<240, 1, GATED>(p, st, why, a);
+  }
 }
 
 }  // namespace
 
 cudaError_t launch_gemm_fp8(const Gemm8Args& a, cudaStream_t st, const char** why) {
-  const bool gated = a.W3 != nullptr;
   GemmParams8 p{};
   p.xe = a.xe;
   p.w1e = a.W1e;
@@ -675,30 +773,7 @@ cudaError_t launch_gemm_fp8(const Gemm8Args& a, cudaStream_t st, const char** wh
   p.NB = (a.N + 127) / 128;
   p.status = a.status;
   *why = "product launch";
-  // Rows per tile.  240 (two accumulators of that width fill tensor memory) read
-  // the weights for the most rows; narrower tiles leave shared memory to the
-  // weights' ring.  So: the narrowest that cuts a group into no more blocks
-  // than 240 would, for groups two standard deviations above the average; and
-  // narrower still while a quarter of the SMs have no tile.  (17 groups of 632
-  // rows, N = 40, K = 528 gated: 10.0 us narrowed against 13.3; 73 groups of
-  // 297, N = 24, K = 144, with a tile for 146 of 148 SMs: 12.7 narrowed against
-  // 9.6.)
-  const int groups = std::min(a.G, a.R), avg = (a.R + groups - 1) / groups;
-  const int top = a.G > 1 ? avg + (int)(2.f * sqrtf((float)avg)) : avg;
-  const int nb = (top + 239) / 240, need = (top + nb - 1) / nb;
-  constexpr int widths[] = {32, 64, 96, 144, 160, 240};
-  int w = 0;
-  while (widths[w] < need) ++w;
-  const long long cols = gated ? (a.N + 63) / 64 : (a.N + 127) / 128;
-  while (w > 0 && (long long)groups * ((avg + widths[w] - 1) / widths[w]) * cols < num_sms() * 3 / 4) --w;
-  switch (widths[w]) {
-    case 32: return launch_any<32>(p, gated, st, why, a);
-    case 64: return launch_any<64>(p, gated, st, why, a);
-    case 96: return launch_any<96>(p, gated, st, why, a);
-    case 144: return launch_any<144>(p, gated, st, why, a);
-    case 160: return launch_any<160>(p, gated, st, why, a);
-    default: return launch_any<240>(p, gated, st, why, a);
-  }
+  return a.W3 ? launch_rows<true>(p, st, why, a) : launch_rows<false>(p, st, why, a);
 }
 
 }  // namespace moe

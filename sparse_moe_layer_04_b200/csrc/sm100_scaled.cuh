@@ -100,6 +100,19 @@ __device__ __forceinline__ uint32_t bytes_word(const int8_t* q, int n) {
   return v;
 }
 
+// Whether the barrier's phase of this parity has completed, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // A barrier of a few warps whose wait is bounded: an mbarrier that one lane of
 // each warp arrives on.  False when the wait gave up (as mbar_wait).
 struct WarpBarrier {

@@ -464,3 +464,48 @@ def test_more_than_2_to_the_31_elements(moe, status):
     for r in (0, 131_072, 262_143, 262_144, R - 64):
         at = torch.arange(r, r + 64, device="cuda")
         assert torch.equal(y[r:r + 64], small[at % 64])
+
+
+@pytest.mark.parametrize("G,R,N,K,gated", [
+    (40, 5000, 3848, 144, False),      # up to 160 rows a tile; the last pair's second weight tile is behind N
+    (40, 5000, 3976, 400, False),      # the last pair's second weight tile is ragged
+    (40, 5000, 2056, 144, True),
+    (37, 4400, 2120, 272, True),
+    (1, 1001, 15496, 4112, False),     # long K: 240 rows a tile, a pair that ends behind N
+    (3, 1400, 15368, 4240, False),
+    (1, 700, 13000, 4112, True),
+    (1, 1100, 15360, 6160, False),
+])
+def test_two_weight_tiles_for_the_same_rows(moe, status, G, R, N, K, gated):
+    """Many tiles: a CTA takes two neighbouring weight tiles at a time."""
+    x, xe, ws = operands(G + R + N + K, G, R, N, K, 2 if gated else 1)
+    xe = xe - 10
+    bounds = spread(G, R, 1, 2, N)
+    if G > 3:                                      # like groups, an empty one, one of a single row
+        bounds = [1 + (R - 3) * g // G for g in range(G)] + [R - 2]
+        bounds[5] = bounds[6]
+        bounds[20] = bounds[21] - 1
+    off = torch.tensor(bounds, dtype=torch.int32, device="cuda")
+    y = torch.full((R, N), 777.0, dtype=torch.bfloat16, device="cuda")
+    unit = (K / 32 + 1) * 2.0 ** -22
+    if gated:
+        call = lambda to: moe.moe_gated_gemm_fp8(x, xe, *ws[0], *ws[1], to, offsets=off, ws=status)
+        g, gm = product64(x, xe, *ws[0], bounds)
+        u, um = product64(x, xe, *ws[1], bounds)
+        silu = g * torch.sigmoid(g)
+        ref = silu * u
+        tol = (2.0 ** -8 + 2.0 ** -16) * ref.abs() + 1.1 * unit * gm * (u.abs() + unit * um) + \
+            silu.abs() * unit * um + 2.0 ** -133
+    else:
+        call = lambda to: moe.moe_grouped_gemm_fp8(x, xe, *ws[0], to, offsets=off, ws=status)
+        ref, mag = product64(x, xe, *ws[0], bounds)
+        tol = unit * mag + 2.0 ** -8 * ref.abs()
+    call(y)
+    none = torch.isnan(ref)
+    assert bool(none[0].all()) and bool((y[none] == 777.0).all())
+    over = ((y.double() - ref).abs() > tol) & ~none
+    assert not bool(over.any()), (int(over.sum()), over.nonzero()[:4].tolist())
+    for _ in range(3):
+        again = torch.full_like(y, 777.0)
+        call(again)
+        assert torch.equal(y, again)
