@@ -291,3 +291,25 @@ def test_with_most_sms_held(moe, fp8):
     assert moe.moe_get_device_status(L.ws) == 0
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_unchosen_experts_that_share_a_unit(moe, fp8):
+    """Narrow experts, many chosen: several of them share a unit of the second
+    product.  Infinite or NaN weights of some still reach only the tokens that
+    chose them."""
+    L = Layer(moe, 8, 2048, 64, 128, 8, 0, 128, fp8, seed=31)
+    out, idx, _ = L.run()
+    L.check(out, idx, _)
+    bad = sorted({int(idx[0, 0]), int(idx[0, 5])})
+    hit = sum((idx == e).any(1).int() for e in bad) > 0
+    assert bool(hit[0]) and not bool(hit.all())
+    for e in bad:
+        if fp8:
+            L.q["W2q"][e] = 0x7f
+        else:
+            L.w["W2"][e] = float("inf")
+    z, i2, _ = L.run()
+    assert torch.equal(i2, idx)
+    assert torch.equal(z[~hit], out[~hit]) and not bool(torch.isfinite(z[hit]).any())
+    assert moe.moe_get_device_status(L.ws) == 0
