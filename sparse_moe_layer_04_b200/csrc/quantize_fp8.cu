@@ -5,16 +5,16 @@
 //                (0 for a block of zeros)
 //   code[r, c] = E4M3(x[r, c] * 2^-e), round to nearest even
 //
-// x * 2^-e is exact in fp32 wherever the code is not zero, so each code has
-// one rounding.  448 = 0.875 * 2^9: with max = 1.m * 2^p (bf16, 7 fraction
+// x * 2^-e is exact in bf16 wherever the code is not zero, so each code has one
+// rounding.  448 = 0.875 * 2^9: with max = 1.m * 2^p (bf16, 7 fraction
 // bits), e = p - 8, or p - 7 when the fraction is above that of 448 = 1.75 *
 // 2^8, which the integer sum below decides without branches.
 //
-// 32768 x 6144 rows gathered from 4096: 65 to 73 us, 600 MB through L2 (each
-// row is read eight times, 50 MB of HBM reads and 203 MB of writes).  Without
-// the loads it takes 43 us, without the arithmetic 57: what the SMs get out of
-// L2 bounds it.  Resident warps that walk rows with the next one on its way took
-// 68.
+// 32768 x 6144 rows gathered from 4096: 66 us, 600 MB through L2 (each row is
+// read eight times, 50 MB of HBM reads and 203 MB of writes).  Without the loads
+// 43, without the arithmetic 57, and the two overlap only as far as other warps
+// are there to run: resident warps that walk rows with the next one on its way
+// took 68, sixteen of them an SM fed by bulk copies 128.
 #include <cuda_bf16.h>
 
 #include "moe_internal.cuh"
@@ -36,6 +36,13 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
 
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// Two bf16 products.
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
 
 // 32 bytes in one load (16-byte aligned addresses that are not 32-byte aligned
 // take two).
@@ -107,13 +114,12 @@ __global__ void __launch_bounds__(kThreads) quantize_fp8_kernel(
     // p - 8 with p = (bits >> 7) - 127, one more when the fraction exceeds
     // 0.75 (0x60 of 0x80): adding 0x1f carries into the exponent exactly then
     const int e = top ? max((int)((top + 0x1fu) >> 7) - 135, kQMinExp) : 0;
-    const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+    const uint32_t inv = (uint32_t)(127 - e) * 0x00800080u;   // 2^-e as bf16, twice
     uint32_t c[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const uint32_t a = w[i][2 * q], b = w[i][2 * q + 1];
-      c[q] = e4m3x2(bf_lo(a) * inv, bf_hi(a) * inv) |
-             (e4m3x2(bf_lo(b) * inv, bf_hi(b) * inv) << 16);
+      const uint32_t y = mul2(w[i][2 * q], inv), z = mul2(w[i][2 * q + 1], inv);
+      c[q] = e4m3x2(bf_lo(y), bf_hi(y)) | (e4m3x2(bf_lo(z), bf_hi(z)) << 16);
     }
     if (odd) {
       // infinities are marked like NaN (the conversion saturates them)
@@ -140,13 +146,15 @@ cudaError_t launch_quantize_fp8(const uint16_t* x, int src_rows, const int32_t* 
   // rows start on 32 bytes when the matrix does (K is a multiple of 16)
   const bool wide = (reinterpret_cast<uintptr_t>(x) & 31u) == 0;
   const int KB = (K + 127) / 128;
-  // A chunk per warp while that fits on the SMs at once (104 rows of 6144: 1.9
-  // us against 2.8); else four, whose loads a warp has in flight together
-  // (32768 rows: 70 us against 75; 17380 rows of 4544: 33 against 30).
-  if ((long long)gx * chunks <= 4ll * num_sms())
+  // A chunk per warp while that is not much more than the SMs hold at once (104
+  // rows of 6144: 1.9 us; 1000 rows: 4.1 against 4.6) or a row has no more (65536
+  // rows of 256: 14 against 21); else two, whose loads a warp has in flight
+  // together (32768 rows of 6144: 66 us, with one 77, with four 67; 16384 rows of
+  // 1024: 7.5, 8.1, 11.6).
+  if (chunks == 1 || (long long)gx * chunks <= 12ll * num_sms())
     return launch_pdl(quantize_fp8_kernel<1>, dim3(gx, chunks), dim3(kThreads), 0, st, x, src_rows,
                       idx, R, K, KB, wide, codes, exps, status);
-  return launch_pdl(quantize_fp8_kernel<4>, dim3(gx, (chunks + 3) / 4), dim3(kThreads), 0, st, x,
+  return launch_pdl(quantize_fp8_kernel<2>, dim3(gx, (chunks + 1) / 2), dim3(kThreads), 0, st, x,
                     src_rows, idx, R, K, KB, wide, codes, exps, status);
 }
 
