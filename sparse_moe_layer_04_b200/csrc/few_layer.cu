@@ -430,7 +430,7 @@ struct FewShared {
   Unit q[kQueue];
   uint32_t tmem_base;
   int abort, bad, last, exit_last;
-  int act_count;         // epilogue warps that have stored their part of a gate/up tile
+  int act_done[4];       // gate/up tiles whose part each epilogue warp has stored
   float act[2][64 * 17]; // FP8: activations of a tile [feature][token], by turns
   int tab[kFewMaxT * 32];        // the tokens' choices: their group of slots, -1 where an
                                  // earlier choice has it too (or there is none)
@@ -603,7 +603,7 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
     ptx::mbar_init(&ss.epi, 4);
     ss.abort = 0;
     ss.bad = 0;
-    ss.act_count = 0;
+    for (int i = 0; i < 4; ++i) ss.act_done[i] = 0;
     ptx::fence_barrier_init();
   }
   ptx::tc_fence_before();
@@ -877,16 +877,20 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
   } else if (warp == 3) {
     // ---------------- hand-over of activations ----------------
     // Counts a slot's finished tiles for the whole GPU, so that the epilogue
-    // does not wait for its stores to get there.
+    // does not wait for its stores to get there.  The epilogue warps may be up to
+    // two tiles apart (the two accumulator sets), and those without rows in a
+    // narrow tile run ahead, so a tile is finished when each of the four has
+    // counted it, not when four counts have come in.
     QueueReader q;
     Unit u;
-    int want = 0;
+    int tiles = 0;
+    const volatile int* done = ss.act_done;
     while (q.next(ss, u, abort, lane)) {
       if (u.down) continue;
-      want += 4;
+      ++tiles;
       const long long t0 = clock64();
       bool ok = true;
-      while (*reinterpret_cast<volatile int*>(&ss.act_count) < want) {
+      while (min(min(done[0], done[1]), min(done[2], done[3])) < tiles) {
         __nanosleep(20);
         if (*abort) { ok = false; break; }
         if (clock64() - t0 > ptx::kWaitBudgetCycles) {
@@ -912,7 +916,7 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
     Unit u;
     ptx::WarpBarrier epi{&ss.epi};
     bool waited = false;
-    int buf = 0, turn = 0;
+    int buf = 0, turn = 0, tiles = 0;
     uint32_t cph = 0, omask = 0;
     float o[16];                         // a down unit's sum over its slots, per token
 #pragma unroll
@@ -1063,10 +1067,11 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
           turn ^= 1;
         }
         // this warp's part is stored, as far as this CTA can see
+        ++tiles;
         __syncwarp();
         if (lane == 0) {
           __threadfence_block();
-          atomicAdd(&ss.act_count, 1);
+          *const_cast<volatile int*>(&ss.act_done[qt]) = tiles;
         }
       } else {
         const int d = u.at * 128 + qt * 32 + lane;
