@@ -1020,8 +1020,7 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
         for (int t = 0; t < 16; t += 2) {
           const float got = __shfl_xor_sync(kAll, up ? v[t] : v[t + 1], 16);
           const float gate = up ? got : v[t], mul = up ? v[t + 1] : got;
-          // (the division is good to 2 units)
-          const float a = f < F ? __fdividef(gate, 1.0f + expf(-gate)) * mul : 0.f;
+          const float a = f < F ? ffn::silu_times_wide<true>(gate, mul) : 0.f;
           const int tt = t + (up ? 1 : 0);
           if (FP8) {
             ss.act[turn][(qt * 16 + (lane & 15)) * 17 + tt] = a;
