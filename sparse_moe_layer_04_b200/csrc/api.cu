@@ -169,9 +169,15 @@ bool ws_layout(const moe_dims_t& d, WsLayout* L) {
   };
   L->status = take(256);
   L->ticket = take(256);
-  // counters of the few-token layer: zero between calls, so they stand where
-  // no other T of the same layer moves them
+  // What a call finds zero and leaves zero stands where no other T of the same
+  // layer moves it, so that calls of any T may share a workspace: the counters
+  // of the few-token layer, of a launch that zeroes its own (per group, then the
+  // tile claim counter and the exit ticket) and of the shared experts' launch
+  // next to the routing (the same), and the experts' token bits.
   L->f_claim = take((64 + 3 + S + std::min<size_t>(E, kFewMaxT * k) + (D + 127) / 128) * 4);
+  L->counters_d = take((E + S + 2) * 4);
+  L->counters_s = take((S + 2) * 4);
+  L->gmask = take(E * (kPermBlockTokens / 32) * 4);
   L->partials = take((size_t)sp.nsplit * T * E * 4);
   L->wr3 = take(sp.tensor && !sp.fused ? E * 3 * D * 2 : 0);
   L->idx = take(T * k * 4);
@@ -181,16 +187,13 @@ bool ws_layout(const moe_dims_t& d, WsLayout* L) {
   L->perm = take(T * k * 4);
   L->inv = take(T * k * 4);
   L->blk_base = take(nblk * E * 4);
-  L->counters = take((E + S + 2) * 4);   // per-group counters, the tile claim counter and
-                                         // the exit ticket of a launch that zeroes them itself
-  L->counters_s = take((S + 2) * 4);     // the same for a shared-experts-only launch, + its exit
-                                         // ticket
+  L->counters = take((E + S + 1) * 4);   // per-group counters and the tile claim counter of a
+                                         // launch for which the row gather zeroes them
   L->xperm = take(T * k * D * 2);
   L->act_r = take(T * k * F * 2);
   L->act_s = take(S * T * Fs * 2);
   L->y = take((T * k + S * T) * D * 4);
   L->touched = take(4);
-  L->gmask = take(T <= kPermBlockTokens ? E * (kPermBlockTokens / 32) * 4 : 0);
   L->f_route = L->f_slots = L->f_w = L->f_mask = L->f_hq = L->f_hqe = L->f_act = L->f_exp = L->f_planes = 0;
   if (T > 0 && T <= (size_t)kFewMaxT) {
     const FewPlan p16 = few_plan(d, false), p8 = few_plan(d, true);
@@ -497,6 +500,7 @@ int forward_impl(const void* h, const float* Wr, const float* bias, const Expert
   FfnArgs a = ffn_args(hb, xperm, offsets, wt, w, y, counters, dims);
   if (overlap_shared) a.part = kFfnRouted;
   if (dense) {
+    a.counters = w.at<int32_t>(w.L.counters_d);
     a.dense_a = 1;
     a.idx = idx;
     a.inv = inv;

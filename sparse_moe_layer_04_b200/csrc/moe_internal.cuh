@@ -57,11 +57,12 @@ cudaError_t noalloc_scratch(int32_t** out);
 
 // Workspace layout (byte offsets from the workspace base, 256-aligned).
 struct WsLayout {
-  size_t status, ticket, partials, wr3, idx, w, counts, offsets, perm, inv, blk_base, counters,
-      counters_s, xperm,
-      act_r, act_s, y, touched, gmask, total;
-  // the few-token layer: its counters, and for T <= kFewMaxT its scratch
-  size_t f_claim, f_route, f_slots, f_w, f_mask, f_hq, f_hqe, f_act, f_exp, f_planes;
+  // zero between calls, at the same place for every T
+  size_t status, ticket, f_claim, counters_d, counters_s, gmask;
+  size_t partials, wr3, idx, w, counts, offsets, perm, inv, blk_base, counters, xperm, act_r, act_s,
+      y, touched, total;
+  // the few-token layer's scratch, for T <= kFewMaxT
+  size_t f_route, f_slots, f_w, f_mask, f_hq, f_hqe, f_act, f_exp, f_planes;
 };
 bool ws_layout(const moe_dims_t& d, WsLayout* out);
 
