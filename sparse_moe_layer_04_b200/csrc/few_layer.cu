@@ -1016,11 +1016,24 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
         const int f = u.at + qt * 16 + (lane & 15);
         const size_t row0 = (size_t)(sh ? u.slot : u.slot - p.S) * p.PA;
         // lanes 0-15 finish the even tokens, lanes 16-31 the odd ones
+        float act[8];
+        auto gates = [&](auto&& silu) {
+#pragma unroll
+          for (int t = 0; t < 16; t += 2) {
+            const float got = __shfl_xor_sync(kAll, up ? v[t] : v[t + 1], 16);
+            act[t / 2] = silu(t + (up ? 1 : 0), up ? got : v[t], up ? v[t + 1] : got);
+          }
+        };
+        float least = 0.f;               // of the gates that count
+        gates([&](int tt, float g, float u) {
+          if ((mask >> tt) & 1u) least = fminf(least, g);
+          return ffn::silu_times_near<true>(g, u);
+        });
+        if (__any_sync(kAll, least < ffn::kGateFar))
+          gates([](int, float g, float u) { return ffn::silu_times_wide<true>(g, u); });
 #pragma unroll
         for (int t = 0; t < 16; t += 2) {
-          const float got = __shfl_xor_sync(kAll, up ? v[t] : v[t + 1], 16);
-          const float gate = up ? got : v[t], mul = up ? v[t + 1] : got;
-          const float a = f < F ? ffn::silu_times_wide<true>(gate, mul) : 0.f;
+          const float a = f < F ? act[t / 2] : 0.f;
           const int tt = t + (up ? 1 : 0);
           if (FP8) {
             ss.act[turn][(qt * 16 + (lane & 15)) * 17 + tt] = a;
