@@ -82,9 +82,12 @@ typedef enum moe_status {
   MOE_ERR_BOUNDS = -7        /* device: index/offset out of range or repeated */
 } moe_status_t;
 
-/* Bytes of workspace that moe_forward needs for `dims` (a superset of what
- * every other entry point needs).  The workspace must be 256-byte aligned.
- * Returns 0 if the dimensions are invalid. */
+/* Bytes of workspace for `dims`: what moe_forward, moe_forward_few and every
+ * other entry point need for this layer with dims->T tokens or fewer.  One
+ * workspace of this size serves calls of them all, in any order, as long as
+ * they do not overlap on the GPU.  (A call asks only for what it needs itself:
+ * moe_forward for fewer tokens accepts a smaller one.)  The workspace must be
+ * 256-byte aligned.  Returns 0 if the dimensions are invalid. */
 size_t moe_workspace_size(const moe_dims_t* dims);
 
 /* Router logits ("Routing: learned", MoE panel; fp32 router):
@@ -285,8 +288,8 @@ int moe_forward_fp8(const void* h, const float* Wr, const float* bias, const moe
  * with its 24 significant bits instead of 8.  Capturable in a CUDA graph; no internal
  * stream.  moe_ws_expert_counts and moe_ws_touched_experts hold for it too.
  * Repeated calls give identical bits.  Calls that share a workspace must not
- * overlap on the GPU; one workspace sized for the largest T may serve calls of
- * this layer with any T (and with either kind of weights). */
+ * overlap on the GPU; one workspace sized for the largest T serves calls of this
+ * layer with any T, those of moe_forward and moe_forward_fp8 among them. */
 int moe_forward_few(const void* h, const float* Wr, const float* bias, const void* W1,
                     const void* W3, const void* W2, const void* Ws1, const void* Ws3,
                     const void* Ws2, const moe_dims_t* dims, float* out, int32_t* idx_out,

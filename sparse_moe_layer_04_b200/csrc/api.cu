@@ -94,8 +94,9 @@ struct Ws {
   int* status() const { return base ? reinterpret_cast<int*>(base + L.status) : nullptr; }
 };
 
-int check_ws(const moe_dims_t* d, void* ws, size_t ws_bytes, Ws* out) {
+int check_ws(const moe_dims_t* d, void* ws, size_t ws_bytes, Ws* out, bool few = false) {
   if (!ws_layout(*d, &out->L)) return fail(MOE_ERR_INVALID_ARG, "workspace layout overflow");
+  if (few) few_layout(*d, &out->L);
   if (!ws) return fail(MOE_ERR_WORKSPACE, "workspace is NULL");
   if (reinterpret_cast<uintptr_t>(ws) & 255u)
     return fail(MOE_ERR_WORKSPACE, "workspace is not 256-byte aligned");
@@ -178,11 +179,13 @@ bool ws_layout(const moe_dims_t& d, WsLayout* L) {
   L->counters_d = take((E + S + 2) * 4);
   L->counters_s = take((S + 2) * 4);
   L->gmask = take(E * (kPermBlockTokens / 32) * 4);
-  L->partials = take((size_t)sp.nsplit * T * E * 4);
-  L->wr3 = take(sp.tensor && !sp.fused ? E * 3 * D * 2 : 0);
   L->idx = take(T * k * 4);
   L->w = take(T * k * 4);
   L->counts = take(E * 4);
+  L->touched = take(4);
+  L->scratch = off;
+  L->partials = take((size_t)sp.nsplit * T * E * 4);
+  L->wr3 = take(sp.tensor && !sp.fused ? E * 3 * D * 2 : 0);
   L->offsets = take((E + 1) * 4);
   L->perm = take(T * k * 4);
   L->inv = take(T * k * 4);
@@ -193,31 +196,61 @@ bool ws_layout(const moe_dims_t& d, WsLayout* L) {
   L->act_r = take(T * k * F * 2);
   L->act_s = take(S * T * Fs * 2);
   L->y = take((T * k + S * T) * D * 4);
-  L->touched = take(4);
-  L->f_route = L->f_slots = L->f_w = L->f_mask = L->f_hq = L->f_hqe = L->f_act = L->f_exp = L->f_planes = 0;
-  if (T > 0 && T <= (size_t)kFewMaxT) {
-    const FewPlan p16 = few_plan(d, false), p8 = few_plan(d, true);
-    const size_t slots = p16.max_slots, most = slots - S;
-    // bytes of the activations (bf16 or codes) and of their exponents
-    const size_t act = std::max((most * F + S * Fs) * p16.PA * 2 + 16,
-                                (most * F + S * Fs) * p8.PA + 16) + 256;
-    const size_t ex = (most * ((F + 127) / 128) + S * ((Fs + 127) / 128)) * 4 * T + 256;
-    // planes of the down products: few_plan splits K only while all the parts
-    // of all units are at most kSplitTargetBlocks, so the bound grows with T and
-    // a workspace serves every smaller T
-    const size_t planes = std::max(slots, (size_t)kSplitTargetBlocks / p16.nd);
-    L->f_route = take(2 * T * E * 4);
-    L->f_slots = take((64 + T * k + slots) * 4);
-    L->f_w = take(slots * kFewMaxT * 4);
-    L->f_mask = take(slots * 4);
-    L->f_hq = take(3 * T * D);
-    L->f_hqe = take(T * ((D + 127) / 128));
-    L->f_act = take(act);
-    L->f_exp = take(ex);
-    L->f_planes = take(planes * T * D * 4);
-  }
   L->total = off;
   return true;
+}
+
+// The few-token layer's scratch, which takes the place of the others' (T in [1,
+// kFewMaxT]); `total` becomes what its calls need.
+void few_layout(const moe_dims_t& d, WsLayout* L) {
+  const size_t T = d.T, D = d.D, E = d.E, F = d.F, k = d.k, S = d.S, Fs = d.S > 0 ? d.Fs : 0;
+  const FewPlan p16 = few_plan(d, false), p8 = few_plan(d, true);
+  const size_t slots = p16.max_slots, pairs = T * k, shared = S * T;
+  size_t off = L->scratch;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = align256(off + bytes);
+    return at;
+  };
+  // activations of the chosen and the shared experts, in bf16 pieces or E4M3 codes,
+  // and the codes' exponents
+  auto act = [&](const FewPlan& p, size_t es) {
+    return align256(pairs * p.pieces_a * F * es) + shared * p.pieces_a * Fs * es;
+  };
+  L->f_route = take(2 * T * E * 4);
+  L->f_slots = take((64 + pairs + slots) * 4);
+  L->f_w = take(pairs * 4);
+  L->f_mask = take(slots * 4);
+  L->f_hq = take(p8.pieces_h * T * D);
+  L->f_hqe = take(T * ((D + 127) / 128));
+  L->f_act = take(std::max(act(p16, 2), act(p8, 1)));
+  L->f_exp = take((pairs * ((F + 127) / 128) + shared * ((Fs + 127) / 128)) * 4);
+  L->f_rows = take(std::max(p16.parts, p8.parts) * (pairs + shared) * D * 4);
+  L->total = std::max(L->total, off);
+}
+
+// Bytes that serve calls of this layer with any number of tokens up to d.T.
+size_t ws_size(const moe_dims_t& d) {
+  WsLayout L;
+  auto need = [&](int T, bool few) {
+    moe_dims_t t = d;
+    t.T = T;
+    ws_layout(t, &L);
+    if (few) few_layout(t, &L);
+    return L.total;
+  };
+  // The layout grows with T but for the router's partial sums, whose cut changes
+  // at multiples of 64 tokens alone.  Above 256 tokens they are never more than
+  // (128 * kSplitTargetBlocks + T) x E, so the search downwards soon ends.
+  size_t most = need(d.T, false);
+  for (int T = 64; T <= 256 && T < d.T; T += 64) most = std::max(most, need(T, false));
+  for (int T = (d.T - 1) / 64 * 64; T > 256; T -= 64) {
+    const size_t n = need(T, false);
+    most = std::max(most, n);
+    if (n + ((size_t)128 * kSplitTargetBlocks + T) * d.E * 4 <= most) break;
+  }
+  for (int T = 1; T <= std::min(d.T, kFewMaxT); ++T) most = std::max(most, need(T, true));
+  return most;
 }
 
 namespace {
@@ -543,10 +576,10 @@ int forward_few_impl(const void* h, const float* Wr, const float* bias, const Ex
   if (w_out && !aligned16(w_out)) return fail(MOE_ERR_INVALID_ARG, "w_out is not 16-byte aligned");
   Ws w;
   int rc;
-  if ((rc = check_ws(dims, ws, ws_bytes, &w))) return rc;
+  if ((rc = check_ws(dims, ws, ws_bytes, &w, true))) return rc;
   if ((rc = check_device())) return rc;
   const FewPlan L = few_plan(*dims, wt.fp8);
-  const size_t most = L.max_slots - dims->S;
+  const size_t pairs = (size_t)dims->T * dims->k;
   FewArgs a{};
   a.d = *dims;
   a.h = static_cast<const uint16_t*>(h);
@@ -562,10 +595,10 @@ int forward_few_impl(const void* h, const float* Wr, const float* bias, const Ex
   a.order = w.at<uint32_t>(w.L.f_route) + (size_t)dims->T * dims->E;
   int32_t* slots = w.at<int32_t>(w.L.f_slots);
   a.nslots = slots;
-  a.slot_of = slots + 64;
-  a.slot_expert = a.slot_of + dims->T * dims->k;
+  a.pair_of = slots + 64;
+  a.slot_expert = a.pair_of + pairs;
   a.slot_mask = w.at<uint32_t>(w.L.f_mask);
-  a.slot_w = w.at<float>(w.L.f_w);
+  a.pair_w = w.at<float>(w.L.f_w);
   a.counts = w.at<int32_t>(w.L.counts);
   a.touched = w.at<int32_t>(w.L.touched);
   a.ticket = w.at<int32_t>(w.L.f_claim);
@@ -574,10 +607,10 @@ int forward_few_impl(const void* h, const float* Wr, const float* bias, const Ex
   a.hqe = w.at<int8_t>(w.L.f_hqe);
   // chosen experts' activations first, then the shared experts'
   a.a_r = w.at<uint8_t>(w.L.f_act);
-  a.a_s = a.a_r + align256(most * L.PA * dims->F * (wt.fp8 ? 1 : 2));
+  a.a_s = a.a_r + align256(pairs * L.pieces_a * dims->F * (wt.fp8 ? 1 : 2));
   a.ae_r = w.at<int8_t>(w.L.f_exp);
-  a.ae_s = a.ae_r + most * (size_t)dims->T * 4 * ((dims->F + 127) / 128);
-  a.planes = w.at<float>(w.L.f_planes);
+  a.ae_s = a.ae_r + pairs * 4 * ((dims->F + 127) / 128);
+  a.rows = w.at<float>(w.L.f_rows);
   a.status = w.status();
   const char* why = "launch failed";
   const cudaError_t e = launch_few(a, reinterpret_cast<cudaStream_t>(stream), &why);
@@ -683,9 +716,7 @@ extern "C" {
 
 size_t moe_workspace_size(const moe_dims_t* dims) {
   if (check_dims(dims) != MOE_OK) return 0;
-  WsLayout L;
-  ws_layout(*dims, &L);
-  return L.total;
+  return ws_size(*dims);
 }
 
 const char* moe_last_error(void) { return g_err.c_str(); }

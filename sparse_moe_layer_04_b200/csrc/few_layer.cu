@@ -14,10 +14,12 @@
 //     gate/up  (slot, up to 64 features): act = silu(W1 h) * (W3 h) for every
 //              token, kept for the tokens that chose the expert
 //     down     (slots, 128 output rows, part of K): y = W2 act of one slot, or
-//              of a few when the experts are narrow, weighted and added, written
-//              to a plane of its own; whoever completes the last plane of 128
-//              output rows adds the planes, shared experts first, then in the
-//              order of the token's choices
+//              of a few in turn when the experts are narrow, weighted, a row
+//              for each token that chose it; whoever completes the last unit of
+//              128 output rows adds each token's rows, shared experts first, then
+//              in the order of its choices
+// Activations and results are held for (token, choice) pairs alone, ordered by
+// slot and then by token; a slot's word of tokens says where its pairs start.
 // The shared experts' gate/up tiles need no routing, so this kernel starts on
 // them while the first one runs (programmatic dependent launch).
 //
@@ -74,10 +76,10 @@ struct FewRoute {
   uint32_t* order;        // [T, E] the keys' order
   int32_t* idx;           // [T, k]
   float* w;               // [T, k]
-  int32_t* slot_of;       // [T, k] chosen-expert slot of each pair, -1 for none
-  float* slot_w;          // [slots][kFewMaxT] weight of a slot for each token that chose it
+  int32_t* pair_of;       // [T, k] pair of each choice, -1 for none
+  float* pair_w;          // [pairs] weight
   int32_t* slot_expert;   // [slots]
-  uint32_t* slot_mask;    // [slots] bit t: token t chose it
+  uint32_t* slot_mask;    // [slots] bit t: token t chose it; its first pair from bit 16 on
   int32_t* nslots;        // chosen experts
   int32_t* counts;        // [E] pairs per expert
   int32_t* ticket;        // zero between calls
@@ -212,16 +214,16 @@ __device__ __forceinline__ void router_block(const FewRoute& p, float* s_part) {
   if (bad && p.status) atomicOr(p.status, kStNonFinite);
 }
 
-// Shared memory of the selection: the experts' token masks and slots (E
+// Shared memory of the selection: the experts' token masks and first pairs (E
 // rounded up to 32 each), then the keys' order [T][E].
 __host__ __device__ constexpr int select_words(int T, int E) { return 2 * ((E + 31) / 32 * 32) + T * E; }
 
 // Selection for every token (a warp each), then the slots.  One block.
 __device__ void select_and_list(const FewRoute& p, uint32_t* smem) {
-  __shared__ int s_cnt[32];
+  __shared__ int s_cnt[32], s_pairs[32];   // slots and pairs of 32 experts
   const int EP = (p.E + 31) / 32 * 32, groups = EP / 32;
   uint32_t* s_mask = smem;
-  int* s_slot = reinterpret_cast<int*>(smem + EP);
+  int* s_first = reinterpret_cast<int*>(smem + EP);
   uint32_t* s_ord = smem + 2 * EP;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int e = threadIdx.x; e < EP; e += kRouterThreads) s_mask[e] = 0u;
@@ -258,30 +260,48 @@ __device__ void select_and_list(const FewRoute& p, uint32_t* smem) {
   }
   __syncthreads();
   for (int g = warp; g < groups; g += kRouterWarps) {
-    const unsigned b = __ballot_sync(kAll, s_mask[g * 32 + lane] != 0u);
-    if (lane == 0) s_cnt[g] = __popc(b);
+    const uint32_t m = s_mask[g * 32 + lane];
+    const unsigned b = __ballot_sync(kAll, m != 0u);
+    const int pairs = __reduce_add_sync(kAll, __popc(m));
+    if (lane == 0) {
+      s_cnt[g] = __popc(b);
+      s_pairs[g] = pairs;
+    }
   }
   __syncthreads();
   for (int g = warp; g < groups; g += kRouterWarps) {
     const int e = g * 32 + lane;
     const uint32_t m = s_mask[e];
     const unsigned b = __ballot_sync(kAll, m != 0u);
-    int base = 0;
-    for (int q = 0; q < g; ++q) base += s_cnt[q];
+    int base = 0, first = 0;
+    for (int q = 0; q < g; ++q) {
+      base += s_cnt[q];
+      first += s_pairs[q];
+    }
     const int slot = base + __popc(b & ((1u << lane) - 1u));
-    s_slot[e] = slot;
+    int upto = __popc(m);                // pairs of this group's experts up to this one
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(kAll, upto, o);
+      if (lane >= o) upto += v;
+    }
+    first += upto - __popc(m);
+    s_first[e] = first;
     if (m) {
       p.slot_expert[slot] = e;
-      p.slot_mask[slot] = m;
+      p.slot_mask[slot] = (uint32_t)first << 16 | m;
     }
     if (e < p.E) p.counts[e] = __popc(m);
     if (g == groups - 1 && lane == 31) *p.nslots = slot + (m != 0u);
   }
   __syncthreads();
   if (t < p.T && lane < p.k) {
-    const int slot = my_e != INT_MAX ? s_slot[my_e] : -1;
-    p.slot_of[t * p.k + lane] = slot;
-    if (slot >= 0) p.slot_w[slot * kFewMaxT + t] = my_w;
+    int pair = -1;
+    if (my_e != INT_MAX) {
+      pair = s_first[my_e] + __popc(s_mask[my_e] & ((1u << t) - 1u));
+      p.pair_w[pair] = my_w;
+    }
+    p.pair_of[t * p.k + lane] = pair;
   }
 }
 
@@ -375,7 +395,7 @@ constexpr int kQueue = 4;
 
 struct alignas(64) FewFfn {
   CUtensorMap x;                         // hidden rows (bf16) or their pieces, box NX x 128 B
-  CUtensorMap act_r, act_s;              // activations [slots * PA, F], box PA x 128 B
+  CUtensorMap act_r, act_s;              // activations [pairs * pieces, F], box 16 x 128 B
   CUtensorMap w1_r, w3_r, w1_s, w3_s;    // [E * F, D], box 16 rows
   CUtensorMap w2_r, w2_s;                // [E * D, F], box 128 rows
   const int8_t *e1_r, *e3_r, *e2_r, *e1_s, *e3_s, *e2_s;
@@ -391,14 +411,15 @@ struct alignas(64) FewFfn {
   int spu_r, spu_s;      // slots of a down unit: chosen, shared
   int ngs;               // shared groups of slots (units per output block and part)
   // routing (written by the first kernel)
-  const int32_t *slot_of, *slot_expert, *nslots;
+  const int32_t *pair_of, *slot_expert, *nslots;
   const uint32_t* slot_mask;
-  const float* slot_w;
+  const float* pair_w;
   const int8_t* hqe;     // FP8: exponents of the hidden rows [T, KB]
-  // activations, their exponents (FP8: one per 32 features, [slots, T, 4 * KB])
+  // activations: a slot's pairs by piece, [pieces][its pairs] rows from row pieces *
+  // (its first pair) on; their exponents (FP8: one per 32 features, [pairs, 4 * KB])
   uint8_t *a_r, *a_s;
   int8_t *ae_r, *ae_s;
-  float* planes;         // [group * parts + part][T][D]
+  float* rows;           // [part][S * T + pairs][D]: the shared experts' results, then the pairs'
   float* out;
   int32_t* claim;        // claim counter, exit ticket, blocks of pieces written, then
                          // per-slot counts, then per-output-block tickets; zero
@@ -414,11 +435,11 @@ struct Unit {
   int at;                // first feature, or output block
   int part;
   int expert;            // row of the weight arrays
-  uint32_t mask;         // tokens that chose it
-  // down units of several slots come one slot at a time: 1 the first, 2 the last
-  int ends;
-  int plane;
+  uint32_t mask;         // its tokens and first pair, as slot_mask; shared: slot * T
+  int last;              // down units of several slots come one slot at a time
 };
+__device__ __forceinline__ uint32_t unit_tokens(const Unit& u) { return u.mask & 0xffffu; }
+__device__ __forceinline__ int unit_first(const Unit& u) { return (int)(u.mask >> 16); }
 
 struct FewShared {
   uint64_t full[kAStages], empty[kAStages];   // a stage's weights and tokens; its products done
@@ -432,8 +453,7 @@ struct FewShared {
   int abort, bad, last, exit_last;
   int act_done[4];       // gate/up tiles whose part each epilogue warp has stored
   float act[2][64 * 17]; // FP8: activations of a tile [feature][token], by turns
-  int tab[kFewMaxT * 32];        // the tokens' choices: their group of slots, -1 where an
-                                 // earlier choice has it too (or there is none)
+  int tab[kFewMaxT * 32];        // the tokens' choices: their row of a part, -1 for none
 };
 
 constexpr int few_smem() { return 1024 + kRing + (int)sizeof(FewShared); }
@@ -445,7 +465,7 @@ struct QueueReader {
   __device__ __forceinline__ bool next(FewShared& ss, Unit& u, volatile int* abort, int lane) {
     if (__any_sync(kAll, !ptx::mbar_wait(&ss.q_full[slot], phase, abort))) return false;
     const volatile Unit& q = ss.q[slot];
-    u.down = q.down; u.slot = q.slot; u.at = q.at; u.part = q.part; u.expert = q.expert; u.mask = q.mask; u.ends = q.ends; u.plane = q.plane;
+    u.down = q.down; u.slot = q.slot; u.at = q.at; u.part = q.part; u.expert = q.expert; u.mask = q.mask; u.last = q.last;
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive_after_reads(&ss.q_empty[slot]);
     if (++slot == kQueue) { slot = 0; phase ^= 1u; }
@@ -521,18 +541,18 @@ struct RawScales {
   }
 };
 
-// out for 128 columns, from the planes: shared groups, then the groups of the
-// token's choices in their order.  Four groups of 32 threads take every fourth
+// out for 128 columns, from the rows: shared experts, then the token's choices in
+// their order.  Four groups of 32 threads take every fourth
 // token, a thread four columns; kMergeLoads loads are in flight before the
 // first is added.
 constexpr int kMergeLoads = 8;
 __device__ __forceinline__ void merge_block(const FewFfn& p, const FewShared& ss, int at, int tid) {
   const int d = at * 128 + (tid & 31) * 4;
   if (d >= p.D) return;
-  const size_t plane = (size_t)p.T * p.D;
-  // this thread's terms: its tokens one after the other, each token's groups,
-  // each group's K parts
-  const int n = (p.ngs + p.k) * p.parts;
+  const size_t part_rows = (size_t)(p.S + p.k) * p.T;
+  // this thread's terms: its tokens one after the other, each token's experts,
+  // each expert's K parts
+  const int n = (p.S + p.k) * p.parts;
   const int total = (p.T - (tid >> 5) + 3) / 4 * n;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   int lt = tid >> 5, lj = 0, lpart = 0;  // the term being loaded
@@ -543,13 +563,13 @@ __device__ __forceinline__ void merge_block(const FewFfn& p, const FewShared& ss
     for (int i = 0; i < kMergeLoads; ++i) {
       r[i] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (i0 + i < total) {
-        const int g = lj < p.ngs ? lj : ss.tab[lt * p.k + lj - p.ngs];
-        if (g >= 0)
+        const int row = lj < p.S ? lj * p.T + lt : ss.tab[lt * p.k + lj - p.S];
+        if (row >= 0)
           r[i] = __ldcg(reinterpret_cast<const float4*>(
-              p.planes + ((size_t)g * p.parts + lpart) * plane + (size_t)lt * p.D + d));
+              p.rows + (lpart * part_rows + row) * p.D + d));
         if (++lpart == p.parts) {
           lpart = 0;
-          if (++lj == p.ngs + p.k) { lj = 0; lt += 4; }
+          if (++lj == p.S + p.k) { lj = 0; lt += 4; }
         }
       }
     }
@@ -621,12 +641,14 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
       uint32_t phase = 0, qphase = 0, issued = 0, parity = 0;
       int tile = atomicAdd(p.claim, 1);
       for (;;) {
-        Unit u{0, 0, 0, 0, 0, (1u << p.T) - 1u, 3, 0};
+        const uint32_t all = (1u << p.T) - 1u;
+        Unit u{0, 0, 0, 0, 0, all, 1};
         int slots = 1;                   // of a down unit
         if (tile < shared_tiles) {
           u.slot = tile / p.nts;
           u.at = (tile - u.slot * p.nts) * p.fpt_s;
           u.expert = u.slot;
+          u.mask = (uint32_t)(u.slot * p.T) << 16 | all;
         } else {
           const bool fresh = routed < 0;
           if (fresh) ptx::pdl_wait();    // the list of chosen experts
@@ -648,7 +670,6 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
             u.down = g < groups ? 1 : -1;
             u.part = r / p.nd;
             u.at = r - u.part * p.nd;
-            u.plane = g * p.parts + u.part;
             if (g < p.ngs) {
               u.slot = g * p.spu_s;
               slots = min(p.spu_s, p.S - u.slot);
@@ -661,13 +682,14 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
                 mask = __ldcg(p.slot_mask + first);
               }
             }
-            u.ends = slots > 1 ? 1 : 3;
+            u.last = slots <= 1;
           }
           if (u.slot >= p.S) {
             u.expert = expert;
             u.mask = mask;
           } else {
             u.expert = u.slot;
+            u.mask = (uint32_t)(u.slot * p.T) << 16 | all;
           }
         }
         if (!ptx::mbar_wait(&ss.q_empty[qs], qphase ^ 1u, abort)) break;
@@ -687,9 +709,10 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
             Unit v = u;
             if (--slots > 0) {
               ++v.slot;
-              v.ends = slots > 1 ? 0 : 2;
+              v.last = slots <= 1;
               if (sh) {
                 v.expert = v.slot;
+                v.mask = (uint32_t)(v.slot * p.T) << 16 | all;
               } else {
                 v.expert = __ldcg(p.slot_expert + v.slot - p.S);
                 v.mask = __ldcg(p.slot_mask + v.slot - p.S);
@@ -765,8 +788,12 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
       int k0, k1;
       unit_k<EB>(p, u, &k0, &k1);
       const CUtensorMap* m = u.down ? (sh ? &p.act_s : &p.act_r) : &p.x;
-      const int row = u.down ? (sh ? u.slot : u.slot - p.S) * p.PA : 0;
-      const int bytes = (u.down ? p.PA : p.NX) * 128;
+      // down: as many boxes of 16 rows as the slot's pieces fill (what else they
+      // hold, and the stage behind them, are columns that nobody reads)
+      constexpr int pieces_a = FP8 ? kPiecesA : kPiecesB;
+      const int row = u.down ? unit_first(u) * pieces_a : 0;
+      const int boxes = u.down ? (__popc(unit_tokens(u)) * pieces_a + 15) / 16 : 1;
+      const int bytes = u.down ? boxes * 2048 : p.NX * 128;
       const int sub = u.down ? 1 : sh ? p.sub_s : p.sub_r;
       bool ok = true;
       if (ptx::elect_one()) {
@@ -779,9 +806,14 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
           }
           const int n = min(sub, k1 - kb);
           ptx::mbar_arrive_expect_tx(&ss.full[stage], n * bytes);
-          for (int i = 0; i < n; ++i)
-            ptx::tma_load_2d(ring_b + own * kBStage + i * bytes, m, &ss.full[stage], (kb + i) * EB,
-                             row);
+          uint8_t* dst = ring_b + own * kBStage;
+          if (u.down) {
+            for (int i = 0; i < boxes; ++i)
+              ptx::tma_load_2d(dst + i * 2048, m, &ss.full[stage], kb * EB, row + i * 16);
+          } else {
+            for (int i = 0; i < n; ++i)
+              ptx::tma_load_2d(dst + i * bytes, m, &ss.full[stage], (kb + i) * EB, 0);
+          }
           if (++own == kBStages) own = 0;
           issued |= 1u << stage;
           parity = (parity & ~(1u << stage)) | (phase << stage);
@@ -917,21 +949,18 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
     ptx::WarpBarrier epi{&ss.epi};
     bool waited = false;
     int buf = 0, turn = 0, tiles = 0;
-    uint32_t cph = 0, omask = 0;
-    float o[16];                         // a down unit's sum over its slots, per token
-#pragma unroll
-    for (int t = 0; t < 16; ++t) o[t] = 0.f;
+    uint32_t cph = 0;
     // The ticket of a down unit is looked at with the next one, so that its round
     // trip passes under that one's products: lane 0 of the first warp holds
     // its number, and `last_at` is the output block it stands for (-1: none).
-    int ticket = 0, last_at = -1, planes = 0;
-    // All four warps; after this unit's planes are stored, or at the end: merges
-    // the block of the unit before if that was its last plane, then takes this
-    // unit's ticket.  The barrier orders the four warps' plane stores before
-    // lane 0's ticket, whose release makes them visible to the whole GPU.
+    int ticket = 0, last_at = -1, units = 0;
+    // All four warps; after this unit's rows are stored, or at the end: merges the
+    // block of the unit before if that was its last unit, then takes this unit's
+    // ticket.  The barrier orders the four warps' stores before lane 0's ticket,
+    // whose release makes them visible to the whole GPU.
     auto settle = [&](int at) {
       if (qt == 0 && lane == 0) {
-        ss.last = last_at >= 0 && ticket == planes - 1;
+        ss.last = last_at >= 0 && ticket == units - 1;
         if (ss.last) *out_ticket(p, last_at) = 0;
       }
       if (!epi.sync(abort, lane)) return false;
@@ -950,28 +979,24 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
       if (!waited && (u.down || !sh)) {
         ptx::pdl_wait();
         waited = true;
-        planes = (p.ngs + (__ldcg(p.nslots) + p.spu_r - 1) / p.spu_r) * p.parts;
+        units = (p.ngs + (__ldcg(p.nslots) + p.spu_r - 1) / p.spu_r) * p.parts;
         // (read after a barrier of all four warps, in settle)
         for (int i = threadIdx.x - 128; i < p.T * p.k; i += 128) {
-          const int s = __ldcg(p.slot_of + i), g = s / p.spu_r, first = i / p.k * p.k;
-          bool have = s >= 0;
-          if (p.spu_r > 1)
-            for (int j = first; j < i; ++j) {
-              const int o = __ldcg(p.slot_of + j);
-              if (o >= 0 && o / p.spu_r == g) have = false;
-            }
-          ss.tab[i] = have ? p.ngs + g : -1;
+          const int pair = __ldcg(p.pair_of + i);
+          ss.tab[i] = pair >= 0 ? p.S * p.T + pair : -1;
         }
       }
-      const uint32_t mask = u.mask;
-      // a down unit's weights: lane t has token t's
+      const uint32_t mask = unit_tokens(u);
+      const int first = unit_first(u), cnt = __popc(mask);
+      // a down unit's weights: lane i has its pair's
       float wl = 1.f;
-      if (u.down && !sh && lane < kFewMaxT) wl = __ldcg(p.slot_w + (u.slot - p.S) * kFewMaxT + lane);
+      if (u.down && !sh && lane < cnt) wl = __ldcg(p.pair_w + first + lane);
       int k0, k1;
       unit_k<EB>(p, u, &k0, &k1);
-      // the token columns, pieces and accumulators added: v[t] is this lane's
-      // weight row
+      // the columns, pieces and accumulators added: v[i] is this lane's weight row
+      // and token i (gate/up), or the slot's pair i (down)
       const int pieces = u.down ? (FP8 ? kPiecesA : kPiecesB) : (FP8 ? kPiecesH : 1);
+      const int per = u.down ? cnt : p.T;
       const int n = u.down ? p.PA : p.NX;
       const int fpt = sh ? p.fpt_s : p.fpt_r;
       const bool rows = u.down || qt * 16 < fpt;     // this warp's rows belong to the tile
@@ -992,7 +1017,7 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
           uint32_t r[4][16];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            if (i0 + i < reads) ptx::tmem_ld_x16(acc + a * n + c * p.T, r[i]);
+            if (i0 + i < reads) ptx::tmem_ld_x16(acc + a * n + c * per, r[i]);
             if (++a == nacc) { a = 0; --c; }
           }
           ptx::tmem_wait_ld();
@@ -1014,7 +1039,7 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
         const int F = sh ? p.Fs : p.F;
         const bool up = lane >= 16;
         const int f = u.at + qt * 16 + (lane & 15);
-        const size_t row0 = (size_t)(sh ? u.slot : u.slot - p.S) * p.PA;
+        const size_t row0 = (size_t)first * (FP8 ? kPiecesA : kPiecesB);
         // lanes 0-15 finish the even tokens, lanes 16-31 the odd ones
         float act[8];
         auto gates = [&](auto&& silu) {
@@ -1039,12 +1064,12 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
             ss.act[turn][(qt * 16 + (lane & 15)) * 17 + tt] = a;
           } else if (rows && f < F && ((mask >> tt) & 1u)) {
             __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(sh ? p.a_s : p.a_r) +
-                                 (row0 + tt) * F + f;
+                                 (row0 + __popc(mask & ((1u << tt) - 1u))) * F + f;
             float rest = a;
 #pragma unroll
             for (int c = 0; c < kPiecesB; ++c) {
               const __nv_bfloat16 piece = __float2bfloat16_rn(rest);
-              dst[(size_t)c * p.T * F] = piece;
+              dst[(size_t)c * cnt * F] = piece;
               // an infinite piece is all there is
               rest = __hisinf(piece) ? 0.f : rest - __bfloat162float(piece);
             }
@@ -1058,6 +1083,7 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
           for (int i = qt; i < p.T * (fpt / 32); i += 4) {
             const int t = i % p.T, b = i / p.T;
             if (!((mask >> t) & 1u)) continue;
+            const int at = __popc(mask & ((1u << t) - 1u));   // among the slot's pairs
             float a = ss.act[turn][(b * 32 + lane) * 17 + t];
             const bool odd = !isfinite(a);
             if (odd) a = 0.f;
@@ -1066,12 +1092,12 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
             const int fb = u.at + b * 32;
             if (fb >= F) continue;
             if (lane == 0)
-              ae[((size_t)(sh ? u.slot : u.slot - p.S) * p.T + t) * stride + fb / 32] = (int8_t)e;
-            uint8_t* dst = (sh ? p.a_s : p.a_r) + (row0 + t) * F + fb + lane;
+              ae[(size_t)(first + at) * stride + fb / 32] = (int8_t)e;
+            uint8_t* dst = (sh ? p.a_s : p.a_r) + (row0 + at) * F + fb + lane;
 #pragma unroll
             for (int c = 0; c < kPiecesA; ++c) {
               const uint32_t code = piece_code(a, pow2f(4 * c - e), pow2f(e - 4 * c));
-              if (fb + lane < F) dst[(size_t)c * p.T * F] = (uint8_t)(odd ? 0x7fu : code);
+              if (fb + lane < F) dst[(size_t)c * cnt * F] = (uint8_t)(odd ? 0x7fu : code);
             }
           }
           // the next tile writes the other half; a warp that comes back to this
@@ -1087,25 +1113,15 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
         }
       } else {
         const int d = u.at * 128 + qt * 32 + lane;
-        if (u.ends & 1) {
+        const size_t row0 = (size_t)u.part * (p.S + p.k) * p.T + (sh ? 0 : p.S * p.T) + first;
+        float* dst = p.rows + row0 * p.D + d;
 #pragma unroll
-          for (int t = 0; t < 16; ++t) o[t] = 0.f;
-          omask = 0;
+        for (int i = 0; i < 16; ++i) {
+          if (i >= cnt) break;           // (mostly one or two)
+          const float c = __shfl_sync(kAll, wl, i);
+          if (d < p.D) dst[(size_t)i * p.D] = c * v[i];
         }
-        omask |= mask;
-#pragma unroll
-        for (int t = 0; t < 16; ++t) {
-          const float c = __shfl_sync(kAll, wl, t);
-          // (what the slot made of other tokens is left out, whatever it is)
-          if ((mask >> t) & 1u) o[t] = fmaf(c, v[t], o[t]);
-        }
-        if (!(u.ends & 2)) continue;
-        float* plane = p.planes + (size_t)u.plane * p.T * p.D + d;
-        if (d < p.D) {
-#pragma unroll
-          for (int t = 0; t < 16; ++t)
-            if ((omask >> t) & 1u) plane[(size_t)t * p.D] = o[t];
-        }
+        if (!u.last) continue;
         if (!settle(u.at)) break;
       }
     }
@@ -1114,9 +1130,6 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
     // ---------------- scale writers ----------------
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const int KBD = (p.D + 127) / 128;
-    // the piece and token of this lane's two rows of the token operand
-    const int row_c[2] = {lane / p.T, (32 + lane) / p.T};
-    const int row_t[2] = {lane % p.T, (32 + lane) % p.T};
     QueueReader q;
     Unit u;
     bool pieces = false, bad = false;
@@ -1141,8 +1154,14 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
       const int8_t* we = we0 + (u.down ? (size_t)u.expert * KBD + u.at
                                        : (size_t)u.expert * KBF + u.at / 128) * KB;
       const bool inside = ptx::words_inside(we, KB, we0, we_end);
-      const int8_t* ae = (sh ? p.ae_s : p.ae_r) +
-                         (size_t)(sh ? u.slot : u.slot - p.S) * p.T * (KBF * 4);
+      const int8_t* ae = (sh ? p.ae_s : p.ae_r) + (size_t)unit_first(u) * (KBF * 4);
+      // the piece and token (gate/up) or pair (down) of this lane's two rows of the
+      // token operand
+      // (row + 1/2) / per is at least 1/32 away from every whole number
+      const int per = u.down ? __popc(unit_tokens(u)) : p.T;
+      const float inv = __fdividef(1.0f, (float)per);
+      const int row_c[2] = {(int)((lane + 0.5f) * inv), (int)((lane + 32.5f) * inv)};
+      const int row_t[2] = {lane - row_c[0] * per, 32 + lane - row_c[1] * per};
       // Token words: gate/up, one per row (the bytes are K-blocks); down, one per
       // row and K-block (the bytes are its steps of 32, and a row's exponents
       // start on four bytes).  A set's words are loaded while the one before it
@@ -1256,8 +1275,10 @@ cudaError_t launch_few_router(FewRoute& r, int hq_blocks, cudaStream_t st) {
 FewPlan few_plan(const moe_dims_t& d, bool fp8) {
   FewPlan L{};
   auto round16 = [](int n) { return (n + 15) / 16 * 16; };
-  L.NX = fp8 ? round16(kPiecesH * d.T) : 16;
-  L.PA = round16((fp8 ? kPiecesA : kPiecesB) * d.T);
+  L.pieces_h = fp8 ? kPiecesH : 1;
+  L.pieces_a = fp8 ? kPiecesA : kPiecesB;
+  L.NX = round16(L.pieces_h * d.T);
+  L.PA = round16(L.pieces_a * d.T);
   const int most = std::min(d.E, d.T * d.k);     // chosen experts at most
   L.max_slots = d.S + most;
   const int Fs = d.S > 0 ? d.Fs : 0;
@@ -1288,7 +1309,7 @@ FewPlan few_plan(const moe_dims_t& d, bool fp8) {
   L.nd = (d.D + 127) / 128;
   const int eb = fp8 ? 128 : 64;
   const int kb = std::min((d.F + eb - 1) / eb, d.S > 0 ? (Fs + eb - 1) / eb : 1 << 30);
-  // K parts of a down unit, each with a plane to write and to add: only while
+  // K parts of a down unit, each with rows to write and to add: only while
   // all of them have an SM and at least eight K-blocks.  (One chosen expert, 48
   // output blocks: 36 us in two parts, 39 in one, 43 in four; one token through
   // nine experts, 432 units: 114 us in one, two or four parts.)
@@ -1297,8 +1318,8 @@ FewPlan few_plan(const moe_dims_t& d, bool fp8) {
          kb >= 16 * L.parts)
     L.parts *= 2;
   // Slots of a down unit: narrow experts are taken together until a unit has 16
-  // K-blocks, as long as there are two units per SM (a unit's plane and ticket
-  // cost its epilogue 1 us).
+  // K-blocks, as long as there are two units per SM (a unit's ticket costs
+  // its epilogue 1 us).
   auto together = [&](int slots, int kbs) {
     int n = 1;
     while (L.parts == 1 && n * kbs < 16 &&
@@ -1323,7 +1344,7 @@ cudaError_t launch_few(const FewArgs& a, cudaStream_t st, const char** why) {
   r.scores = a.scores;
   r.order = a.order;
   r.idx = a.idx; r.w = a.w;
-  r.slot_of = a.slot_of; r.slot_w = a.slot_w; r.slot_expert = a.slot_expert; r.slot_mask = a.slot_mask;
+  r.pair_of = a.pair_of; r.pair_w = a.pair_w; r.slot_expert = a.slot_expert; r.slot_mask = a.slot_mask;
   r.nslots = a.nslots; r.counts = a.counts;
   r.ticket = a.ticket;
   r.status = a.status;
@@ -1341,15 +1362,15 @@ cudaError_t launch_few(const FewArgs& a, cudaStream_t st, const char** why) {
   auto map = [&](CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint32_t box) {
     return make_tensor_map(m, base, rows, cols, box, eb, es, 128);
   };
-  const int most = L.max_slots - d.S;
-  bool ok = (fp8 ? map(&f.x, a.hq, kPiecesH * d.T, d.D, L.NX) : map(&f.x, a.h, d.T, d.D, L.NX)) &&
-            map(&f.act_r, a.a_r, (uint64_t)most * L.PA, d.F, L.PA) &&
+  const uint64_t pairs = (uint64_t)d.T * d.k;
+  bool ok = (fp8 ? map(&f.x, a.hq, L.pieces_h * d.T, d.D, L.NX) : map(&f.x, a.h, d.T, d.D, L.NX)) &&
+            map(&f.act_r, a.a_r, pairs * L.pieces_a, d.F, 16) &&
             map(&f.w1_r, W1, (uint64_t)d.E * d.F, d.D, 16) &&
             map(&f.w3_r, W3, (uint64_t)d.E * d.F, d.D, 16) &&
             map(&f.w2_r, W2, (uint64_t)d.E * d.D, d.F, 128);
   f.act_s = f.act_r; f.w1_s = f.w1_r; f.w3_s = f.w3_r; f.w2_s = f.w2_r;
   if (ok && d.S > 0)
-    ok = map(&f.act_s, a.a_s, (uint64_t)d.S * L.PA, Fs, L.PA) &&
+    ok = map(&f.act_s, a.a_s, (uint64_t)d.S * d.T * L.pieces_a, Fs, 16) &&
          map(&f.w1_s, S1, (uint64_t)d.S * Fs, d.D, 16) &&
          map(&f.w3_s, S3, (uint64_t)d.S * Fs, d.D, 16) &&
          map(&f.w2_s, S2, (uint64_t)d.S * d.D, Fs, 128);
@@ -1370,12 +1391,12 @@ cudaError_t launch_few(const FewArgs& a, cudaStream_t st, const char** why) {
   f.max_slots = L.max_slots;
   f.spu_r = L.spu_r; f.spu_s = L.spu_s;
   f.ngs = (d.S + L.spu_s - 1) / L.spu_s;
-  f.slot_of = a.slot_of; f.slot_expert = a.slot_expert; f.nslots = a.nslots;
+  f.pair_of = a.pair_of; f.slot_expert = a.slot_expert; f.nslots = a.nslots;
   f.slot_mask = a.slot_mask;
-  f.slot_w = a.slot_w;
+  f.pair_w = a.pair_w;
   f.hqe = a.hqe;
   f.a_r = a.a_r; f.a_s = a.a_s; f.ae_r = a.ae_r; f.ae_s = a.ae_s;
-  f.planes = a.planes;
+  f.rows = a.rows;
   f.out = a.out;
   f.claim = a.claim;
   f.hq_blocks = hq_blocks;
@@ -1394,7 +1415,7 @@ cudaError_t launch_few(const FewArgs& a, cudaStream_t st, const char** why) {
   e = fp8 ? set_smem_once(few_ffn_kernel<true>, few_smem(), set8)
           : set_smem_once(few_ffn_kernel<false>, few_smem(), set16);
   if (e != cudaSuccess) return e;
-  const long long gu = (long long)d.S * f.nts + (long long)most * f.ntr;
+  const long long gu = (long long)d.S * f.nts + (long long)(L.max_slots - d.S) * f.ntr;
   const long long dn = (long long)L.max_slots * L.nd * L.parts;
   const int grid = (int)std::min<long long>(num_sms(), gu + dn);
   return fp8 ? launch_pdl(few_ffn_kernel<true>, dim3(grid), dim3(384), few_smem(), st, f)

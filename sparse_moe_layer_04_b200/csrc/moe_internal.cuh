@@ -59,12 +59,16 @@ cudaError_t noalloc_scratch(int32_t** out);
 struct WsLayout {
   // zero between calls, at the same place for every T
   size_t status, ticket, f_claim, counters_d, counters_s, gmask;
-  size_t partials, wr3, idx, w, counts, offsets, perm, inv, blk_base, counters, xperm, act_r, act_s,
-      y, touched, total;
-  // the few-token layer's scratch, for T <= kFewMaxT
-  size_t f_route, f_slots, f_w, f_mask, f_hq, f_hqe, f_act, f_exp, f_planes;
+  // outputs that a call leaves to be asked for
+  size_t idx, w, counts, touched;
+  // scratch
+  size_t scratch, partials, wr3, offsets, perm, inv, blk_base, counters, xperm, act_r, act_s, y;
+  // the few-token layer's scratch, in the same place
+  size_t f_route, f_slots, f_w, f_mask, f_hq, f_hqe, f_act, f_exp, f_rows;
+  size_t total;
 };
 bool ws_layout(const moe_dims_t& d, WsLayout* out);
+void few_layout(const moe_dims_t& d, WsLayout* out);
 
 // Raises a kernel's dynamic shared-memory limit to `bytes` on the current
 // device, once per device: `done` holds one bit per device ordinal (two host
@@ -234,6 +238,7 @@ cudaError_t launch_gemm_fp8(const Gemm8Args& a, cudaStream_t st, const char** wh
 // The layer for at most kFewMaxT tokens (few_layer.cu).
 constexpr int kFewMaxT = 16;
 struct FewPlan {
+  int pieces_h, pieces_a;  // pieces of a hidden value, of an activation
   int NX, PA;      // rows of the token operand: gate/up, down
   int max_slots;   // shared experts + the most experts the call can choose
   // features per gate/up tile and K-blocks per stage of one, of a chosen and
@@ -255,12 +260,12 @@ struct FewArgs {
   // workspace
   float* scores;           // [T, E]
   uint32_t* order;         // [T, E]
-  int32_t *slot_of, *slot_expert, *nslots, *counts, *touched, *ticket, *claim;
+  int32_t *pair_of, *slot_expert, *nslots, *counts, *touched, *ticket, *claim;
   uint32_t* slot_mask;
-  float* slot_w;           // [slots, kFewMaxT]
+  float* pair_w;           // [T * k]
   uint8_t *hq, *a_r, *a_s;
   int8_t *hqe, *ae_r, *ae_s;
-  float* planes;
+  float* rows;             // [parts, (S + k) * T, D]
   int* status;
 };
 cudaError_t launch_few(const FewArgs& a, cudaStream_t st, const char** why);
