@@ -1248,6 +1248,10 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
   __syncthreads();
   if (ss.exit_last) {
     __threadfence();
+    // no expert at all (no token has a key that is a number): nothing was merged
+    ptx::pdl_wait();
+    if (p.S == 0 && __ldcg(p.nslots) == 0)
+      for (int i = threadIdx.x; i < p.T * p.D; i += blockDim.x) p.out[i] = 0.f;
     for (int i = threadIdx.x; i < p.max_slots; i += blockDim.x) *slot_count(p, i) = 0;
     if (threadIdx.x == 0) {
       *p.touched = __ldcg(p.nslots);
