@@ -332,7 +332,7 @@ int moe_fp8_dequantize(const void* codes, const int8_t* exps, int G, int R, int 
  *                 max |x[idx[r], 128 b ..]| <= 448 * 2^e; 0 for a block of zeros
  *   codes[r, c] = E4M3(x[idx[r], c] * 2^-e), rounded to nearest even
  * x [src_rows, K] bf16, idx [R] int32 (rows may repeat); K a positive multiple
- * of 16; x, idx and codes 16-byte aligned, exps without an alignment rule.
+ * of 16, at most 65535 * 1024; x, idx and codes 16-byte aligned, exps without an alignment rule.
  * A NaN or an infinity gets the NaN code 0x7F, counts for no exponent and
  * raises MOE_ERR_NONFINITE; an index outside [0, src_rows) gives a row of
  * zeros and raises MOE_ERR_BOUNDS (in the status word of ws; ws may be NULL:
@@ -347,8 +347,8 @@ int moe_quantize_fp8(const void* x, int src_rows, const int32_t* idx, int R, int
  * (non-decreasing, within [0, R]; groups may be empty), W [G, N, K] codes, We
  * [G, ceil(N/128), ceil(K/128)]; y [R, N], fp32 or (y_bf16 != 0) bf16, rounded
  * once from the fp32 sum.  offsets may be NULL when G = 1: all R rows.
- * 1 <= G <= 1024, N a positive multiple of 8, K a positive multiple of 16;
- * R = 0 launches nothing.  Code, offset and output pointers are 16-byte
+ * 1 <= G <= 1024, N a positive multiple of 8, K a positive multiple of 16; R, K
+ * and G * N at most 2^31 - 256; R = 0 launches nothing.  Code, offset and output pointers are 16-byte
  * aligned, exponents have no alignment rule and may be any int8 but -128,
  * which raises MOE_ERR_BOUNDS like offsets out of order (no row is written
  * then); ws holds the status word and may be NULL: then nothing is reported.

@@ -341,6 +341,13 @@ def _ws_arg(ws: Optional[torch.Tensor], dev: int):
     return _arg(ws, torch.uint8, (n,), dev, "ws"), n
 
 
+def _int32(**sizes) -> None:
+    """Refuses a size that the C ABI's 32 bits would cut off."""
+    for name, n in sizes.items():
+        if n > 0x7fffffff:
+            raise ValueError(f"{name} = {n}: at most 2^31 - 1")
+
+
 def moe_quantize_fp8(x, codes, exps, idx=None, ws=None, stream=None) -> None:
     """x [src, K] bf16 -> codes [R, K] E4M3 (uint8 or float8_e4m3fn) and exps
     [R, ceil(K/128)] int8 of the rows x[idx] (idx [R] int32; None: of x itself)."""
@@ -348,6 +355,8 @@ def moe_quantize_fp8(x, codes, exps, idx=None, ws=None, stream=None) -> None:
         raise ValueError("x [src, K] expected")
     src, K = x.shape
     R = src if idx is None else idx.numel()
+    if src > 0x7fffffff or R > 0x7fffffff or K > 0x7fffffff:
+        _int32(src=src, R=R, K=K)
     dev = _device()
     _check(_lib.moe_quantize_fp8(
         _arg(x, torch.bfloat16, (src, K), dev, "x"), src,
@@ -362,6 +371,8 @@ def _product_sizes(x, W):
         raise ValueError("x [R, K] and W [G, N, K] (or [N, K]) expected")
     R, K = x.shape
     G, N = (1, W.shape[0]) if W.dim() == 2 else W.shape[:2]
+    if R > 0x7fffffff or N > 0x7fffffff or K > 0x7fffffff or G > 0x7fffffff:
+        _int32(R=R, N=N, K=K, G=G)
     # weights may come as [N, K] and their exponents as [NB, KB] when there is one group
     lead = () if W.dim() == 2 else (G,)
     return G, R, N, K, lead, (*lead, (N + 127) // 128, (K + 127) // 128)

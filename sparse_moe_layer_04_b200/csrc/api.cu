@@ -635,10 +635,13 @@ int check_gemm_fp8(const void* x, const int8_t* xe, const int32_t* offsets, cons
   if (R < 0) return fail(MOE_ERR_INVALID_ARG, "R = %d < 0", R);
   if (N < 8 || N % 8) return fail(MOE_ERR_INVALID_ARG, "N = %d not a positive multiple of 8", N);
   if (K < 16 || K % 16) return fail(MOE_ERR_INVALID_ARG, "K = %d not a positive multiple of 16", K);
-  if ((long long)G * N >= (1ll << 31)) return fail(MOE_ERR_UNSUPPORTED, "G*N >= 2^31");
   // tiles are numbered with 32 bits: R / 32 + G row blocks times N / 64 columns
   if (((long long)R / 32 + G + 1) * (N / 64 + 1) >= (1ll << 30))
     return fail(MOE_ERR_UNSUPPORTED, "R x N is too large for one call");
+  constexpr long long most = (1ll << 31) - 256;
+  if (R > most || K > most || (long long)G * N > most)
+    return fail(MOE_ERR_UNSUPPORTED, "R = %d, K = %d, G * N = %lld: at most 2^31 - 256 each", R, K,
+                (long long)G * N);
   if (G > 1 && !offsets) return fail(MOE_ERR_INVALID_ARG, "offsets is NULL with G > 1");
   if (R == 0) return MOE_OK;
   MOE_CHECK_PTR(x);
@@ -1029,6 +1032,8 @@ int moe_quantize_fp8(const void* x, int src_rows, const int32_t* idx, int R, int
   g_launches = 0;
   if (src_rows < 0 || R < 0) return fail(MOE_ERR_INVALID_ARG, "src_rows and R must be >= 0");
   if (K < 16 || K % 16) return fail(MOE_ERR_INVALID_ARG, "K = %d is not a positive multiple of 16", K);
+  // (two chunks of 512 columns a block, along a grid axis of 65535)
+  if (K > 65535 * 1024) return fail(MOE_ERR_UNSUPPORTED, "K = %d: at most %d", K, 65535 * 1024);
   if (!idx && R > src_rows)
     return fail(MOE_ERR_INVALID_ARG, "R = %d rows from %d without an index", R, src_rows);
   if (R == 0) return MOE_OK;

@@ -194,7 +194,7 @@ struct Walk {
     const int nb = gm.prefix[g + 1] - gm.prefix[g];
     int local = t - gm.prefix[g] * p.nt, b = 0, per = rows;
     if (nb > 1) {                              // equal blocks, in steps of 16 rows
-      per = ((rows + nb - 1) / nb + 15) / 16 * 16;
+      per = ((rows - 1) / nb + 16) / 16 * 16;
       b = local % nb;
       local /= nb;
     }
@@ -743,9 +743,10 @@ cudaError_t launch_any(GemmParams8& p, cudaStream_t st, const char** why, const 
 // 724 against 766, and 765 with one weight tile).
 template <bool GATED>
 cudaError_t launch_rows(GemmParams8& p, cudaStream_t st, const char** why, const Gemm8Args& a) {
-  const int groups = std::min(a.G, a.R), avg = (a.R + groups - 1) / groups;
+  // (sizes end 256 below 2^31, so that a tile's width can be added to them)
+  const int groups = std::min(a.G, a.R), avg = (a.R - 1) / groups + 1;
   const int top = a.G > 1 ? avg + (int)(2.f * sqrtf((float)avg)) : avg;
-  const int nb = (top + 239) / 240, need = (top + nb - 1) / nb;
+  const int nb = (top + 239) / 240, need = (top - 1) / nb + 1;
   constexpr int widths[] = {32, 64, 96, 144, 160, 240};
   int w = 0;
   while (widths[w] < need) ++w;

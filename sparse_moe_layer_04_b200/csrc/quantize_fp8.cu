@@ -70,10 +70,10 @@ __global__ void __launch_bounds__(kThreads) quantize_fp8_kernel(
   ptx::pdl_launch_dependents();
   ptx::pdl_wait();
   const int lane = threadIdx.x & 31;
-  const int r = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-  if (r >= R) return;
+  const unsigned r = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);   // (R may end at 2^31)
+  if (r >= (unsigned)R) return;
   const int col0 = blockIdx.y * (512 * U) + lane * 16;
-  const int s = idx ? idx[r] : r;
+  const int s = idx ? idx[r] : (int)r;
   int bad = 0;
   const bool ok = s >= 0 && s < src_rows;
   if (!ok) bad = kStBounds;
@@ -142,7 +142,7 @@ cudaError_t launch_quantize_fp8(const uint16_t* x, int src_rows, const int32_t* 
                                 uint8_t* codes, int8_t* exps, int* status, cudaStream_t st) {
   const int chunks = (K + 511) / 512;
   const int warps = kThreads / 32;
-  const unsigned gx = (unsigned)((R + warps - 1) / warps);
+  const unsigned gx = ((unsigned)R + warps - 1) / warps;
   // rows start on 32 bytes when the matrix does (K is a multiple of 16)
   const bool wide = (reinterpret_cast<uintptr_t>(x) & 31u) == 0;
   const int KB = (K + 127) / 128;
