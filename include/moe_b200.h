@@ -324,7 +324,8 @@ int moe_fp8_dequantize(const void* codes, const int8_t* exps, int G, int R, int 
  * so a product is one chain of fp32 accumulation over all of K.
  * An expert FFN on grouped rows is moe_quantize_fp8 (with perm as the index),
  * moe_gated_gemm_fp8, moe_quantize_fp8 on its output, moe_grouped_gemm_fp8,
- * moe_combine.
+ * moe_combine.  Shared experts are S groups more of the T rows each (an index that
+ * names every token S times), whose results go behind the T*k routed rows.
  *
  * Quantisation of rows: codes [R, K] E4M3 and exps [R, ceil(K/128)] int8 of the
  * bf16 rows x[idx[r]] (x[r] when idx is NULL, which needs R <= src_rows):
