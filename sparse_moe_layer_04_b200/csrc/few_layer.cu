@@ -50,6 +50,7 @@
 #include <cuda_bf16.h>
 
 #include "ffn_common.cuh"
+#include "gate.cuh"
 #include "route_order.cuh"
 #include "sm100_scaled.cuh"
 
@@ -1052,10 +1053,10 @@ __global__ void __launch_bounds__(FP8 ? 384 : 256, 1) few_ffn_kernel(const __gri
         float least = 0.f;               // of the gates that count
         gates([&](int tt, float g, float u) {
           if ((mask >> tt) & 1u) least = fminf(least, g);
-          return ffn::silu_times_near<true>(g, u);
+          return silu_times_near<true>(g, u);
         });
-        if (__any_sync(kAll, least < ffn::kGateFar))
-          gates([](int, float g, float u) { return ffn::silu_times_wide<true>(g, u); });
+        if (__any_sync(kAll, least < kGateFar))
+          gates([](int, float g, float u) { return silu_times_wide<true>(g, u); });
 #pragma unroll
         for (int t = 0; t < 16; t += 2) {
           const float a = f < F ? act[t / 2] : 0.f;

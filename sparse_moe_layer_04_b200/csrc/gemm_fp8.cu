@@ -48,6 +48,7 @@
 #include <cuda_bf16.h>
 
 #include "ffn_common.cuh"
+#include "gate.cuh"
 #include "sm100_scaled.cuh"
 
 namespace moe {
@@ -256,20 +257,20 @@ __device__ __forceinline__ void store16(const GemmParams8& p, const Tile8& ti, i
       const float got = __uint_as_float(__shfl_xor_sync(kAll, up ? v[j] : v[j + 1], 16));
       const float own = __uint_as_float(up ? v[j + 1] : v[j]);
       const float g = up ? got : own;
-      const float a = ffn::silu_times_near<false>(g, up ? own : got);
+      const float a = silu_times_near<false>(g, up ? own : got);
       least = fminf(least, g);
       if (j < mine) *y = __float2bfloat16_rn(a);
       y += step;
     }
     // (looked at once for all rows; a branch for each gate takes 64 experts, 8192
     // rows, N = 2048, K = 6144 from 295 us to 306; none at all 293)
-    if (__any_sync(kAll, least < ffn::kGateFar)) {
+    if (__any_sync(kAll, least < kGateFar)) {
       y -= 8 * step;
 #pragma unroll
       for (int j = 0; j < 16; j += 2) {
         const float got = __uint_as_float(__shfl_xor_sync(kAll, up ? v[j] : v[j + 1], 16));
         const float own = __uint_as_float(up ? v[j + 1] : v[j]);
-        const float a = ffn::silu_times_wide<false>(up ? got : own, up ? own : got);
+        const float a = silu_times_wide<false>(up ? got : own, up ? own : got);
         if (j < mine) *y = __float2bfloat16_rn(a);
         y += step;
       }
@@ -651,8 +652,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
             if (GATED) { u.x += w[r].x; u.y += w[r].y; u.z += w[r].z; u.w += w[r].w; }
           }
         if (GATED) {
-          s.x = ffn::silu_times_wide<false>(s.x, u.x); s.y = ffn::silu_times_wide<false>(s.y, u.y);
-          s.z = ffn::silu_times_wide<false>(s.z, u.z); s.w = ffn::silu_times_wide<false>(s.w, u.w);
+          s.x = silu_times_wide<false>(s.x, u.x); s.y = silu_times_wide<false>(s.y, u.y);
+          s.z = silu_times_wide<false>(s.z, u.z); s.w = silu_times_wide<false>(s.w, u.w);
         }
         // (N is a multiple of 8: four columns are all there or not at all)
         const size_t out = (size_t)(ti.row0 + c) * p.N + ti.n0 + f;
