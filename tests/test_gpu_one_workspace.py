@@ -2,6 +2,8 @@
 tokens, of either kind: moe_forward and moe_forward_few (and their forms with
 8-bit weights), whose scratch lies at places that move with T, while what a call
 must find zero does not."""
+import re
+
 import pytest
 import torch
 
@@ -71,3 +73,30 @@ def test_any_T_of_both_kinds(moe, D, E, F, k, S, Fs, fp8):
         assert torch.equal(moe.moe_ws_expert_counts(one, d), counts)
         assert int(moe.moe_ws_touched_experts(one, d)) == int((counts > 0).sum())
     assert moe.moe_get_device_status(one) == 0
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("T,D,E,F,k,S,Fs", [
+    (1, 16, 1, 16, 1, 0, 0),
+    (1, 6144, 4, 2048, 1, 0, 0),        # the second product's K in parts
+    (16, 128, 1, 2048, 1, 0, 0),        # the same for sixteen tokens
+    (10, 5040, 98, 128, 3, 0, 0),       # several slots to a unit
+    (16, 512, 1024, 64, 32, 2, 128),    # the most pairs
+    (16, 64, 8, 1040, 8, 16, 992),      # wide experts, the most shared ones
+    (13, 272, 9, 208, 4, 1, 336),
+])
+def test_nothing_is_written_behind_what_a_call_asks_for(moe, T, D, E, F, k, S, Fs, fp8):
+    """The few-token layer in exactly the bytes its refusal names, with what
+    follows them filled beforehand."""
+    L = Layer(moe, T, D, E, F, k, S, Fs, fp8, seed=41)
+    want = L.run()
+    with pytest.raises(moe.MoeError, match="needs") as refused:
+        L.run(ws=torch.zeros(256, dtype=torch.uint8, device="cuda"))
+    need = int(re.search(r"needs (\d+)", str(refused.value)).group(1))
+    assert need <= moe.moe_workspace_size(L.d)
+    room = torch.full((need + 65536,), 0xa5, dtype=torch.uint8, device="cuda")
+    room[:need] = 0
+    for _ in range(2):
+        assert all(torch.equal(a, b) for a, b in zip(L.run(ws=room[:need]), want))
+    assert moe.moe_get_device_status(room[:need]) == 0
+    assert bool((room[need:] == 0xa5).all())
